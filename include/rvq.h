@@ -83,7 +83,7 @@ extern "C" {
 #endif
 
 #define RVQ_VERSION_MAJOR 0
-#define RVQ_VERSION_MINOR 4
+#define RVQ_VERSION_MINOR 5
 #define RVQ_VERSION_PATCH 0
 
 /* Distance of the argmin (rvq_dims.metric). */
@@ -329,6 +329,180 @@ RVQ_API int64_t rvq_set_stream_max_frames(int64_t max_frames);
  * fails, RVQ_ERR_CUDA.  RVQ_ERR_INVALID_ARG (plan untouched) for bad dims,
  * n_q outside 1..Q, n_frames < 0 or a null plan. */
 RVQ_API rvq_status rvq_stream_plan(rvq_dims dims, int32_t n_q, int64_t n_frames, int64_t *plan);
+
+/* ---------------------------------------------------------------------------
+ * Operators of a code predictor: the model that gives, for each frame, one
+ * row of K logits per stage (often with a mask code beside the K codes,
+ * omnivoice.cpp ARCHITECTURE.md, "GGUF layout") over normalised features, and
+ * whose chosen codes go to rvq_decode.
+ *
+ * Tensors are float32, bfloat16 or float16 (RVQ_DTYPE_*); arithmetic, sums
+ * and statistics are float32, and a 16-bit result is rounded once.  Rows are
+ * contiguous and lie `*_stride` elements apart (at least the row's width), so
+ * slices of wider tensors are taken as they are; pointers need the alignment
+ * of their element only (16-byte aligned rows are the fastest).  As above,
+ * every pointer is caller-owned device memory, each call only enqueues work
+ * on `stream`, and arguments are checked on the host first:
+ * RVQ_ERR_INVALID_ARG for null or misaligned pointers, negative counts,
+ * strides below the width, unknown dtypes or modes and a workspace that is
+ * too small; RVQ_ERR_UNSUPPORTED beyond the limits that each call names.
+ * Results do not depend on timing: equal inputs give equal bits.
+ * --------------------------------------------------------------------------- */
+#define RVQ_DTYPE_F32 0
+#define RVQ_DTYPE_BF16 1
+#define RVQ_DTYPE_F16 2
+
+/* Layer norm of `rows` rows of `width` elements (1 <= width <= 16384; zero
+ * rows are valid).  dtype: of x, y, dy, dx; param_dtype: of weight, bias and
+ * their gradients (float32, or the same as dtype); eps >= 0 is added to the
+ * variance. */
+typedef struct rvq_norm_dims {
+  int64_t rows;
+  int32_t width;
+  int32_t dtype;
+  int32_t param_dtype;
+  float eps;
+} rvq_norm_dims;
+
+/* y = (x - mean) * rstd * weight + bias per row, with mean and
+ * rstd = 1 / sqrt(var + eps) of the row (var: the mean squared deviation).
+ * weight and bias are nullable (one and zero).  mean and rstd ([rows],
+ * nullable) are kept for the backward pass.  y may be x. */
+RVQ_API rvq_status rvq_layer_norm(rvq_norm_dims dims, const void *x, int64_t x_stride, const void *weight,
+                                  const void *bias, void *y, int64_t y_stride, float *mean, float *rstd,
+                                  rvq_stream_t stream);
+
+/* Workspace bytes of rvq_layer_norm_backward (0 for unsupported arguments). */
+RVQ_API size_t rvq_layer_norm_workspace_bytes(int64_t rows, int32_t width);
+
+/* Gradients of rvq_layer_norm: with h = (x - mean) * rstd and g = dy * weight,
+ *   dx = rstd * (g - mean(g) - h * mean(g * h)),
+ *   dweight = sum over rows of dy * h,  dbias = sum over rows of dy.
+ * dx, dweight and dbias are each nullable (not computed); dx may be dy or x.
+ * With zero rows dweight and dbias are set to zero.  The workspace (16-byte
+ * aligned) is needed for dweight and dbias; its contents mean nothing before
+ * and after the call. */
+RVQ_API rvq_status rvq_layer_norm_backward(rvq_norm_dims dims, const void *dy, int64_t dy_stride, const void *x,
+                                           int64_t x_stride, const void *weight, const float *mean, const float *rstd,
+                                           void *dx, int64_t dx_stride, void *dweight, void *dbias, void *workspace,
+                                           size_t workspace_bytes, rvq_stream_t stream);
+
+/* Distillation of `rows` rows of `vocab` student logits from each row's `top`
+ * teacher entries (1 <= vocab <= 2^20, 1 <= top <= 256).  dtype: of logits and
+ * dlogits; top_dtype: of the teacher's logits; temperature T > 0 divides both
+ * sides' logits. */
+typedef struct rvq_distill_dims {
+  int64_t rows;
+  int32_t vocab;
+  int32_t top;
+  int32_t dtype;
+  int32_t top_dtype;
+  float temperature;
+} rvq_distill_dims;
+
+/* Per row, with p = softmax(logits / T) and the teacher's entries (t_j, i_j)
+ * (top_logits, top_codes: [rows][top], contiguous):
+ *   teacher_lse NULL:  q = softmax(t / T) over the entries,
+ *     loss = w * sum_j q_j (log q_j - log p[i_j]);
+ *   teacher_lse given ([rows]: log sum exp of ALL the teacher's logits / T):
+ *     q_j = exp(t_j / T - teacher_lse), and the codes without an entry are one
+ *     more outcome with q_r = 1 - sum_j q_j and p_r = their sum of p:
+ *     loss = w * (sum_j q_j (log q_j - log p[i_j]) + q_r (log q_r - log p_r)).
+ *     q_r below 2^-20 (the rounding of the sum) counts as zero.
+ * weights ([rows], nullable: ones) gives w.  A row with w = 0 has loss 0 and
+ * gradient 0 whatever its logits hold.
+ * An entry with code -1 is empty.  Other codes outside [0, vocab), and a code
+ * that stands a second time in its row (the first counts), are treated as
+ * empty and counted into *bad_codes if it is not NULL (device int64, added to
+ * atomically, as in rvq_decode).  A row without entries has loss 0 and
+ * gradient 0, and so has, without teacher_lse, one whose entries are all -inf.
+ * Terms with q = 0 are zero even where p is zero; q > 0 where p = 0 gives an
+ * infinite loss and a finite gradient.  A NaN or +inf in a row with w != 0
+ * makes that row's results NaN, and no other's.
+ * Writes loss [rows]; if not NULL, lse [rows][2] for rvq_distill_backward (the
+ * largest logit m and the sum of exp((logit - m) / T) over all codes, or, with
+ * teacher_lse, over the codes without an entry; zeros where w = 0); if not
+ * NULL, dlogits = d loss / d logits in the same pass.  dlogits may be logits itself (same stride). */
+RVQ_API rvq_status rvq_distill(rvq_distill_dims dims, const void *logits, int64_t logits_stride,
+                               const void *top_logits, const int32_t *top_codes, const float *teacher_lse,
+                               const float *weights, float *loss, float *lse, void *dlogits, int64_t dlogits_stride,
+                               int64_t *bad_codes, rvq_stream_t stream);
+
+/* dlogits = grad_loss[row] * d loss[row] / d logits, from the same arguments
+ * and the lse that rvq_distill wrote.  grad_loss ([rows], nullable: ones) is
+ * the gradient of the caller's total with respect to loss. */
+RVQ_API rvq_status rvq_distill_backward(rvq_distill_dims dims, const float *grad_loss, const void *logits,
+                                        int64_t logits_stride, const void *top_logits, const int32_t *top_codes,
+                                        const float *teacher_lse, const float *weights, const float *lse,
+                                        void *dlogits, int64_t dlogits_stride, rvq_stream_t stream);
+
+/* What rvq_beam_select adds to a beam's score (rvq_beam_dims.mode). */
+#define RVQ_BEAM_LOGITS 0 /* log softmax of the beam's row */
+#define RVQ_BEAM_RAW 1    /* the row's values as they are (log probabilities, or minus a distance) */
+
+/* A beam step over `groups` independent searches of `beams` beams each
+ * (1 <= beams <= 64), `vocab` codes (1 <= vocab <= 2^24), keeping `select`
+ * candidates (1 <= select <= 64).  dtype: of the logits. */
+typedef struct rvq_beam_dims {
+  int64_t groups;
+  int32_t beams;
+  int32_t vocab;
+  int32_t select;
+  int32_t mode;
+  int32_t dtype;
+} rvq_beam_dims;
+
+/* Workspace bytes of rvq_beam_select (0 for unsupported dims). */
+RVQ_API size_t rvq_beam_workspace_bytes(rvq_beam_dims dims);
+
+/* Per group, the `select` best candidates (beam b, code v) by
+ *   total = scores[b] + logits[b][v] - log sum exp(logits[b])   (RVQ_BEAM_LOGITS)
+ *   total = scores[b] + logits[b][v]                            (RVQ_BEAM_RAW)
+ * in float32, best first; equal totals: the lower beam first, then (of one
+ * beam) the larger logit, then the lower code.
+ *   logits [groups * beams] rows of vocab, logits_stride apart;
+ *   scores [groups][beams]; a beam whose score is -inf or NaN has no
+ *     candidates and its row is not read (the first step of a search: one
+ *     live beam);
+ *   finished [groups][beams] bytes (nullable: none): a finished beam offers
+ *     end_code alone, at its score unchanged, and its row is not read.
+ *     end_code is in [0, vocab), or -1 (no end code) where finished is NULL.
+ * Candidates whose total is -inf or NaN are never chosen.  Writes
+ * out_scores, parents (the beam) and codes, each [groups][select], and, if
+ * not NULL, out_finished (bytes: the parent was finished, or the code is
+ * end_code).  A slot for which no candidate is left gets -inf, -1, -1 and
+ * finished 1. */
+RVQ_API rvq_status rvq_beam_select(rvq_beam_dims dims, const void *logits, int64_t logits_stride, const float *scores,
+                                   const uint8_t *finished, int32_t end_code, float *out_scores, int32_t *parents,
+                                   int32_t *codes, uint8_t *out_finished, void *workspace, size_t workspace_bytes,
+                                   rvq_stream_t stream);
+
+/* One state tensor that follows the beams: `layers` x groups x beams rows of
+ * row_bytes contiguous bytes (layers 1 where the tensor has no such axis);
+ * strides in bytes.  dst holds `select` rows per group.  dst == src (and equal
+ * strides) reorders in place and needs select == beams; other overlaps are
+ * not allowed. */
+typedef struct rvq_beam_state {
+  const void *src;
+  void *dst;
+  int64_t layers;
+  int64_t row_bytes;
+  int64_t src_layer_stride;
+  int64_t src_group_stride;
+  int64_t src_beam_stride;
+  int64_t dst_layer_stride;
+  int64_t dst_group_stride;
+  int64_t dst_beam_stride;
+} rvq_beam_state;
+
+#define RVQ_BEAM_MAX_STATES 32
+
+/* dst[layer][group][j] = src[layer][group][parents[group][j]] for every state
+ * (host array of n_states <= RVQ_BEAM_MAX_STATES); a parent outside
+ * [0, beams) gives a row of zeros.  Uses dims.groups, beams and select.  In
+ * place, rows that stay where they are are not touched. */
+RVQ_API rvq_status rvq_beam_reorder(rvq_beam_dims dims, const int32_t *parents, const rvq_beam_state *states,
+                                    int32_t n_states, rvq_stream_t stream);
 
 /* Static strings. */
 RVQ_API const char *rvq_status_string(rvq_status status);

@@ -212,6 +212,6 @@ RVQ_API rvq_status rvq_read_error_count(const int64_t *bad_codes, int64_t *n_bad
   return RVQ_OK;
 }
 
-RVQ_API const char *rvq_version(void) { return "rvq-gb300 0.4.0 (sm_103a)"; }
+RVQ_API const char *rvq_version(void) { return "rvq-gb300 0.5.0 (sm_103a)"; }
 
 }  // extern "C"

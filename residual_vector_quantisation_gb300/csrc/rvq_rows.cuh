@@ -1,0 +1,141 @@
+// Rows of 32- or 16-bit floats: element types, 16-byte vectors of them, and
+// the reductions that the row operators (rvq_norm.cu, rvq_distill.cu,
+// rvq_beam.cu) share.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <math_constants.h>
+#include <stdint.h>
+
+#include "rvq.h"
+
+namespace rvq {
+
+// Element sizes of RVQ_DTYPE_* (0: unknown).
+inline int dtype_bytes(int32_t dtype) {
+  return dtype == RVQ_DTYPE_F32 ? 4 : dtype == RVQ_DTYPE_BF16 || dtype == RVQ_DTYPE_F16 ? 2 : 0;
+}
+inline bool aligned_to(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+// Whether rows of `bytes`-sized elements at p, `stride` elements apart, all start on a 16-byte boundary.
+inline bool rows_aligned16(const void *p, int64_t stride, int64_t rows, int bytes) {
+  return aligned_to(p, 16) && (rows <= 1 || (stride * bytes) % 16 == 0);
+}
+
+__device__ __forceinline__ float to_float(float v) { return v; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_float(__half v) { return __half2float(v); }
+template <class T>
+__device__ __forceinline__ T from_float(float v);
+template <>
+__device__ __forceinline__ float from_float<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ __forceinline__ __half from_float<__half>(float v) { return __float2half_rn(v); }
+
+// A 16-byte vector (N = 16 / sizeof(T)) or one element (N = 1) as floats.
+template <class T>
+__device__ __forceinline__ void unpack16(const uint4 &v, float (&f)[16 / sizeof(T)]) {
+  if constexpr (sizeof(T) == 4) {
+    f[0] = __uint_as_float(v.x), f[1] = __uint_as_float(v.y), f[2] = __uint_as_float(v.z), f[3] = __uint_as_float(v.w);
+  } else {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      } else {
+        const float2 p = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+        f[2 * i] = p.x, f[2 * i + 1] = p.y;
+      }
+    }
+  }
+}
+
+template <class T>
+__device__ __forceinline__ uint4 pack16(const float (&f)[16 / sizeof(T)]) {
+  uint4 v;
+  if constexpr (sizeof(T) == 4) {
+    v = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+  } else {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+        const __nv_bfloat162 p = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t *>(&p);
+      } else {
+        const __half2 p = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t *>(&p);
+      }
+    }
+    v = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  return v;
+}
+
+// A row that may start anywhere: its elements seen as 16-byte vectors from the
+// boundary at or below its start.  Element e of the row is place phase + e;
+// vector v holds the places [v * N, v * N + N).
+template <class T>
+struct RowVectors {
+  static constexpr int N = 16 / (int)sizeof(T);
+  uintptr_t at;  // address of place 0 (never dereferenced outside the row)
+  int phase, width;
+  __device__ __forceinline__ RowVectors(const T *row, int width_) : width(width_) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(row);
+    phase = (int)(a & 15) / (int)sizeof(T);
+    at = a - (a & 15);
+  }
+  __device__ __forceinline__ int count() const { return (phase + width + N - 1) / N; }
+  __device__ __forceinline__ bool inside(int v) const { return v * N >= phase && (v + 1) * N <= phase + width; }
+  // Vector v; places outside the row read as `fill`.
+  __device__ __forceinline__ uint4 load(int v, T fill) const {
+    if (inside(v)) return *reinterpret_cast<const uint4 *>(at + (uintptr_t)v * 16);
+    union {
+      uint4 u;
+      T t[N];
+    } r;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int p = v * N + i;
+      r.t[i] = p >= phase && p < phase + width ? reinterpret_cast<const T *>(at)[p] : fill;
+    }
+    return r.u;
+  }
+  __device__ __forceinline__ void store(int v, const float (&f)[N]) const {
+    if (inside(v)) {
+      *reinterpret_cast<uint4 *>(at + (uintptr_t)v * 16) = pack16<T>(f);
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int p = v * N + i;
+      if (p >= phase && p < phase + width) reinterpret_cast<T *>(at)[p] = from_float<T>(f[i]);
+    }
+  }
+};
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+// 2^x to about 2 units in the last place (subnormal results become zero).
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+
+}  // namespace rvq
