@@ -17,7 +17,7 @@ namespace rvq {
 namespace {
 
 constexpr int kDistillMaxVocab = 1 << 20;
-constexpr int kDistillMaxTop = 256;
+constexpr int kDistillMaxTop = 256;  // a power of two
 constexpr float kTailFloor = 9.5367431640625e-07f;  // 2^-20: a smaller 1 - sum q is that sum's rounding
 
 struct DistillArgs {
@@ -59,9 +59,47 @@ __device__ __forceinline__ Sum warp_join(Sum v, float c) {
   return v;
 }
 
+// A row cut at 16-byte boundaries: `head` elements before the first, `full`
+// vectors, `tail` elements after the last.  The head and tail elements (under
+// N each) belong to 2 N threads, one each; so no vector needs a check.
+// Element e has place e - head + 8: a vector's places start at a multiple of N.
+template <class T>
+struct Row {
+  static constexpr int N = 16 / (int)sizeof(T);
+  const T *z;
+  T *d;  // null: no gradient wanted
+  int width, head, full, tail;
+  bool same;  // z and d start equally far from a boundary
+  __device__ __forceinline__ Row(const DistillArgs &a, int64_t row)
+      : z(static_cast<const T *>(a.logits) + row * a.logits_stride),
+        d(a.dlogits ? static_cast<T *>(a.dlogits) + row * a.dlogits_stride : nullptr),
+        width(a.dm.vocab) {
+    const int past = (int)(reinterpret_cast<uintptr_t>(z) & 15) / (int)sizeof(T);
+    head = min(width, past ? N - past : 0);
+    full = (width - head) / N;
+    tail = width - head - full * N;
+    same = ((reinterpret_cast<uintptr_t>(z) ^ reinterpret_cast<uintptr_t>(d)) & 15) == 0;
+  }
+  __device__ __forceinline__ uint4 vector(int v) const { return *reinterpret_cast<const uint4 *>(z + head + v * N); }
+  __device__ __forceinline__ int place(int e) const { return e - head + 8; }
+  // the element that thread t holds beside its vectors (-1: none)
+  __device__ __forceinline__ int edge(int t) const {
+    return t < head ? t : t >= N && t < N + tail ? head + full * N + t - N : -1;
+  }
+  __device__ __forceinline__ void put(int v, const float (&f)[N]) const {
+    T *at = d + head + v * N;
+    if (same) {
+      *reinterpret_cast<uint4 *>(at) = pack16<T>(f);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) at[i] = from_float<T>(f[i]);
+    }
+  }
+};
+
 // What a row's shared memory holds: the bits of the codes with an entry, by
-// place (RowVectors), and the entries: code (-1: empty), the teacher's logit t
-// and the student's z.
+// place, and the entries: code (-1: empty), the teacher's logit t and the
+// student's z.
 struct TopList {
   uint32_t *bits;
   int32_t *code;
@@ -69,30 +107,36 @@ struct TopList {
 };
 __host__ __device__ inline int distill_bit_words(int vocab) { return (vocab + 8 + 31) / 32; }
 inline size_t distill_smem(int vocab, int top) { return (size_t)(distill_bit_words(vocab) + 3 * top) * 4; }
+__device__ __forceinline__ TopList top_list(uint32_t *at, int words, int top) {
+  return {at, reinterpret_cast<int32_t *>(at + words), reinterpret_cast<float *>(at + words + top),
+          reinterpret_cast<float *>(at + words + 2 * top)};
+}
 
 // One warp reads a row's entries (bits cleared before).  An entry counts where
-// its code is in range and stands for the first time; the order within a warp
-// and from warp to warp of 32 is the list's, so the choice does not depend on timing.
+// its code is in range and stands for the first time, by the list's order.
 template <class T>
-__device__ void read_top(const DistillArgs &a, int64_t row, const T *z, int phase, const TopList &l) {
+__device__ __forceinline__ void read_top(const DistillArgs &a, int64_t row, const Row<T> &r, const TopList &l) {
   const int lane = threadIdx.x & 31, top = a.dm.top;
   int bad = 0;
   for (int j0 = 0; j0 < top; j0 += 32) {
     const int j = j0 + lane;
     const int code = j < top ? a.top_codes[row * top + j] : -1;
-    bool ok = code >= 0 && code < a.dm.vocab;
-    const unsigned same = __match_any_sync(0xffffffffu, ok ? code : -1 - lane);
-    ok = ok && __ffs(same) - 1 == lane;
+    bool ok = code >= 0 && code < a.dm.vocab, seen = false;
     if (ok) {
-      const int p = code + phase;
+      const int p = r.place(code);
       const uint32_t bit = 1u << (p & 31);
-      ok = !(atomicOr(&l.bits[p >> 5], bit) & bit);
+      seen = atomicOr(&l.bits[p >> 5], bit) & bit;
+    }
+    const unsigned all_seen = __ballot_sync(0xffffffffu, seen);
+    if (all_seen) {  // a code twice: the first of its lanes has it, unless an earlier 32 had
+      const unsigned same = __match_any_sync(0xffffffffu, ok ? code : -1 - lane);
+      ok = ok && __ffs(same) - 1 == lane && (same & ~all_seen);
     }
     bad += j < top && code != -1 && !ok;
     if (j < top) {
       l.code[j] = ok ? code : -1;
       l.t[j] = ok ? load_any(a.top_logits, a.dm.top_dtype, row * top + j) : -CUDART_INF_F;
-      l.z[j] = ok ? to_float(z[code]) : -CUDART_INF_F;
+      l.z[j] = ok ? to_float(r.z[code]) : -CUDART_INF_F;
     }
     __syncwarp();
   }
@@ -102,199 +146,477 @@ __device__ void read_top(const DistillArgs &a, int64_t row, const T *z, int phas
   }
 }
 
-// What the gradient needs of a row: off the list e^((z - rest_m) / T) *
-// rest_scale (rest_m = +inf: zero whatever z is), on it (p - q) * scale with
-// p = e^((z - all.m) / T) / all.s and log q = (t - t_m) / T - t_log.
-struct RowPlan {
-  float rest_m, rest_scale, scale, loss, t_m, t_log;
-  Sum all;
-};
-// Logarithms of the entries are natural ones: a logit of the type's lowest
+// What the list alone gives, relative to the list's largest logits (t_m, z_m):
+//   u_j = q_j (with the tail) or e^((t_j - t_m) / T) (renormalised: q_j = u_j / u),
+//   u = sum u_j,  on = sum e^((z_j - z_m) / T),
+//   ul = sum u_j ((t_j - t_m) / T - t_log - (z_j - z_m) / T) / kMaxTop (which
+//   keeps the sum in range while any u_j of it is).
+// Logarithms of single entries are natural ones: a logit of the type's lowest
 // value, times log2(e), would be -inf.
-__device__ __forceinline__ float log_q(const RowPlan &r, float t, float inv_t) {
-  return fmaf(t - r.t_m, inv_t, -r.t_log);
+struct TopSums {
+  bool any;
+  float t_m, t_log, z_m, on, u, ul;
+};
+__device__ __forceinline__ float entry_u(const TopSums &r, float t, float inv_t) {
+  return exp2_fast(fmaf(t - r.t_m, inv_t, -r.t_log) * kLog2e);
 }
 
-// One warp: the row's plan from `sum`, the sum over every code (renormalised)
-// or over the codes without an entry (with the tail).
-__device__ RowPlan plan_row(const DistillArgs &a, int64_t row, float w, Sum sum, float c, const TopList &l) {
+__device__ __forceinline__ TopSums top_sums(const DistillArgs &a, int64_t row, float inv_t, const TopList &l) {
   const int lane = threadIdx.x & 31, top = a.dm.top;
-  const float inv_t = 1.f / a.dm.temperature;
   const bool tail = a.teacher_lse != nullptr;
+  TopSums r;
   bool any = false;
-  Sum t = no_sum(), on = no_sum();
-  for (int j = lane; j < top; j += 32) {
-    if (l.code[j] < 0) continue;
-    any = true;
-    if (tail)
-      on = join(on, {l.z[j], 1.f}, c);
-    else
-      t = join(t, {l.t[j], 1.f}, c);
+  float tm = -CUDART_INF_F, zm = -CUDART_INF_F;
+  for (int j = lane; j < top; j += 32) {  // empty entries are -inf
+    any |= l.code[j] >= 0;
+    tm = fmaxf(tm, l.t[j]);
+    zm = fmaxf(zm, l.z[j]);
   }
-  any = __any_sync(0xffffffffu, any);
-  RowPlan r;
-  r.scale = w / a.dm.temperature;
+  r.any = __any_sync(0xffffffffu, any);
+  zm = warp_max_order(zm);
+  r.z_m = zm == -CUDART_INF_F ? 0.f : zm;
   if (tail) {
     r.t_m = 0.f, r.t_log = a.teacher_lse[row];
-    r.all = join(sum, warp_join(on, c), c);
   } else {
-    t = warp_join(t, c);
-    r.t_m = t.m, r.t_log = logf(t.s);
-    r.all = sum;
+    tm = warp_max_order(tm);
+    r.t_m = tm == -CUDART_INF_F ? 0.f : tm, r.t_log = 0.f;
   }
-  if (!any || (!tail && t.s == 0.f)) {
-    r.loss = r.rest_scale = r.scale = 0.f;
-    r.rest_m = CUDART_INF_F;
-    return r;
-  }
-  const bool empty = r.all.m == -CUDART_INF_F && r.all.s == 0.f;  // no code has a share
-  const float log_all = logf(r.all.s);
-  float q_sum = 0.f, loss = 0.f;
+  r.on = r.u = r.ul = 0.f;
   for (int j = lane; j < top; j += 32) {
     if (l.code[j] < 0) continue;
-    const float lq = log_q(r, l.t[j], inv_t), q = exp2_fast(lq * kLog2e);
-    const float lp = empty ? -CUDART_INF_F : (l.z[j] - r.all.m) * inv_t - log_all;
-    q_sum += q;
-    if (q != 0.f) loss = fmaf(q, lq - lp, loss);  // a NaN goes on
+    const float zr = (l.z[j] - r.z_m) * inv_t, lt = fmaf(l.t[j] - r.t_m, inv_t, -r.t_log);
+    const float u = exp2_fast(lt * kLog2e);
+    r.on += exp2_fast(zr * kLog2e);
+    r.u += u;
+    if (u != 0.f) r.ul = fmaf(u * (1.f / kDistillMaxTop), lt - zr, r.ul);  // a NaN goes on
   }
-  q_sum = warp_sum(q_sum);
-  loss = warp_sum(loss);
-  r.rest_m = sum.m;
-  r.rest_scale = r.scale / sum.s;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    r.on += __shfl_xor_sync(0xffffffffu, r.on, o);
+    r.u += __shfl_xor_sync(0xffffffffu, r.u, o);
+    r.ul += __shfl_xor_sync(0xffffffffu, r.ul, o);
+  }
+  return r;
+}
+
+// What the gradient needs of a row: off the list e^((z - m) / T) * rest_scale
+// (`zero`: nothing), on it (e^((z - all_m) / T) * all_r - u_j * u_r) * scale.
+struct RowPlan {
+  float m, rest_scale, scale, loss, all_m, all_r, u_r;
+  bool zero;
+};
+__device__ __forceinline__ float log_fast(float x) { return __log2f(x) * 0.6931471805599453f; }
+
+// The plan from `sum`, the sum over every code (renormalised) or over the
+// codes without an entry (with the tail).
+__device__ __forceinline__ RowPlan plan_row(bool tail, float w, Sum sum, const TopSums &t, float c, float inv_t) {
+  const Sum all = tail && t.any ? join(sum, {t.z_m, t.on}, c) : sum;
+  RowPlan r{sum.m, 0.f, w * inv_t, 0.f, all.m, 0.f, 1.f, false};
+  if (!t.any || (!tail && t.u == 0.f)) {
+    r.scale = 0.f;
+    r.zero = true;
+    return r;
+  }
+  const float log_all = log_fast(all.s);
+  if (all.s != 0.f) r.all_r = __fdividef(1.f, all.s);
+  // sum q_j (log q_j - log p_j), log p_j = log_p + (z_j - z_m) / T
+  const float log_p = all.s == 0.f ? -CUDART_INF_F : (t.z_m - all.m) * inv_t - log_all;
+  float loss;
   if (tail) {
-    float q_rest = 1.f - q_sum;
+    loss = t.u == 0.f ? 0.f : fmaf(-t.u, log_p, t.ul * kDistillMaxTop);
+  } else {
+    r.u_r = __fdividef(1.f, t.u);
+    loss = t.ul * r.u_r * kDistillMaxTop - log_fast(t.u) - log_p;
+  }
+  if (t.u != t.u) loss = r.scale = t.u;
+  r.rest_scale = __fdividef(r.scale, sum.s);
+  if (tail) {
+    float q_rest = 1.f - t.u;
     if (q_rest <= kTailFloor) q_rest = 0.f;
-    const bool none = sum.m == -CUDART_INF_F && sum.s == 0.f;
-    const float lp_rest = none ? -CUDART_INF_F : (sum.m - r.all.m) * inv_t + (logf(sum.s) - log_all);
-    if (q_rest != 0.f) loss = fmaf(q_rest, logf(q_rest) - lp_rest, loss);
+    const float lp_rest = sum.s == 0.f ? -CUDART_INF_F : (sum.m - all.m) * inv_t + (log_fast(sum.s) - log_all);
+    if (q_rest != 0.f) loss = fmaf(q_rest, log_fast(q_rest) - lp_rest, loss);
     r.rest_scale *= exp2_fast(lp_rest * kLog2e) - q_rest;
   }
-  if (sum.s == 0.f) r.rest_m = CUDART_INF_F, r.rest_scale = 0.f;  // no code off the list has a share
+  if (sum.s == 0.f) r.m = 0.f, r.rest_scale = 0.f;  // no code off the list has a share
   r.loss = loss * w;
   return r;
 }
 
 // Entry j's gradient.
-__device__ __forceinline__ float top_grad(const RowPlan &r, float t, float z, float c, float inv_t) {
+__device__ __forceinline__ float top_grad(const RowPlan &r, const TopSums &t, const TopList &l, int j, float c,
+                                          float inv_t) {
   if (r.scale == 0.f) return 0.f;
-  const float p = r.all.s == 0.f ? 0.f : share(z, r.all.m, c) / r.all.s;
-  return (p - exp2_fast(log_q(r, t, inv_t) * kLog2e)) * r.scale;
+  const float p = r.all_r == 0.f ? 0.f : share(l.z[j], r.all_m, c) * r.all_r;
+  return (p - entry_u(t, l.t[j], inv_t) * r.u_r) * r.scale;
 }
 
-// A row per block, read twice: once for the sum, once for the gradient (the
-// second time from the L2).
+// e^((z - m) / T).  m is subtracted first: as 2^(z c - m c), one operation less,
+// the product m c would have to be exact (masks of -1e9 and of the type's
+// lowest value are large ms).
+struct Power {
+  float m, c;
+  __device__ __forceinline__ Power(float m_, float c_) {
+    m = m_ == -CUDART_INF_F ? 0.f : m_;
+    c = c_;
+  }
+  __device__ __forceinline__ float operator()(float z) const { return exp2_fast((z - m) * c); }
+};
+
 template <class T>
-__global__ void __launch_bounds__(256) k_distill(const DistillArgs a) {
+__device__ __forceinline__ uint4 all_low() {  // a vector of -inf
+  const uint32_t w = sizeof(T) == 4 ? 0xff800000u : std::is_same<T, __half>::value ? 0xfc00fc00u : 0xff80ff80u;
+  return make_uint4(w, w, w, w);
+}
+template <class T>
+__device__ __forceinline__ float largest(const uint4 &v, float m) {
+  float f[16 / sizeof(T)];
+  unpack16<T>(v, f);
+#pragma unroll
+  for (int i = 0; i < 16 / (int)sizeof(T); ++i) m = fmaxf(m, f[i]);
+  return m;
+}
+
+// A thread's share of a row in registers: the vectors t, t + threads, ... and
+// perhaps an edge element.
+template <class T, int NV>
+struct Share {
+  static constexpr int N = 16 / (int)sizeof(T);
+  float e[NV][N], edge;
+  uint4 raw[NV];
+  __device__ __forceinline__ void load(const Row<T> &r, int t, int threads) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) raw[j] = t + j * threads < r.full ? r.vector(t + j * threads) : all_low<T>();
+    const int at = r.edge(t);
+    edge = at >= 0 ? to_float(r.z[at]) : -CUDART_INF_F;
+  }
+  __device__ __forceinline__ float most() const {
+    float m = edge;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) m = largest<T>(raw[j], m);
+    return m;
+  }
+  // The powers in place of the values; the sum of those without a bit.
+  __device__ __forceinline__ float powers(const Row<T> &r, const Power &pw, const uint32_t *bits, int t, int threads) {
+    float s = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int v = t + j * threads, at = v * N + 8;
+      const uint32_t skip = bits && v < r.full ? bits[at >> 5] >> (at & 31) : 0;
+      unpack16<T>(raw[j], e[j]);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        e[j][i] = pw(e[j][i]);
+        if (!(skip >> i & 1)) s += e[j][i];
+      }
+    }
+    const int at = r.edge(t);
+    edge = pw(edge);
+    if (at >= 0 && !(bits && bits[r.place(at) >> 5] >> (r.place(at) & 31) & 1)) s += edge;
+    return s;
+  }
+  __device__ __forceinline__ void put(const Row<T> &r, bool zero, float factor, int t, int threads) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if (t + j * threads >= r.full) continue;
+#pragma unroll
+      for (int i = 0; i < N; ++i) e[j][i] = zero ? 0.f : e[j][i] * factor;
+      r.put(t + j * threads, e[j]);
+    }
+    const int at = r.edge(t);
+    if (at >= 0) r.d[at] = from_float<T>(zero ? 0.f : edge * factor);
+  }
+};
+
+// The sum over a row's threads: a warp's, or a block's through `box` (after a
+// barrier that every earlier use of it has passed).
+template <bool WARP>
+__device__ __forceinline__ Sum row_join(Sum v, float c, Sum *box) {
+  v = warp_join(v, c);
+  if constexpr (!WARP) {
+    const int lane = threadIdx.x & 31;
+    __syncthreads();
+    if (lane == 0) box[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = warp_join(lane < (int)blockDim.x >> 5 ? box[lane] : no_sum(), c);
+  }
+  return v;
+}
+
+// The sum over the codes without an entry, from its own largest value: where
+// the entries hold all but 1e-25 of the row.
+template <class T, bool WARP>
+__device__ __noinline__ Sum small_rest(const Row<T> &r, const uint32_t *bits, int t, int threads, float c, Sum *box) {
+  Sum sum = no_sum();
+  for (int e = t; e < r.width; e += threads) {
+    const int p = r.place(e);
+    if (!(bits[p >> 5] >> (p & 31) & 1)) sum = join(sum, {to_float(r.z[e]), to_float(r.z[e]) == -CUDART_INF_F ? 0.f : 1.f}, c);
+  }
+  return row_join<WARP>(sum, c, box);
+}
+constexpr float kSmallRest = 1e-25f;
+
+// A row without weight: thread t of `threads`.
+template <class T>
+__device__ __forceinline__ void skip_row(const DistillArgs &a, int64_t row, const Row<T> &r, int t, int threads) {
+  if (t == 0 && a.sums_in == nullptr) {
+    a.loss[row] = 0.f;
+    if (a.sums) a.sums[2 * row] = a.sums[2 * row + 1] = 0.f;
+  }
+  if (!r.d) return;
+  const float zero[Row<T>::N] = {};
+  for (int v = t; v < r.full; v += threads) r.put(v, zero);
+  const int at = r.edge(t);
+  if (at >= 0) r.d[at] = from_float<T>(0.f);
+}
+
+// A row in the registers of a warp (WARP: kRowWarps rows a block, no barrier)
+// or of a block: one read of the logits, one write of the gradient.
+constexpr int kRowWarps = 4, kMaxWarps = 16;
+template <class T, int NV, bool WARP>
+__global__ void __launch_bounds__(WARP ? 32 * kRowWarps : 32 * kMaxWarps) k_distill(const DistillArgs a) {
+  extern __shared__ uint32_t smem[];
+  __shared__ Sum box[kMaxWarps];
+  __shared__ TopSums shared_top;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, top = a.dm.top, words = distill_bit_words(a.dm.vocab);
+  const int t = WARP ? lane : threadIdx.x, threads = WARP ? 32 : blockDim.x;
+  const int64_t row = WARP ? (int64_t)blockIdx.x * kRowWarps + warp : blockIdx.x;
+  if (row >= a.dm.rows) return;
+  const Row<T> r(a, row);
+  float w = a.weights ? a.weights[row] : 1.f;
+  if (w == 0.f) return skip_row(a, row, r, t, threads);
+  const bool tail = a.teacher_lse != nullptr, known = a.sums_in != nullptr;
+  const float inv_t = 1.f / a.dm.temperature, c = kLog2e * inv_t;
+  Share<T, NV> x;
+  x.load(r, t, threads);
+  const TopList l = top_list(smem + (WARP ? (size_t)warp * (words + 3 * top) : 0), words, top);
+  for (int i = t; i < words; i += threads) l.bits[i] = 0;
+  TopSums ts;
+  if constexpr (WARP) {
+    __syncwarp();
+    read_top(a, row, r, l);
+    ts = top_sums(a, row, inv_t, l);
+  } else {
+    __syncthreads();
+    if (warp == 0) {
+      read_top(a, row, r, l);
+      ts = top_sums(a, row, inv_t, l);
+      if (lane == 0) shared_top = ts;
+    }
+    __syncthreads();
+    ts = shared_top;
+  }
+  Sum sum;
+  float m;
+  if (known) {
+    sum = {a.sums_in[2 * row], a.sums_in[2 * row + 1]};
+    if (a.grad_loss) w *= a.grad_loss[row];
+    m = sum.m;
+  } else {
+    m = warp_max_order(x.most());
+  }
+  Power pw(m, c);
+  const float s = x.powers(r, pw, tail && !known ? l.bits : nullptr, t, threads);
+  if (!known) {
+    if constexpr (WARP) {
+      sum = {m, warp_sum(s)};
+    } else {
+      const float all = warp_sum(s);
+      if (lane == 0) box[warp] = {m, all};
+      __syncthreads();
+      sum = warp_join(lane < threads >> 5 ? box[lane] : no_sum(), c);
+    }
+    if (tail && sum.s < kSmallRest) {
+      sum = small_rest<T, WARP>(r, l.bits, t, threads, c, box);
+      m = sum.m;
+      pw = Power(m, c);
+      x.load(r, t, threads);
+      x.powers(r, pw, nullptr, t, threads);
+    }
+  }
+  const RowPlan p = plan_row(tail, w, sum, ts, c, inv_t);
+  if (!known && t == 0) {
+    a.loss[row] = p.loss;
+    if (a.sums) a.sums[2 * row] = sum.m, a.sums[2 * row + 1] = sum.s;
+  }
+  if (!r.d) return;
+  x.put(r, p.zero, p.rest_scale == 0.f ? 0.f : p.rest_scale * share(m, p.m, c), t, threads);
+  // the entries' gradients go over what was written in their place
+  if constexpr (WARP)
+    __syncwarp();
+  else
+    __syncthreads();
+  for (int j = t; j < top; j += threads)
+    if (l.code[j] >= 0) r.d[l.code[j]] = from_float<T>(top_grad(p, ts, l, j, c, inv_t));
+}
+
+// Longer rows: a row per block, read twice (the second time from the L2), U
+// vectors of a thread at a time.
+constexpr int kLongThreads = 512;
+template <class T, int U>
+__global__ void __launch_bounds__(kLongThreads) k_distill_long(const DistillArgs a) {
   constexpr int N = 16 / (int)sizeof(T);
   extern __shared__ uint32_t smem[];
-  __shared__ Sum box[8];
-  __shared__ RowPlan plan;
-  const int vocab = a.dm.vocab, top = a.dm.top, words = distill_bit_words(vocab);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-  const TopList l = {smem, reinterpret_cast<int32_t *>(smem + words), reinterpret_cast<float *>(smem + words + top),
-                     reinterpret_cast<float *>(smem + words + 2 * top)};
-  const float c = kLog2e / a.dm.temperature;
+  __shared__ Sum box[kMaxWarps];
+  __shared__ TopSums shared_top;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, threads = blockDim.x;
+  const int top = a.dm.top, words = distill_bit_words(a.dm.vocab);
+  const int64_t row = blockIdx.x;
+  const Row<T> r(a, row);
+  float w = a.weights ? a.weights[row] : 1.f;
+  if (w == 0.f) return skip_row(a, row, r, threadIdx.x, threads);
   const bool tail = a.teacher_lse != nullptr, known = a.sums_in != nullptr;
-  for (int64_t row = blockIdx.x; row < a.dm.rows; row += gridDim.x) {
-    const RowVectors<T> in(static_cast<const T *>(a.logits) + row * a.logits_stride, vocab);
-    const int nv = in.count();
-    T *out_row = a.dlogits ? static_cast<T *>(a.dlogits) + row * a.dlogits_stride : nullptr;
-    const RowVectors<T> out(out_row, vocab);
-    const float w = (a.weights ? a.weights[row] : 1.f);
-    if (w == 0.f) {
-      if (threadIdx.x == 0 && !known) {
-        a.loss[row] = 0.f;
-        if (a.sums) a.sums[2 * row] = a.sums[2 * row + 1] = 0.f;
-      }
-      const float zero[N] = {};
-      if (out_row)
-        for (int v = threadIdx.x; v < out.count(); v += blockDim.x) out.store(v, zero);
-      continue;
-    }
-    __syncthreads();  // the row before is done with the shared memory
-    for (int i = threadIdx.x; i < words; i += blockDim.x) l.bits[i] = 0;
-    __syncthreads();
-    if (warp == 0) read_top(a, row, static_cast<const T *>(a.logits) + row * a.logits_stride, in.phase, l);
-    __syncthreads();
-    Sum sum = no_sum();
-    if (!known) {
-      for (int v = threadIdx.x; v < nv; v += blockDim.x) {
-        float f[N];
-        unpack16<T>(in.load(v, from_float<T>(-CUDART_INF_F)), f);
-        const uint32_t skip = tail ? l.bits[v * N >> 5] >> (v * N & 31) : 0;
-        float m = -CUDART_INF_F;
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          if (skip >> i & 1) f[i] = -CUDART_INF_F;
-          m = fmaxf(m, f[i]);
-        }
-        const float at = m == -CUDART_INF_F ? 0.f : m;
-        float s = 0.f;
-#pragma unroll
-        for (int i = 0; i < N; ++i) s += share(f[i], at, c);
-        sum = join(sum, {m, s}, c);
-      }
-      sum = warp_join(sum, c);
-      if (lane == 0) box[warp] = sum;
-      __syncthreads();
-    }
-    if (warp == 0) {
-      if (known)
-        sum = {a.sums_in[2 * row], a.sums_in[2 * row + 1]};
-      else
-        sum = warp_join(lane < warps ? box[lane] : no_sum(), c);
-      const RowPlan r = plan_row(a, row, known && a.grad_loss ? w * a.grad_loss[row] : w, sum, c, l);
-      if (lane == 0) {
-        plan = r;
-        if (!known) {
-          a.loss[row] = r.loss;
-          if (a.sums) a.sums[2 * row] = sum.m, a.sums[2 * row + 1] = sum.s;
-        }
-      }
-    }
-    if (!out_row) continue;
-    __syncthreads();
-    const RowPlan r = plan;
-    for (int v = threadIdx.x; v < nv; v += blockDim.x) {
-      float f[N];
-      unpack16<T>(in.load(v, from_float<T>(-CUDART_INF_F)), f);
-#pragma unroll
-      for (int i = 0; i < N; ++i)
-        f[i] = r.rest_m == CUDART_INF_F && r.rest_scale == 0.f ? 0.f : share(f[i], r.rest_m, c) * r.rest_scale;
-      if (out.phase == in.phase) {
-        out.store(v, f);
-      } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const int e = v * N + i - in.phase;
-          if (e >= 0 && e < vocab) out_row[e] = from_float<T>(f[i]);
-        }
-      }
-    }
-    __syncthreads();  // the entries' gradients go over what was written in their place
-    for (int j = threadIdx.x; j < top; j += blockDim.x)
-      if (l.code[j] >= 0) out_row[l.code[j]] = from_float<T>(top_grad(r, l.t[j], l.z[j], c, 1.f / a.dm.temperature));
+  const float inv_t = 1.f / a.dm.temperature, c = kLog2e * inv_t;
+  const TopList l = top_list(smem, words, top);
+  for (int i = threadIdx.x; i < words; i += threads) l.bits[i] = 0;
+  __syncthreads();
+  if (warp == 0) {
+    read_top(a, row, r, l);
+    const TopSums t = top_sums(a, row, inv_t, l);
+    if (lane == 0) shared_top = t;
   }
+  __syncthreads();
+  const TopSums ts = shared_top;
+  const int edge = r.edge(threadIdx.x);
+  Sum sum;
+  if (known) {
+    sum = {a.sums_in[2 * row], a.sums_in[2 * row + 1]};
+    if (a.grad_loss) w *= a.grad_loss[row];
+  } else {
+    float m = edge >= 0 ? to_float(r.z[edge]) : -CUDART_INF_F, s = 0.f;
+    Power pw(m, c);
+    if (edge >= 0 && !(tail && l.bits[r.place(edge) >> 5] >> (r.place(edge) & 31) & 1)) s = pw(to_float(r.z[edge]));
+    for (int v0 = threadIdx.x; v0 < r.full; v0 += U * threads) {
+      uint4 raw[U];
+      float most = m;
+#pragma unroll
+      for (int j = 0; j < U; ++j) raw[j] = v0 + j * threads < r.full ? r.vector(v0 + j * threads) : all_low<T>();
+#pragma unroll
+      for (int j = 0; j < U; ++j) most = largest<T>(raw[j], most);
+      if (most > m) {
+        s *= share(m, most, c);
+        m = most;
+        pw = Power(m, c);
+      }
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        const int v = v0 + j * threads, at = v * N + 8;
+        const uint32_t skip = tail && v < r.full ? l.bits[at >> 5] >> (at & 31) : 0;
+        float f[N];
+        unpack16<T>(raw[j], f);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const float e = pw(f[i]);
+          if (!(skip >> i & 1)) s += e;
+        }
+      }
+    }
+    sum = row_join<false>({m, s}, c, box);
+    if (tail && sum.s < kSmallRest) sum = small_rest<T, false>(r, l.bits, threadIdx.x, threads, c, box);
+  }
+  const RowPlan p = plan_row(tail, w, sum, ts, c, inv_t);
+  if (!known && threadIdx.x == 0) {
+    a.loss[row] = p.loss;
+    if (a.sums) a.sums[2 * row] = sum.m, a.sums[2 * row + 1] = sum.s;
+  }
+  if (!r.d) return;
+  const Power pw(p.m, c);
+  const float factor = p.rest_scale;
+  for (int v0 = threadIdx.x; v0 < r.full; v0 += U * threads) {
+    uint4 raw[U];
+#pragma unroll
+    for (int j = 0; j < U; ++j) raw[j] = v0 + j * threads < r.full ? r.vector(v0 + j * threads) : all_low<T>();
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      if (v0 + j * threads >= r.full) continue;
+      float f[N];
+      unpack16<T>(raw[j], f);
+#pragma unroll
+      for (int i = 0; i < N; ++i) f[i] = p.zero ? 0.f : pw(f[i]) * factor;
+      r.put(v0 + j * threads, f);
+    }
+  }
+  if (edge >= 0) r.d[edge] = from_float<T>(p.zero ? 0.f : pw(to_float(r.z[edge])) * factor);
+  __syncthreads();
+  for (int j = threadIdx.x; j < top; j += threads)
+    if (l.code[j] >= 0) r.d[l.code[j]] = from_float<T>(top_grad(p, ts, l, j, c, inv_t));
+}
+
+// How a row is laid over threads: at most 32 elements of its vectors a thread,
+// in a warp or a block of 64 .. 512; above that the two reads (threads 0).
+struct DistillShape {
+  int threads, vectors;  // of a row; of a thread
+};
+inline DistillShape distill_shape(int vocab, int n) {
+  const int full = vocab / n;
+  for (int threads = 32; threads <= 32 * kMaxWarps; threads *= 2) {
+    const int each = (full + threads - 1) / threads;
+    if (each * n <= 32) return {threads, each > 0 ? each : 1};
+  }
+  return {0, 1};
+}
+
+template <class T, int NV>
+cudaError_t launch_distill_shape(const DistillArgs &a, int threads, cudaStream_t st) {
+  const size_t smem = distill_smem(a.dm.vocab, a.dm.top);
+  if (threads == 32)
+    k_distill<T, NV, true>
+        <<<(unsigned)((a.dm.rows + kRowWarps - 1) / kRowWarps), 32 * kRowWarps, smem * kRowWarps, st>>>(a);
+  else
+    k_distill<T, NV, false><<<(unsigned)a.dm.rows, threads, smem, st>>>(a);
+  return cudaGetLastError();
 }
 
 template <class T>
 cudaError_t launch_distill_typed(const DistillArgs &a, cudaStream_t st) {
+  constexpr int N = 16 / (int)sizeof(T), U = 8 / N;  // vectors of 8 elements
+  const DistillShape s = distill_shape(a.dm.vocab, N);
+  if (s.threads) {
+    switch ((s.vectors + U - 1) / U) {
+      case 1: return launch_distill_shape<T, U>(a, s.threads, st);
+      case 2: return launch_distill_shape<T, 2 * U>(a, s.threads, st);
+      case 3: return launch_distill_shape<T, 3 * U>(a, s.threads, st);
+      default: return launch_distill_shape<T, 4 * U>(a, s.threads, st);
+    }
+  }
   const size_t smem = distill_smem(a.dm.vocab, a.dm.top);
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(k_distill<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (smem > 40 * 1024) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(k_distill_long<T, 4>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
   }
-  const int block = a.dm.vocab <= 2048 ? 128 : 256;
-  k_distill<T><<<(unsigned)(a.dm.rows < (1 << 30) ? a.dm.rows : (1 << 30)), block, smem, st>>>(a);
+  k_distill_long<T, 4><<<(unsigned)a.dm.rows, kLongThreads, smem, st>>>(a);
   return cudaGetLastError();
 }
 
-cudaError_t launch_distill(const DistillArgs &a, cudaStream_t st) {
+// Rows go to the grid's first axis.
+constexpr int64_t kDistillMaxRows = ((int64_t)1 << 31) - 8;
+cudaError_t launch_distill_rows(const DistillArgs &a, cudaStream_t st) {
   switch (a.dm.dtype) {
     case RVQ_DTYPE_F32: return launch_distill_typed<float>(a, st);
     case RVQ_DTYPE_BF16: return launch_distill_typed<__nv_bfloat16>(a, st);
     default: return launch_distill_typed<__half>(a, st);
   }
+}
+
+cudaError_t launch_distill(DistillArgs a, cudaStream_t st) {
+  const int64_t rows = a.dm.rows;
+  const int e = dtype_bytes(a.dm.dtype), te = dtype_bytes(a.dm.top_dtype);
+  for (int64_t r0 = 0; r0 < rows; r0 += kDistillMaxRows) {
+    DistillArgs b = a;
+    b.dm.rows = rows - r0 < kDistillMaxRows ? rows - r0 : kDistillMaxRows;
+    auto skip = [&](auto &p, int64_t n) {
+      if (p) p += n;
+    };
+    b.logits = static_cast<const char *>(a.logits) + r0 * a.logits_stride * e;
+    b.top_logits = static_cast<const char *>(a.top_logits) + r0 * a.dm.top * te;
+    b.top_codes += r0 * a.dm.top;
+    if (a.dlogits) b.dlogits = static_cast<char *>(a.dlogits) + r0 * a.dlogits_stride * e;
+    skip(b.teacher_lse, r0), skip(b.weights, r0), skip(b.grad_loss, r0), skip(b.loss, r0);
+    skip(b.sums, 2 * r0), skip(b.sums_in, 2 * r0);
+    const cudaError_t err = launch_distill_rows(b, st);
+    if (err != cudaSuccess) return err;
+  }
+  return cudaSuccess;
 }
 
 rvq_status check_distill(const DistillArgs &a) {

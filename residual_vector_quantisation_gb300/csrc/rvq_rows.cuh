@@ -130,6 +130,14 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
+// The largest of a warp's values, by one integer reduction over their order (a
+// NaN's place in it is unspecified).
+__device__ __forceinline__ float warp_max_order(float v) {
+  const uint32_t b = __float_as_uint(v);
+  const uint32_t o = __reduce_max_sync(0xffffffffu, b & 0x80000000u ? ~b : b | 0x80000000u);
+  return __uint_as_float(o & 0x80000000u ? o & 0x7fffffffu : ~o);
+}
+
 // 2^x to about 2 units in the last place (subnormal results become zero).
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
