@@ -2,10 +2,13 @@
 // the reordering of the states that follow them (rvq_beam_select,
 // rvq_beam_reorder).
 //
-// Selection is one read of the logits.  k_beam_rows: blocks over pieces of the
-// beams' rows, each leaving its piece's best `select` entries in order and its
-// part of the row's log sum exp.  k_beam_groups: a warp per group walks those
-// lists from their heads.
+// Selection is one read of the logits.  A warp takes pieces of a row (32
+// elements a lane, in registers) and keeps the row's best `select` entries so
+// far: the n-th best of the lanes' largest values is a bar that at least n
+// entries reach and few others do, so that only those are put in order.  A
+// group of few pieces runs in one block that also joins the beams
+// (k_beam_group); larger ones spread a row over blocks (k_beam_rows), whose
+// lists a second kernel joins (k_beam_join).
 #include "rvq_internal.cuh"
 #include "rvq_rows.cuh"
 
@@ -14,10 +17,12 @@ namespace {
 
 constexpr int kBeamMax = 64;           // beams, and candidates kept
 constexpr int kBeamMaxVocab = 1 << 24;
-constexpr int kRowThreads = 256;
-constexpr int kRowPiece = 16;          // elements of a thread per step
-constexpr int kRowStep = kRowThreads * kRowPiece;
-constexpr int kBeamMaxSplits = 16;
+constexpr int kRowWarps = 8;           // of a block that shares a row
+constexpr int kGroupWarps = 16;        // most warps of a block that takes a group
+constexpr int kGroupItems = 64;        // most pieces of such a group
+constexpr int kMaxLists = 128;         // most lists that a group's join reads
+constexpr int kLane = 32;              // elements of a lane in a piece
+constexpr int kRoom = 128;             // entries that a warp puts in order at once, beside those it holds
 
 // An entry's place in the order: the larger value first, then the lower code.
 // 0 is no entry (NaN and -inf have none).
@@ -67,193 +72,335 @@ __device__ __forceinline__ bool beam_live(const BeamArgs &a, int64_t row) {
   return a.scores[row] > -CUDART_INF_F && !(a.finished && a.finished[row]);
 }
 
+// A warp's shared memory: the entries to be put in order, and the best so far.
+struct WarpRoom {
+  uint64_t room[kRoom + kBeamMax], best[kBeamMax];
+  int count;
+};
+
+// Lane l gets the (l + 1)-th largest of the lanes' values.
+__device__ __forceinline__ uint32_t warp_sorted(uint32_t v) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int k = 2; k <= 32; k *= 2)
+#pragma unroll
+    for (int j = k / 2; j; j /= 2) {
+      const uint32_t o = __shfl_xor_sync(0xffffffffu, v, j);
+      const bool high = ((lane & k) == 0) == ((lane & j) == 0);
+      v = high ? max(v, o) : min(v, o);
+    }
+  return v;
+}
+
+// The pieces `first`, `first` + `step`, ... of a row: the best n entries in
+// order in r.best (0: none), and the sum of e^z as (m, s), s of this lane alone.
 template <class T>
-__global__ void __launch_bounds__(kRowThreads) k_beam_rows(const BeamArgs a) {
-  constexpr int N = 16 / (int)sizeof(T), NV = kRowPiece / N;
-  constexpr int kRoom = kBeamMax * kRowPiece + kBeamMax;
-  __shared__ uint64_t best[kBeamMax], most[kRowThreads], room[kRoom];
+__device__ __forceinline__ void warp_pieces(const CutRow<T> &in, int first, int step, int n, bool raw, float add,
+                                            WarpRoom &r, float &m, float &s) {
+  constexpr int N = 16 / (int)sizeof(T), NV = kLane / N;
+  const int lane = threadIdx.x & 31;
+  for (int i = lane; i < kBeamMax; i += 32) r.best[i] = 0;
+  if (lane == 0) r.count = 0;
+  m = -CUDART_INF_F, s = 0.f;
+  __syncwarp();
+  bool held = false;
+  for (int p = first; p == 0 || p * NV * 32 < in.full; p += step) {
+    float z[NV][N];
+    uint4 raw4[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int v = (p * NV + j) * 32 + lane;
+      raw4[j] = v < in.full ? in.vector(v) : all_low<T>();
+    }
+    const int edge_at = p == 0 ? in.edge(lane) : -1;
+    float edge = edge_at >= 0 ? to_float(in.z[edge_at]) : -CUDART_INF_F;
+    float half[2] = {-CUDART_INF_F, -CUDART_INF_F};  // the largest of each half of the lane's elements
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      unpack16<T>(raw4[j], z[j]);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        if (raw) z[j][i] += add;
+        half[j * N >= kLane / 2] = fmaxf(half[j * N >= kLane / 2], z[j][i]);
+      }
+    }
+    if (raw) edge += add;
+    half[0] = fmaxf(half[0], edge);
+    const float high = fmaxf(half[0], half[1]);
+    if (!raw) {
+      const float most = fmaxf(m, warp_max_order(high)), at = most == -CUDART_INF_F ? 0.f : most;
+      s *= exp2_fast((m - at) * kLog2e);
+      m = most;
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < N; ++i) s += exp2_fast((z[j][i] - at) * kLog2e);
+      s += exp2_fast((edge - at) * kLog2e);
+    }
+    const uint64_t last = held ? r.best[n - 1] : 0;  // an entry counts if it is above this
+    const uint32_t last_value = (uint32_t)(last >> 32);
+    if (!__any_sync(0xffffffffu, order_of(high) > 0 && order_of(high) >= last_value)) continue;
+    uint32_t bar;
+    if (n <= 32) {
+      bar = __shfl_sync(0xffffffffu, warp_sorted(order_of(high)), n - 1);
+    } else {
+      const int at = (n + 1) / 2 - 1;
+      bar = min(__shfl_sync(0xffffffffu, warp_sorted(order_of(half[0])), at),
+                __shfl_sync(0xffffffffu, warp_sorted(order_of(half[1])), at));
+    }
+    bar = max(bar, last_value);
+    const float line = bar ? value_of(bar) : -3.402823466e38f;
+    int mine = edge >= line;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < N; ++i) mine += z[j][i] >= line;
+    const int reach = __reduce_add_sync(0xffffffffu, mine);
+    if (reach <= kRoom) {
+      if (mine) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+          for (int i = 0; i < N; ++i)
+            if (z[j][i] >= line) {
+              const uint64_t k = key_of(z[j][i], in.head + ((p * NV + j) * 32 + lane) * N + i);
+              if (k > last) r.room[atomicAdd(&r.count, 1)] = k;
+            }
+        if (edge >= line) {
+          const uint64_t k = key_of(edge, edge_at);
+          if (k > last) r.room[atomicAdd(&r.count, 1)] = k;
+        }
+      }
+    } else {
+      // many equal values at the bar: the best n one after the other
+      uint64_t below = ~0ull;
+      for (int c = 0; c < n; ++c) {
+        uint64_t k = 0;
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            const uint64_t e = key_of(z[j][i], in.head + ((p * NV + j) * 32 + lane) * N + i);
+            if (e < below && e > k) k = e;
+          }
+        const uint64_t e = key_of(edge, edge_at);
+        if (e < below && e > k) k = e;
+        const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(k >> 32));
+        const uint32_t lo = __reduce_max_sync(0xffffffffu, (uint32_t)(k >> 32) == hi ? (uint32_t)k : 0u);
+        below = (uint64_t)hi << 32 | lo;
+        if (below <= last) break;
+        if (lane == 0) r.room[c] = below, r.count = c + 1;
+      }
+    }
+    __syncwarp();
+    // every entry's place among the new ones and those held
+    const int fresh = r.count;
+    if (fresh) {
+      const int all = held ? fresh + n : fresh;
+      if (held)
+        for (int i = lane; i < n; i += 32) r.room[fresh + i] = r.best[i];
+      __syncwarp();
+      for (int i = lane; i < all; i += 32) {
+        const uint64_t k = r.room[i];
+        int place = 0;
+        for (int j = 0; j < all; ++j) place += r.room[j] > k;
+        if (k && place < n) r.best[place] = k;
+      }
+      held = true;
+      if (lane == 0) r.count = 0;
+      __syncwarp();
+    }
+  }
+}
+
+// The join of a group's lists in shared memory: `lists` of n entries each, list
+// i of beam i / per, sum[i] its part of the beam's sum; by all threads.
+struct Join {
+  uint64_t room[2 * kRoom + kBeamMax], tie[2 * kRoom + kBeamMax];
+  float2 lse[kBeamMax];  // of a row: m, log s
+  uint64_t head[32];
+  uint32_t bar;
+  int count;
+};
+
+__device__ __forceinline__ uint32_t total_of(const BeamArgs &a, const Join &w, float score, int beam, uint64_t key) {
+  if (!key) return 0;
+  const float v = value_of((uint32_t)(key >> 32));
+  return order_of(a.dm.mode == RVQ_BEAM_RAW ? v : score + ((v - w.lse[beam].x) - w.lse[beam].y));
+}
+
+__device__ void join_group(const BeamArgs &a, int64_t g, uint64_t *list, const float2 *sum, int per, Join &w) {
+  const int B = a.dm.beams, n = a.dm.select, lists = B * per, tid = threadIdx.x, lane = tid & 31;
+  for (int b = tid; b < B; b += blockDim.x) {
+    const int64_t row = g * B + b;
+    float m = 0.f, s = 1.f;
+    if (beam_live(a, row)) {
+      if (a.dm.mode != RVQ_BEAM_RAW) {
+        m = -CUDART_INF_F, s = 0.f;
+        for (int i = 0; i < per; ++i) join_sum(m, s, sum[b * per + i].x, sum[b * per + i].y);
+      }
+    } else {
+      // a finished beam's one candidate, at its score; a dead one's none
+      const bool done = a.scores[row] > -CUDART_INF_F;
+      for (int i = 0; i < per * n; ++i) list[b * per * n + i] = 0;
+      if (done) list[b * per * n] = key_of(0.f, a.end_code);
+    }
+    w.lse[b] = make_float2(m, logf(s));
+  }
+  if (tid == 0) w.bar = 0, w.count = 0;
+  __syncthreads();
+  auto total = [&](int i) -> uint32_t {  // of entry i
+    const int b = i / n / per;
+    const int64_t row = g * B + b;
+    const uint64_t k = list[i];
+    if (k && a.finished && a.finished[row]) return order_of(a.scores[row]);
+    return k ? total_of(a, w, a.scores[row], b, k) : 0;
+  };
+  // the best of the lists' last entries is a bar that n entries reach
+  uint32_t bar = 0;
+  for (int i = tid; i < lists; i += blockDim.x) bar = max(bar, total(i * n + n - 1));
+  bar = __reduce_max_sync(0xffffffffu, bar);
+  if (lane == 0 && bar) atomicMax(&w.bar, bar);
+  __syncthreads();
+  bar = max(w.bar, 1u);
+  constexpr int kTop = 2 * kRoom;
+  for (int i = tid; i < lists * n; i += blockDim.x) {
+    const uint32_t t = total(i);
+    if (t >= bar) {
+      const int at = atomicAdd(&w.count, 1);
+      if (at < kTop) {
+        w.room[at] = (uint64_t)t << 32 | (uint32_t)~(i / n / per);
+        w.tie[at] = list[i];
+      }
+    }
+  }
+  __syncthreads();
+  const int all = w.count;
+  auto put = [&](int place, uint64_t k, uint64_t tie) {
+    const int64_t o = g * n + place;
+    const int beam = (int)~(uint32_t)k, code = (int)~(uint32_t)tie;
+    a.out_scores[o] = value_of((uint32_t)(k >> 32));
+    a.parents[o] = beam;
+    a.codes[o] = code;
+    if (a.out_finished) a.out_finished[o] = (a.finished && a.finished[g * B + beam]) || code == a.end_code;
+  };
+  int found = min(all, n);
+  if (all <= kTop) {
+    for (int i = tid; i < all; i += blockDim.x) {
+      const uint64_t k = w.room[i], t = w.tie[i];
+      int place = 0;
+      for (int j = 0; j < all; ++j) place += w.room[j] > k || (w.room[j] == k && w.tie[j] > t);
+      if (place < n) put(place, k, t);
+    }
+  } else if (tid < 32) {
+    // many equal totals: the best n one after the other
+    uint64_t k0 = ~0ull, t0 = ~0ull;
+    for (int c = 0; c < n; ++c) {
+      uint64_t k = 0, t = 0;
+      for (int i = lane; i < lists * n; i += 32) {
+        const uint32_t tot = total(i);
+        if (!tot) continue;
+        const uint64_t ki = (uint64_t)tot << 32 | (uint32_t)~(i / n / per), ti = list[i];
+        if ((ki < k0 || (ki == k0 && ti < t0)) && (ki > k || (ki == k && ti > t))) k = ki, t = ti;
+      }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) {
+        const uint64_t k2 = __shfl_xor_sync(0xffffffffu, k, o), t2 = __shfl_xor_sync(0xffffffffu, t, o);
+        if (k2 > k || (k2 == k && t2 > t)) k = k2, t = t2;
+      }
+      if (lane == 0) put(c, k, t);
+      k0 = k, t0 = t;
+    }
+  }
+  for (int j = found + tid; j < n; j += blockDim.x) {
+    const int64_t o = g * n + j;
+    a.out_scores[o] = -CUDART_INF_F;
+    a.parents[o] = a.codes[o] = -1;
+    if (a.out_finished) a.out_finished[o] = 1;
+  }
+}
+
+// A block per group: `per` warps' shares of each beam's row, then the join.
+template <class T>
+__global__ void __launch_bounds__(32 * kGroupWarps) k_beam_group(const BeamArgs a) {
+  extern __shared__ uint64_t smem[];
+  __shared__ Join join;
+  const int n = a.dm.select, B = a.dm.beams, lane = threadIdx.x & 31, warps = blockDim.x >> 5, per = a.splits;
+  uint64_t *list = smem;
+  float2 *sum = reinterpret_cast<float2 *>(list + (size_t)B * per * n);
+  WarpRoom &room = reinterpret_cast<WarpRoom *>(sum + B * per)[threadIdx.x >> 5];
+  const int64_t g = blockIdx.x;
+  const bool raw = a.dm.mode == RVQ_BEAM_RAW;
+  for (int i = threadIdx.x >> 5; i < B * per; i += warps) {
+    const int64_t row = g * B + i / per;
+    if (!beam_live(a, row)) continue;
+    const CutRow<T> in(static_cast<const T *>(a.logits) + row * a.stride, a.dm.vocab);
+    float m, s;
+    warp_pieces<T>(in, i % per, per, n, raw, raw ? a.scores[row] : 0.f, room, m, s);
+    if (!raw) s = warp_sum(s);
+    if (lane == 0) sum[i] = make_float2(m, s);
+    for (int j = lane; j < n; j += 32) list[i * n + j] = room.best[j];
+    __syncwarp();
+  }
+  __syncthreads();
+  join_group(a, g, list, sum, per, join);
+}
+
+// `splits` blocks per row; each leaves its best entries and its part of the sum.
+template <class T>
+__global__ void __launch_bounds__(32 * kRowWarps) k_beam_rows(const BeamArgs a) {
+  __shared__ WarpRoom room[kRowWarps];
+  __shared__ uint64_t all[kRowWarps * kBeamMax];
+  __shared__ float2 sums[kRowWarps];
   __shared__ uint64_t bar;
-  __shared__ int found;
-  __shared__ float2 box[kRowThreads / 32];
-  const int n = a.dm.select, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  __shared__ int count;
+  const int n = a.dm.select, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const bool raw = a.dm.mode == RVQ_BEAM_RAW;
   const int64_t row = blockIdx.x / a.splits;
   const int split = (int)(blockIdx.x % a.splits);
   if (!beam_live(a, row)) return;
-  const RowVectors<T> in(static_cast<const T *>(a.logits) + row * a.stride, a.dm.vocab);
-  // pieces of whole steps, as even as they come
-  const int nv = in.count(), steps = (nv + kRowThreads * NV - 1) / (kRowThreads * NV);
-  const int s0 = (int)((int64_t)steps * split / a.splits), s1 = (int)((int64_t)steps * (split + 1) / a.splits);
-  const float add = raw ? a.scores[row] : 0.f;
-  float m = -CUDART_INF_F, s = 0.f;
-  if (tid < kBeamMax) best[tid] = 0;
-  if (tid == 0) found = 0, bar = 0;
-  for (int st = s0; st < s1; ++st) {
-    float f[NV][N];
-    uint64_t top = 0;
-    float high = -CUDART_INF_F;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int v = (st * NV + j) * kRowThreads + tid;
-      uint4 u = v < nv ? in.load(v, from_float<T>(-CUDART_INF_F)) : make_uint4(0, 0, 0, 0);
-      unpack16<T>(u, f[j]);
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        if (v >= nv) f[j][i] = -CUDART_INF_F;
-        if (raw) f[j][i] += add;
-        high = fmaxf(high, f[j][i]);
-        const uint64_t k = key_of(f[j][i], v * N + i - in.phase);
-        top = k > top ? k : top;
-      }
-    }
-    if (!raw) {
-      const float at = high == -CUDART_INF_F ? 0.f : high;
-      float t = 0.f;
-#pragma unroll
-      for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int i = 0; i < N; ++i) t += exp2_fast((f[j][i] - at) * kLog2e);
-      join_sum(m, s, high, t);
-    }
-    // The n-th best of the threads' best entries is a bar that n entries reach
-    // and that those of n threads at most can reach.
-    most[tid] = top;
-    __syncthreads();
-    int rank = 0;
-    for (int i = 0; i < kRowThreads; ++i) rank += most[i] > top;
-    const uint64_t held = best[n - 1];
-    if (rank == n - 1 && top > held) bar = top;  // one thread at most: keys differ, and 0 is not > held
-    __syncthreads();
-    const uint64_t line = bar > held ? bar : held + 1;
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const int v = (st * NV + j) * kRowThreads + tid;
-        const uint64_t k = key_of(f[j][i], v * N + i - in.phase);
-        if (k >= line) room[atomicAdd(&found, 1)] = k;
-      }
-    __syncthreads();
-    const int fresh = found, all = fresh + n;
-    if (tid < n) room[fresh + tid] = best[tid];
-    __syncthreads();
-    // each entry's place among them (empty ones, 0, have none)
-    for (int i = tid; i < all; i += kRowThreads) {
-      const uint64_t k = room[i];
-      if (!k) continue;
-      int place = 0;
-      for (int j = 0; j < all; ++j) place += room[j] > k;
-      if (place < n) best[place] = k;
-    }
-    __syncthreads();
-    if (tid == 0) found = 0, bar = 0;
+  const CutRow<T> in(static_cast<const T *>(a.logits) + row * a.stride, a.dm.vocab);
+  float m, s;
+  warp_pieces<T>(in, split * kRowWarps + warp, a.splits * kRowWarps, n, raw, raw ? a.scores[row] : 0.f, room[warp], m,
+                 s);
+  if (!raw) s = warp_sum(s);
+  if (lane == 0) sums[warp] = make_float2(m, s);
+  if (threadIdx.x == 0) bar = 0, count = 0;
+  __syncthreads();
+  // the best of the warps' last entries is a bar that n entries reach
+  if (threadIdx.x < kRowWarps && room[threadIdx.x].best[n - 1])
+    atomicMax(reinterpret_cast<unsigned long long *>(&bar), (unsigned long long)room[threadIdx.x].best[n - 1]);
+  __syncthreads();
+  for (int i = lane; i < n; i += 32) {
+    const uint64_t k = room[warp].best[i];
+    if (k && k >= bar) all[atomicAdd(&count, 1)] = k;
   }
   __syncthreads();
-  const int64_t at = row * a.splits + split;
-  if (tid < n) a.parts.list[at * n + tid] = best[tid];
-  if (raw) return;
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
-    join_sum(m, s, m2, s2);
+  const int c = count;
+  uint64_t *out = a.parts.list + blockIdx.x * (int64_t)n;
+  for (int i = threadIdx.x; i < c; i += blockDim.x) {
+    int place = 0;
+    for (int j = 0; j < c; ++j) place += all[j] > all[i];
+    if (place < n) out[place] = all[i];
   }
-  if (lane == 0) box[warp] = make_float2(m, s);
-  __syncthreads();
-  if (tid == 0) {
-    for (int w = 1; w < kRowThreads / 32; ++w) join_sum(m, s, box[w].x, box[w].y);
-    a.parts.sum[at] = make_float2(m, s);
+  for (int j = c + threadIdx.x; j < n; j += blockDim.x) out[j] = 0;
+  if (threadIdx.x == 0 && !raw) {
+    for (int w = 1; w < kRowWarps; ++w) join_sum(sums[0].x, sums[0].y, sums[w].x, sums[w].y);
+    a.parts.sum[blockIdx.x] = sums[0];
   }
 }
 
-// One warp per group.  A lane keeps the heads of the lists lane, lane + 32,
-// ...; the best head over the warp is chosen `select` times.
-constexpr int kGroupWarps = 4;
-
-struct Head {
-  uint32_t total;  // order_of the candidate's total; 0: none left
-  int32_t beam;
-  uint64_t key;    // its entry: value, then code
-};
-__device__ __forceinline__ bool better(const Head &x, const Head &y) {
-  if (x.total != y.total) return x.total > y.total;
-  if (x.beam != y.beam) return x.beam < y.beam;
-  return x.key > y.key;
-}
-
-__global__ void __launch_bounds__(32 * kGroupWarps) k_beam_groups(const BeamArgs a) {
-  __shared__ float2 lse[kGroupWarps][kBeamMax];  // of a row: m, log s
-  __shared__ uint8_t next[kGroupWarps][kBeamMax * kBeamMaxSplits];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t g = (int64_t)blockIdx.x * kGroupWarps + warp;
-  if (g >= a.dm.groups) return;
-  const int B = a.dm.beams, n = a.dm.select, S = a.splits, lists = B * S;
-  const bool raw = a.dm.mode == RVQ_BEAM_RAW;
-  for (int b = lane; b < B; b += 32) {
-    const int64_t row = g * B + b;
-    float m = 0.f, s = 1.f;
-    if (!raw && beam_live(a, row)) {
-      m = -CUDART_INF_F, s = 0.f;
-      for (int i = 0; i < S; ++i) join_sum(m, s, a.parts.sum[row * S + i].x, a.parts.sum[row * S + i].y);
-    }
-    lse[warp][b] = make_float2(m, logf(s));
-  }
-  for (int i = lane; i < lists; i += 32) next[warp][i] = 0;
-  __syncwarp();
-  auto head = [&](int list) {
-    const int b = list / S, at = next[warp][list];
-    const int64_t row = g * B + b;
-    Head h{0, b, 0};
-    const float score = a.scores[row];
-    if (!(score > -CUDART_INF_F) || at >= n) return h;
-    if (a.finished && a.finished[row]) {
-      if (list % S == 0 && at == 0) h.key = key_of(0.f, a.end_code), h.total = order_of(score);
-      return h;
-    }
-    h.key = a.parts.list[(row * S + list % S) * n + at];
-    if (h.key) {
-      const float v = value_of((uint32_t)(h.key >> 32));
-      h.total = order_of(raw ? v : score + ((v - lse[warp][b].x) - lse[warp][b].y));
-    }
-    return h;
-  };
-  Head mine{0, 0, 0};
-  int from = -1;
-  auto look = [&]() {
-    mine.total = 0;
-    from = -1;
-    for (int i = lane; i < lists; i += 32) {
-      const Head h = head(i);
-      if (h.total && (from < 0 || better(h, mine))) mine = h, from = i;
-    }
-  };
-  look();
-  for (int j = 0; j < n; ++j) {
-    const uint32_t total = __reduce_max_sync(0xffffffffu, mine.total);
-    bool in = mine.total == total && total;
-    const uint32_t beam = __reduce_min_sync(0xffffffffu, in ? (uint32_t)mine.beam : ~0u);
-    in = in && (uint32_t)mine.beam == beam;
-    const uint32_t hi = __reduce_max_sync(0xffffffffu, in ? (uint32_t)(mine.key >> 32) : 0u);
-    in = in && (uint32_t)(mine.key >> 32) == hi;
-    const uint32_t lo = __reduce_max_sync(0xffffffffu, in ? (uint32_t)mine.key : 0u);
-    in = in && (uint32_t)mine.key == lo;
-    const int64_t o = g * n + j;
-    if (total == 0) {
-      if (lane == 0) {
-        a.out_scores[o] = -CUDART_INF_F;
-        a.parents[o] = a.codes[o] = -1;
-        if (a.out_finished) a.out_finished[o] = 1;
-      }
-    } else if (in) {
-      const int code = (int)~(uint32_t)mine.key;
-      a.out_scores[o] = value_of(mine.total);
-      a.parents[o] = mine.beam;
-      a.codes[o] = code;
-      if (a.out_finished)
-        a.out_finished[o] = (a.finished && a.finished[g * B + mine.beam]) || code == a.end_code;
-      ++next[warp][from];
-      look();
-    }
-  }
+__global__ void __launch_bounds__(256) k_beam_join(const BeamArgs a) {
+  extern __shared__ uint64_t smem[];
+  __shared__ Join join;
+  const int lists = a.dm.beams * a.splits, n = a.dm.select;
+  const int64_t g = blockIdx.x;
+  float2 *sum = reinterpret_cast<float2 *>(smem + (size_t)lists * n);
+  // (dead and finished beams' entries are never written: join_group replaces them)
+  for (int i = threadIdx.x; i < lists * n; i += blockDim.x) smem[i] = a.parts.list[g * lists * n + i];
+  for (int i = threadIdx.x; i < lists; i += blockDim.x) sum[i] = a.parts.sum[g * lists + i];
+  __syncthreads();
+  join_group(a, g, smem, sum, a.splits, join);
 }
 
 // ---------------------------------------------------------------------------
@@ -331,21 +478,66 @@ rvq_status check_beam(const rvq_beam_dims &dm) {
   if (dm.groups < 0 || dm.beams <= 0 || dm.vocab <= 0 || dm.select <= 0 || !dtype_bytes(dm.dtype)) return RVQ_ERR_INVALID_ARG;
   if (dm.mode != RVQ_BEAM_LOGITS && dm.mode != RVQ_BEAM_RAW) return RVQ_ERR_INVALID_ARG;
   if (dm.beams > kBeamMax || dm.select > kBeamMax || dm.vocab > kBeamMaxVocab) return RVQ_ERR_UNSUPPORTED;
-  if (dm.groups > (int64_t)(1 << 30) / (dm.beams * kBeamMaxSplits)) return RVQ_ERR_UNSUPPORTED;
+  if (dm.groups > (int64_t)(1 << 30) / kMaxLists) return RVQ_ERR_UNSUPPORTED;
   return RVQ_OK;
 }
 
-// Pieces of a row: enough blocks for the GPU, no piece below one step.
-int beam_splits(const rvq_beam_dims &dm) {
-  const int64_t rows = dm.groups * dm.beams, steps = (dm.vocab + kRowStep - 1) / kRowStep;
-  int64_t s = rows > 0 ? (152 * 4 + rows - 1) / rows : 1;
-  if (s > steps) s = steps;
-  if (s > kBeamMaxSplits) s = kBeamMaxSplits;
-  return (int)s;
+// How a call runs.  A group of at most kGroupItems pieces: one block, `splits`
+// warps a row.  Else `splits` blocks a row: as many as fill the GPU twice, none
+// without a piece for each of its warps.
+struct BeamPlan {
+  bool group;
+  int splits, warps;
+  size_t smem;
+};
+BeamPlan beam_plan(const rvq_beam_dims &dm) {
+  // whole vectors alone make pieces: the elements beside them go with the first
+  const int vec = 16 / dtype_bytes(dm.dtype), each = 32 * kLane / vec, full = dm.vocab / vec;
+  const int pieces = full > each ? (full + each - 1) / each : 1;
+  BeamPlan p{};
+  p.group = (int64_t)dm.beams * pieces <= kGroupItems;
+  if (p.group) {
+    const int per = kGroupWarps / dm.beams;
+    p.splits = per < 1 ? 1 : per > pieces ? pieces : per;
+    p.warps = dm.beams * p.splits < kGroupWarps ? dm.beams * p.splits : kGroupWarps;
+    p.smem = (size_t)dm.beams * p.splits * (dm.select * 8 + sizeof(float2)) + p.warps * sizeof(WarpRoom);
+    return p;
+  }
+  const int64_t rows = dm.groups * dm.beams;
+  int64_t s = rows > 0 ? (2 * 152 + rows - 1) / rows : 1;
+  const int most = (pieces + kRowWarps - 1) / kRowWarps;
+  s = s > most ? most : s;
+  s = s > kMaxLists / dm.beams ? kMaxLists / dm.beams : s;
+  p.splits = (int)s;
+  p.warps = kRowWarps;
+  p.smem = (size_t)dm.beams * p.splits * (dm.select * 8 + sizeof(float2));
+  return p;
 }
 
-size_t beam_list_at(const rvq_beam_dims &dm) {
-  return align_up((size_t)(dm.groups * dm.beams) * beam_splits(dm) * sizeof(float2));
+size_t beam_list_at(const rvq_beam_dims &dm, int splits) {
+  return align_up((size_t)(dm.groups * dm.beams) * splits * sizeof(float2));
+}
+
+template <class K>
+cudaError_t beam_smem(K kernel, size_t bytes) {
+  return bytes <= 24 * 1024 ? cudaSuccess
+                            : cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
+template <class T>
+cudaError_t launch_beam(const BeamArgs &a, const BeamPlan &p, cudaStream_t st) {
+  if (p.group) {
+    const cudaError_t e = beam_smem(k_beam_group<T>, p.smem);
+    if (e != cudaSuccess) return e;
+    k_beam_group<T><<<(unsigned)a.dm.groups, 32 * p.warps, p.smem, st>>>(a);
+    return cudaGetLastError();
+  }
+  k_beam_rows<T><<<(unsigned)(a.dm.groups * a.dm.beams * p.splits), 32 * kRowWarps, 0, st>>>(a);
+  cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) e = beam_smem(k_beam_join, p.smem);
+  if (e != cudaSuccess) return e;
+  k_beam_join<<<(unsigned)a.dm.groups, 256, p.smem, st>>>(a);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -356,8 +548,9 @@ extern "C" {
 RVQ_API size_t rvq_beam_workspace_bytes(rvq_beam_dims dims) {
   using namespace rvq;
   if (check_beam(dims) != RVQ_OK) return 0;
-  return beam_list_at(dims) +
-         align_up(((size_t)(dims.groups * dims.beams) + (dims.groups == 0)) * beam_splits(dims) * dims.select * 8);
+  const BeamPlan p = beam_plan(dims);
+  if (p.group || dims.groups == 0) return kAlign;  // nothing but the size's own sign that the dims are supported
+  return beam_list_at(dims, p.splits) + align_up((size_t)(dims.groups * dims.beams) * p.splits * dims.select * 8);
 }
 
 RVQ_API rvq_status rvq_beam_select(rvq_beam_dims dims, const void *logits, int64_t logits_stride, const float *scores,
@@ -375,19 +568,14 @@ RVQ_API rvq_status rvq_beam_select(rvq_beam_dims dims, const void *logits, int64
     return RVQ_ERR_INVALID_ARG;
   if (logits_stride < dims.vocab && dims.groups * dims.beams > 1) return RVQ_ERR_INVALID_ARG;
   if (workspace_bytes < rvq_beam_workspace_bytes(dims)) return RVQ_ERR_INVALID_ARG;
-  BeamArgs a{dims, logits, logits_stride, scores, finished, end_code, out_scores, parents, codes, out_finished,
-             beam_splits(dims), {at<float2>(workspace, 0), at<uint64_t>(workspace, beam_list_at(dims))}};
+  const BeamPlan p = beam_plan(dims);
+  const BeamArgs a{dims, logits, logits_stride, scores, finished, end_code, out_scores, parents, codes, out_finished,
+                   p.splits, {at<float2>(workspace, 0), at<uint64_t>(workspace, beam_list_at(dims, p.splits))}};
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const unsigned blocks = (unsigned)(dims.groups * dims.beams * a.splits);
-  if (dims.dtype == RVQ_DTYPE_F32)
-    k_beam_rows<float><<<blocks, kRowThreads, 0, st>>>(a);
-  else if (dims.dtype == RVQ_DTYPE_BF16)
-    k_beam_rows<__nv_bfloat16><<<blocks, kRowThreads, 0, st>>>(a);
-  else
-    k_beam_rows<__half><<<blocks, kRowThreads, 0, st>>>(a);
-  if (cudaGetLastError() != cudaSuccess) return RVQ_ERR_CUDA;
-  k_beam_groups<<<(unsigned)((dims.groups + kGroupWarps - 1) / kGroupWarps), 32 * kGroupWarps, 0, st>>>(a);
-  return cudaGetLastError() == cudaSuccess ? RVQ_OK : RVQ_ERR_CUDA;
+  const cudaError_t e = dims.dtype == RVQ_DTYPE_F32    ? launch_beam<float>(a, p, st)
+                        : dims.dtype == RVQ_DTYPE_BF16 ? launch_beam<__nv_bfloat16>(a, p, st)
+                                                       : launch_beam<__half>(a, p, st);
+  return e == cudaSuccess ? RVQ_OK : RVQ_ERR_CUDA;
 }
 
 RVQ_API rvq_status rvq_beam_reorder(rvq_beam_dims dims, const int32_t *parents, const rvq_beam_state *states,

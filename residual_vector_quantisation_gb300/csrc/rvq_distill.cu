@@ -59,33 +59,19 @@ __device__ __forceinline__ Sum warp_join(Sum v, float c) {
   return v;
 }
 
-// A row cut at 16-byte boundaries: `head` elements before the first, `full`
-// vectors, `tail` elements after the last.  The head and tail elements (under
-// N each) belong to 2 N threads, one each; so no vector needs a check.
-// Element e has place e - head + 8: a vector's places start at a multiple of N.
+// A row of logits and where its gradient goes.  Element e has place e - head +
+// 8: a vector's places start at a multiple of N.
 template <class T>
-struct Row {
-  static constexpr int N = 16 / (int)sizeof(T);
-  const T *z;
-  T *d;  // null: no gradient wanted
-  int width, head, full, tail;
+struct Row : CutRow<T> {
+  using CutRow<T>::N, CutRow<T>::z, CutRow<T>::head;
+  T *d;       // null: no gradient wanted
   bool same;  // z and d start equally far from a boundary
   __device__ __forceinline__ Row(const DistillArgs &a, int64_t row)
-      : z(static_cast<const T *>(a.logits) + row * a.logits_stride),
-        d(a.dlogits ? static_cast<T *>(a.dlogits) + row * a.dlogits_stride : nullptr),
-        width(a.dm.vocab) {
-    const int past = (int)(reinterpret_cast<uintptr_t>(z) & 15) / (int)sizeof(T);
-    head = min(width, past ? N - past : 0);
-    full = (width - head) / N;
-    tail = width - head - full * N;
+      : CutRow<T>(static_cast<const T *>(a.logits) + row * a.logits_stride, a.dm.vocab),
+        d(a.dlogits ? static_cast<T *>(a.dlogits) + row * a.dlogits_stride : nullptr) {
     same = ((reinterpret_cast<uintptr_t>(z) ^ reinterpret_cast<uintptr_t>(d)) & 15) == 0;
   }
-  __device__ __forceinline__ uint4 vector(int v) const { return *reinterpret_cast<const uint4 *>(z + head + v * N); }
   __device__ __forceinline__ int place(int e) const { return e - head + 8; }
-  // the element that thread t holds beside its vectors (-1: none)
-  __device__ __forceinline__ int edge(int t) const {
-    return t < head ? t : t >= N && t < N + tail ? head + full * N + t - N : -1;
-  }
   __device__ __forceinline__ void put(int v, const float (&f)[N]) const {
     T *at = d + head + v * N;
     if (same) {
@@ -262,11 +248,6 @@ struct Power {
   __device__ __forceinline__ float operator()(float z) const { return exp2_fast((z - m) * c); }
 };
 
-template <class T>
-__device__ __forceinline__ uint4 all_low() {  // a vector of -inf
-  const uint32_t w = sizeof(T) == 4 ? 0xff800000u : std::is_same<T, __half>::value ? 0xfc00fc00u : 0xff80ff80u;
-  return make_uint4(w, w, w, w);
-}
 template <class T>
 __device__ __forceinline__ float largest(const uint4 &v, float m) {
   float f[16 / sizeof(T)];

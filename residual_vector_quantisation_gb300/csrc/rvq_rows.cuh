@@ -77,47 +77,32 @@ __device__ __forceinline__ uint4 pack16(const float (&f)[16 / sizeof(T)]) {
   return v;
 }
 
-// A row that may start anywhere: its elements seen as 16-byte vectors from the
-// boundary at or below its start.  Element e of the row is place phase + e;
-// vector v holds the places [v * N, v * N + N).
+// A row cut at 16-byte boundaries: `head` elements before the first, `full`
+// vectors, `tail` elements after the last.  The head and tail elements (under
+// N each) go to 2 N threads, one each, so that no vector needs a check.
 template <class T>
-struct RowVectors {
+struct CutRow {
   static constexpr int N = 16 / (int)sizeof(T);
-  uintptr_t at;  // address of place 0 (never dereferenced outside the row)
-  int phase, width;
-  __device__ __forceinline__ RowVectors(const T *row, int width_) : width(width_) {
-    const uintptr_t a = reinterpret_cast<uintptr_t>(row);
-    phase = (int)(a & 15) / (int)sizeof(T);
-    at = a - (a & 15);
+  const T *z;
+  int width, head, full, tail;
+  __device__ __forceinline__ CutRow(const T *row, int width_) : z(row), width(width_) {
+    const int past = (int)(reinterpret_cast<uintptr_t>(z) & 15) / (int)sizeof(T);
+    head = min(width, past ? N - past : 0);
+    full = (width - head) / N;
+    tail = width - head - full * N;
   }
-  __device__ __forceinline__ int count() const { return (phase + width + N - 1) / N; }
-  __device__ __forceinline__ bool inside(int v) const { return v * N >= phase && (v + 1) * N <= phase + width; }
-  // Vector v; places outside the row read as `fill`.
-  __device__ __forceinline__ uint4 load(int v, T fill) const {
-    if (inside(v)) return *reinterpret_cast<const uint4 *>(at + (uintptr_t)v * 16);
-    union {
-      uint4 u;
-      T t[N];
-    } r;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int p = v * N + i;
-      r.t[i] = p >= phase && p < phase + width ? reinterpret_cast<const T *>(at)[p] : fill;
-    }
-    return r.u;
-  }
-  __device__ __forceinline__ void store(int v, const float (&f)[N]) const {
-    if (inside(v)) {
-      *reinterpret_cast<uint4 *>(at + (uintptr_t)v * 16) = pack16<T>(f);
-      return;
-    }
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int p = v * N + i;
-      if (p >= phase && p < phase + width) reinterpret_cast<T *>(at)[p] = from_float<T>(f[i]);
-    }
+  __device__ __forceinline__ uint4 vector(int v) const { return *reinterpret_cast<const uint4 *>(z + head + v * N); }
+  // the element that thread t holds beside its vectors (-1: none)
+  __device__ __forceinline__ int edge(int t) const {
+    return t < head ? t : t >= N && t < N + tail ? head + full * N + t - N : -1;
   }
 };
+
+template <class T>
+__device__ __forceinline__ uint4 all_low() {  // a vector of -inf
+  const uint32_t w = sizeof(T) == 4 ? 0xff800000u : std::is_same<T, __half>::value ? 0xfc00fc00u : 0xff80ff80u;
+  return make_uint4(w, w, w, w);
+}
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
