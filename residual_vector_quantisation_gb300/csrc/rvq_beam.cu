@@ -21,7 +21,8 @@ constexpr int kRowWarps = 8;           // of a block that shares a row
 constexpr int kGroupWarps = 16;        // most warps of a block that takes a group
 constexpr int kGroupItems = 64;        // most pieces of such a group
 constexpr int kMaxLists = 128;         // most lists that a group's join reads
-constexpr int kLane = 32;              // elements of a lane in a piece
+constexpr int kLane = 32;              // elements of a lane in a piece of a group's block
+constexpr int kRowVectors = 16;        // 16-byte vectors of a lane in a piece of a block that shares a row
 constexpr int kRoom = 128;             // entries that a warp puts in order at once, beside those it holds
 
 // An entry's place in the order: the larger value first, then the lower code.
@@ -78,9 +79,19 @@ struct WarpRoom {
   int count;
 };
 
-// Lane l gets the (l + 1)-th largest of the lanes' values.
-__device__ __forceinline__ uint32_t warp_sorted(uint32_t v) {
+// The n-th largest of the lanes' values (n <= 32): for few by taking the
+// largest away, else by sorting (15 exchanges).
+__device__ __forceinline__ uint32_t warp_nth(uint32_t v, int n) {
   const int lane = threadIdx.x & 31;
+  if (n <= 8) {
+    uint32_t top = 0;
+    for (int i = 0; i < n; ++i) {
+      top = __reduce_max_sync(0xffffffffu, v);
+      const unsigned at = __ballot_sync(0xffffffffu, v == top);
+      if (lane == __ffs(at) - 1) v = 0;
+    }
+    return top;
+  }
 #pragma unroll
   for (int k = 2; k <= 32; k *= 2)
 #pragma unroll
@@ -89,15 +100,16 @@ __device__ __forceinline__ uint32_t warp_sorted(uint32_t v) {
       const bool high = ((lane & k) == 0) == ((lane & j) == 0);
       v = high ? max(v, o) : min(v, o);
     }
-  return v;
+  return __shfl_sync(0xffffffffu, v, n - 1);
 }
 
-// The pieces `first`, `first` + `step`, ... of a row: the best n entries in
-// order in r.best (0: none), and the sum of e^z as (m, s), s of this lane alone.
-template <class T>
+// The pieces `first`, `first` + `step`, ... of a row, NV vectors a lane each:
+// the best n entries in order in r.best (0: none), and the sum of e^z as
+// (m, s), s of this lane alone.
+template <class T, int NV>
 __device__ __forceinline__ void warp_pieces(const CutRow<T> &in, int first, int step, int n, bool raw, float add,
                                             WarpRoom &r, float &m, float &s) {
-  constexpr int N = 16 / (int)sizeof(T), NV = kLane / N;
+  constexpr int N = 16 / (int)sizeof(T);
   const int lane = threadIdx.x & 31;
   for (int i = lane; i < kBeamMax; i += 32) r.best[i] = 0;
   if (lane == 0) r.count = 0;
@@ -105,36 +117,36 @@ __device__ __forceinline__ void warp_pieces(const CutRow<T> &in, int first, int 
   __syncwarp();
   bool held = false;
   for (int p = first; p == 0 || p * NV * 32 < in.full; p += step) {
-    float z[NV][N];
-    uint4 raw4[NV];
+    uint4 z[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int v = (p * NV + j) * 32 + lane;
-      raw4[j] = v < in.full ? in.vector(v) : all_low<T>();
+      z[j] = v < in.full ? in.vector(v) : all_low<T>();
     }
     const int edge_at = p == 0 ? in.edge(lane) : -1;
-    float edge = edge_at >= 0 ? to_float(in.z[edge_at]) : -CUDART_INF_F;
-    float half[2] = {-CUDART_INF_F, -CUDART_INF_F};  // the largest of each half of the lane's elements
+    const float edge = edge_at >= 0 ? to_float(in.z[edge_at]) + add : -CUDART_INF_F;
+    // each vector's largest, and the largest of each half of the lane's elements (z + add: add is 0 where the sum
+    // is wanted).  Once the sum is taken the vectors are done with: the few that hold an entry worth ordering are
+    // read again, by their lanes at the same time.
+    float most[NV], half[2] = {-CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      unpack16<T>(raw4[j], z[j]);
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        if (raw) z[j][i] += add;
-        half[j * N >= kLane / 2] = fmaxf(half[j * N >= kLane / 2], z[j][i]);
-      }
+      most[j] = largest_of<T>(z[j]) + add;
+      half[j >= NV / 2] = fmaxf(half[j >= NV / 2], most[j]);
     }
-    if (raw) edge += add;
     half[0] = fmaxf(half[0], edge);
     const float high = fmaxf(half[0], half[1]);
     if (!raw) {
-      const float most = fmaxf(m, warp_max_order(high)), at = most == -CUDART_INF_F ? 0.f : most;
+      const float top = fmaxf(m, warp_max_order(high)), at = top == -CUDART_INF_F ? 0.f : top;
       s *= exp2_fast((m - at) * kLog2e);
-      m = most;
+      m = top;
 #pragma unroll
-      for (int j = 0; j < NV; ++j)
+      for (int j = 0; j < NV; ++j) {
+        float f[N];
+        unpack16<T>(z[j], f);
 #pragma unroll
-        for (int i = 0; i < N; ++i) s += exp2_fast((z[j][i] - at) * kLog2e);
+        for (int i = 0; i < N; ++i) s += exp2_fast((f[i] - at) * kLog2e);
+      }
       s += exp2_fast((edge - at) * kLog2e);
     }
     const uint64_t last = held ? r.best[n - 1] : 0;  // an entry counts if it is above this
@@ -142,52 +154,55 @@ __device__ __forceinline__ void warp_pieces(const CutRow<T> &in, int first, int 
     if (!__any_sync(0xffffffffu, order_of(high) > 0 && order_of(high) >= last_value)) continue;
     uint32_t bar;
     if (n <= 32) {
-      bar = __shfl_sync(0xffffffffu, warp_sorted(order_of(high)), n - 1);
+      bar = warp_nth(order_of(high), n);
     } else {
-      const int at = (n + 1) / 2 - 1;
-      bar = min(__shfl_sync(0xffffffffu, warp_sorted(order_of(half[0])), at),
-                __shfl_sync(0xffffffffu, warp_sorted(order_of(half[1])), at));
+      const int at = (n + 1) / 2;
+      bar = min(warp_nth(order_of(half[0]), at), warp_nth(order_of(half[1]), at));
     }
     bar = max(bar, last_value);
     const float line = bar ? value_of(bar) : -3.402823466e38f;
-    int mine = edge >= line;
+    auto offer = [&](float v, int code) {
+      const uint64_t k = key_of(v, code);
+      if (k <= last) return;
+      const int at = atomicAdd(&r.count, 1);
+      if (at < kRoom) r.room[at] = k;
+    };
+    uint32_t wanted = 0;
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
+    for (int j = 0; j < NV; ++j) wanted |= (uint32_t)(most[j] >= line) << j;
+    if (edge >= line) offer(edge, edge_at);
+    while (wanted) {
+      const int v = (p * NV + __ffs(wanted) - 1) * 32 + lane;
+      wanted &= wanted - 1;
+      float f[N];
+      unpack16<T>(in.vector(v), f);
 #pragma unroll
-      for (int i = 0; i < N; ++i) mine += z[j][i] >= line;
-    const int reach = __reduce_add_sync(0xffffffffu, mine);
-    if (reach <= kRoom) {
-      if (mine) {
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-#pragma unroll
-          for (int i = 0; i < N; ++i)
-            if (z[j][i] >= line) {
-              const uint64_t k = key_of(z[j][i], in.head + ((p * NV + j) * 32 + lane) * N + i);
-              if (k > last) r.room[atomicAdd(&r.count, 1)] = k;
-            }
-        if (edge >= line) {
-          const uint64_t k = key_of(edge, edge_at);
-          if (k > last) r.room[atomicAdd(&r.count, 1)] = k;
-        }
-      }
-    } else {
+      for (int i = 0; i < N; ++i)
+        if (f[i] + add >= line) offer(f[i] + add, in.head + v * N + i);
+    }
+    __syncwarp();
+    if (r.count > kRoom) {
       // many equal values at the bar: the best n one after the other
+      __syncwarp();
       uint64_t below = ~0ull;
       for (int c = 0; c < n; ++c) {
-        uint64_t k = 0;
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
+        uint64_t k = key_of(edge, edge_at);
+        if (k >= below) k = 0;
+        for (int j = 0; j < NV; ++j) {
+          const int v = (p * NV + j) * 32 + lane;
+          if (v >= in.full) break;
+          float f[N];
+          unpack16<T>(in.vector(v), f);
 #pragma unroll
           for (int i = 0; i < N; ++i) {
-            const uint64_t e = key_of(z[j][i], in.head + ((p * NV + j) * 32 + lane) * N + i);
+            const uint64_t e = key_of(f[i] + add, in.head + v * N + i);
             if (e < below && e > k) k = e;
           }
-        const uint64_t e = key_of(edge, edge_at);
-        if (e < below && e > k) k = e;
+        }
         const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(k >> 32));
         const uint32_t lo = __reduce_max_sync(0xffffffffu, (uint32_t)(k >> 32) == hi ? (uint32_t)k : 0u);
         below = (uint64_t)hi << 32 | lo;
+        if (lane == 0 && c == 0) r.count = 0;
         if (below <= last) break;
         if (lane == 0) r.room[c] = below, r.count = c + 1;
       }
@@ -229,8 +244,56 @@ __device__ __forceinline__ uint32_t total_of(const BeamArgs &a, const Join &w, f
   return order_of(a.dm.mode == RVQ_BEAM_RAW ? v : score + ((v - w.lse[beam].x) - w.lse[beam].y));
 }
 
+__device__ __forceinline__ void put_candidate(const BeamArgs &a, int64_t g, int place, uint32_t total, int beam,
+                                              int code) {
+  const int64_t o = g * a.dm.select + place;
+  a.out_scores[o] = total ? value_of(total) : -CUDART_INF_F;
+  a.parents[o] = total ? beam : -1;
+  a.codes[o] = total ? code : -1;
+  if (a.out_finished)
+    a.out_finished[o] = !total || (a.finished && a.finished[g * a.dm.beams + beam]) || code == a.end_code;
+}
+
+// At most 32 entries: a lane of the first warp has one each.
+__device__ __forceinline__ void join_in_warp(const BeamArgs &a, int64_t g, const uint64_t *list, const float2 *sum,
+                                             int per) {
+  const int n = a.dm.select, lane = threadIdx.x & 31, entries = a.dm.beams * per * n;
+  if (threadIdx.x >= 32) return;
+  uint32_t total = 0;
+  uint64_t key = 0;
+  const int b = lane / n / per;
+  if (lane < entries) {
+    const int64_t row = g * a.dm.beams + b;
+    const float score = a.scores[row];
+    if (beam_live(a, row)) {
+      key = list[lane];
+      const float v = value_of((uint32_t)(key >> 32));
+      if (a.dm.mode == RVQ_BEAM_RAW) {
+        total = (uint32_t)(key >> 32);
+      } else if (key) {
+        float m = -CUDART_INF_F, s = 0.f;
+        for (int i = 0; i < per; ++i) join_sum(m, s, sum[b * per + i].x, sum[b * per + i].y);
+        total = order_of(score + ((v - m) - logf(s)));
+      }
+    } else if (lane % (per * n) == 0 && score > -CUDART_INF_F) {
+      key = key_of(0.f, a.end_code), total = order_of(score);
+    }
+  }
+  const uint64_t mine = (uint64_t)total << 32 | (uint32_t)~b;
+  int place = 0;
+  for (int i = 0; i < entries; ++i) {
+    const uint64_t k = __shfl_sync(0xffffffffu, mine, i), t = __shfl_sync(0xffffffffu, key, i);
+    place += k > mine || (k == mine && t > key);
+  }
+  const int found = __popc(__ballot_sync(0xffffffffu, total != 0));
+  if (total && place < n) put_candidate(a, g, place, total, b, (int)~(uint32_t)key);
+  if (lane >= found && lane < n) put_candidate(a, g, lane, 0, 0, 0);
+  for (int i = lane + 32; i < n; i += 32) put_candidate(a, g, i, 0, 0, 0);
+}
+
 __device__ void join_group(const BeamArgs &a, int64_t g, uint64_t *list, const float2 *sum, int per, Join &w) {
   const int B = a.dm.beams, n = a.dm.select, lists = B * per, tid = threadIdx.x, lane = tid & 31;
+  if (lists * n <= 32) return join_in_warp(a, g, list, sum, per);
   for (int b = tid; b < B; b += blockDim.x) {
     const int64_t row = g * B + b;
     float m = 0.f, s = 1.f;
@@ -277,12 +340,7 @@ __device__ void join_group(const BeamArgs &a, int64_t g, uint64_t *list, const f
   __syncthreads();
   const int all = w.count;
   auto put = [&](int place, uint64_t k, uint64_t tie) {
-    const int64_t o = g * n + place;
-    const int beam = (int)~(uint32_t)k, code = (int)~(uint32_t)tie;
-    a.out_scores[o] = value_of((uint32_t)(k >> 32));
-    a.parents[o] = beam;
-    a.codes[o] = code;
-    if (a.out_finished) a.out_finished[o] = (a.finished && a.finished[g * B + beam]) || code == a.end_code;
+    put_candidate(a, g, place, (uint32_t)(k >> 32), (int)~(uint32_t)k, (int)~(uint32_t)tie);
   };
   int found = min(all, n);
   if (all <= kTop) {
@@ -312,12 +370,7 @@ __device__ void join_group(const BeamArgs &a, int64_t g, uint64_t *list, const f
       k0 = k, t0 = t;
     }
   }
-  for (int j = found + tid; j < n; j += blockDim.x) {
-    const int64_t o = g * n + j;
-    a.out_scores[o] = -CUDART_INF_F;
-    a.parents[o] = a.codes[o] = -1;
-    if (a.out_finished) a.out_finished[o] = 1;
-  }
+  for (int j = found + tid; j < n; j += blockDim.x) put_candidate(a, g, j, 0, 0, 0);
 }
 
 // A block per group: `per` warps' shares of each beam's row, then the join.
@@ -336,7 +389,7 @@ __global__ void __launch_bounds__(32 * kGroupWarps) k_beam_group(const BeamArgs 
     if (!beam_live(a, row)) continue;
     const CutRow<T> in(static_cast<const T *>(a.logits) + row * a.stride, a.dm.vocab);
     float m, s;
-    warp_pieces<T>(in, i % per, per, n, raw, raw ? a.scores[row] : 0.f, room, m, s);
+    warp_pieces<T, kLane * (int)sizeof(T) / 16>(in, i % per, per, n, raw, raw ? a.scores[row] : 0.f, room, m, s);
     if (!raw) s = warp_sum(s);
     if (lane == 0) sum[i] = make_float2(m, s);
     for (int j = lane; j < n; j += 32) list[i * n + j] = room.best[j];
@@ -361,8 +414,8 @@ __global__ void __launch_bounds__(32 * kRowWarps) k_beam_rows(const BeamArgs a) 
   if (!beam_live(a, row)) return;
   const CutRow<T> in(static_cast<const T *>(a.logits) + row * a.stride, a.dm.vocab);
   float m, s;
-  warp_pieces<T>(in, split * kRowWarps + warp, a.splits * kRowWarps, n, raw, raw ? a.scores[row] : 0.f, room[warp], m,
-                 s);
+  warp_pieces<T, kRowVectors>(in, split * kRowWarps + warp, a.splits * kRowWarps, n, raw, raw ? a.scores[row] : 0.f,
+                              room[warp], m, s);
   if (!raw) s = warp_sum(s);
   if (lane == 0) sums[warp] = make_float2(m, s);
   if (threadIdx.x == 0) bar = 0, count = 0;
@@ -411,30 +464,69 @@ struct StateList {
   rvq_beam_state s[RVQ_BEAM_MAX_STATES];
 };
 
-// One block per (layer, group, slot) and piece of the row, states on grid.z.
-constexpr int kMoveThreads = 256;
+// A block per (layer, group) and piece of the row, all slots of the group: a
+// parent that several slots have is read from memory once.  W: the widest word
+// that the state's addresses allow; `pieces` of `words` words a row.
+constexpr int kMoveThreads = 256, kMoveDepth = 4;
+template <class W>
+__device__ __forceinline__ void move_rows(const rvq_beam_state &s, const int32_t *parents, int64_t layer, int64_t g,
+                                          int beams, int select, int64_t piece, int piece_words) {
+  const int64_t words = s.row_bytes / (int64_t)sizeof(W), w0 = piece * piece_words;
+  if (w0 >= words) return;
+  const uint32_t here = (uint32_t)min((int64_t)piece_words, words - w0), all = here * (uint32_t)select;
+  const char *src = static_cast<const char *>(s.src) + layer * s.src_layer_stride + g * s.src_group_stride + w0 * sizeof(W);
+  char *dst = static_cast<char *>(s.dst) + layer * s.dst_layer_stride + g * s.dst_group_stride + w0 * sizeof(W);
+  for (uint32_t i0 = threadIdx.x; i0 < all; i0 += kMoveThreads * kMoveDepth) {
+    W v[kMoveDepth];
+#pragma unroll
+    for (int k = 0; k < kMoveDepth; ++k) {
+      const uint32_t i = i0 + k * kMoveThreads;
+      v[k] = W{};
+      if (i < all) {
+        const uint32_t j = i / here;
+        const int p = parents[g * select + j];
+        if (p >= 0 && p < beams) v[k] = reinterpret_cast<const W *>(src + p * s.src_beam_stride)[i - j * here];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kMoveDepth; ++k) {
+      const uint32_t i = i0 + k * kMoveThreads;
+      if (i < all) {
+        const uint32_t j = i / here;
+        reinterpret_cast<W *>(dst + j * s.dst_beam_stride)[i - j * here] = v[k];
+      }
+    }
+  }
+}
+
+__host__ __device__ inline int state_word(const rvq_beam_state &s) {
+  const uintptr_t all = reinterpret_cast<uintptr_t>(s.src) | reinterpret_cast<uintptr_t>(s.dst) | (uintptr_t)s.row_bytes |
+                        (uintptr_t)s.src_layer_stride | (uintptr_t)s.src_group_stride | (uintptr_t)s.src_beam_stride |
+                        (uintptr_t)s.dst_layer_stride | (uintptr_t)s.dst_group_stride | (uintptr_t)s.dst_beam_stride;
+  return (all & 15) == 0 ? 16 : (all & 3) == 0 ? 4 : 1;
+}
+// Words of a row that a block moves for each slot, and pieces of a row.
+inline int move_words(int select) {
+  const int w = kMoveThreads * kMoveDepth / select;
+  return w < 32 ? 32 : w;
+}
+
 __global__ void __launch_bounds__(kMoveThreads)
     k_beam_reorder(const __grid_constant__ StateList list, const int32_t *__restrict__ parents, int64_t groups,
-                   int beams, int select) {
-  const rvq_beam_state s = list.s[blockIdx.z];
-  const int64_t slots = s.layers * groups * select;
-  for (int64_t i = blockIdx.x; i < slots; i += gridDim.x) {
-    const int64_t layer = i / (groups * select), gs = i % (groups * select), g = gs / select;
-    const int j = (int)(gs % select), p = parents[gs];
-    const char *src = static_cast<const char *>(s.src) + layer * s.src_layer_stride + g * s.src_group_stride +
-                      (p >= 0 && p < beams ? p : 0) * s.src_beam_stride;
-    char *dst = static_cast<char *>(s.dst) + layer * s.dst_layer_stride + g * s.dst_group_stride + j * s.dst_beam_stride;
-    const bool none = p < 0 || p >= beams;
-    const uintptr_t both = reinterpret_cast<uintptr_t>(src) | reinterpret_cast<uintptr_t>(dst) | (uintptr_t)s.row_bytes;
-    const int64_t t = (int64_t)blockIdx.y * kMoveThreads + threadIdx.x, step = (int64_t)gridDim.y * kMoveThreads;
-    if ((both & 15) == 0) {
-      for (int64_t k = t; k < s.row_bytes / 16; k += step)
-        reinterpret_cast<uint4 *>(dst)[k] = none ? make_uint4(0, 0, 0, 0) : reinterpret_cast<const uint4 *>(src)[k];
-    } else if ((both & 3) == 0) {
-      for (int64_t k = t; k < s.row_bytes / 4; k += step)
-        reinterpret_cast<uint32_t *>(dst)[k] = none ? 0u : reinterpret_cast<const uint32_t *>(src)[k];
-    } else {
-      for (int64_t k = t; k < s.row_bytes; k += step) dst[k] = none ? 0 : src[k];
+                   int beams, int select, int piece_words) {
+  const rvq_beam_state &s = list.s[blockIdx.z];
+  const int word = state_word(s);
+  const int64_t pieces = (s.row_bytes / word + piece_words - 1) / piece_words;
+  for (int64_t lg = blockIdx.y; lg < s.layers * groups; lg += gridDim.y) {
+    int64_t layer = 0, g = lg;
+    if (s.layers > 1) layer = lg / groups, g = lg - layer * groups;
+    for (int64_t piece = blockIdx.x; piece < pieces; piece += gridDim.x) {
+      if (word == 16)
+        move_rows<uint4>(s, parents, layer, g, beams, select, piece, piece_words);
+      else if (word == 4)
+        move_rows<uint32_t>(s, parents, layer, g, beams, select, piece, piece_words);
+      else
+        move_rows<uint8_t>(s, parents, layer, g, beams, select, piece, piece_words);
     }
   }
 }
@@ -448,12 +540,7 @@ __global__ void __launch_bounds__(kMoveThreads)
   constexpr int kCols = 32;
   __shared__ W tile[kBeamMax][kCols];
   const rvq_beam_state s = list.s[blockIdx.z];
-  if (s.src != s.dst) return;
-  // widest words that the rows allow
-  const uintptr_t all = reinterpret_cast<uintptr_t>(s.dst) | (uintptr_t)s.row_bytes | (uintptr_t)s.dst_layer_stride |
-                        (uintptr_t)s.dst_group_stride | (uintptr_t)s.dst_beam_stride;
-  const int wide = (all & 15) == 0 ? 16 : (all & 3) == 0 ? 4 : 1;
-  if (wide != (int)sizeof(W)) return;
+  if (state_word(s) != (int)sizeof(W)) return;
   const int64_t words = s.row_bytes / (int64_t)sizeof(W), pieces = (words + kCols - 1) / kCols;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = kMoveThreads / 32;
   for (int64_t i = blockIdx.x; i < s.layers * groups * pieces; i += gridDim.x) {
@@ -505,7 +592,7 @@ BeamPlan beam_plan(const rvq_beam_dims &dm) {
   }
   const int64_t rows = dm.groups * dm.beams;
   int64_t s = rows > 0 ? (2 * 152 + rows - 1) / rows : 1;
-  const int most = (pieces + kRowWarps - 1) / kRowWarps;
+  const int block = 32 * kRowVectors * kRowWarps, most = full > block ? (full + block - 1) / block : 1;
   s = s > most ? most : s;
   s = s > kMaxLists / dm.beams ? kMaxLists / dm.beams : s;
   p.splits = (int)s;
@@ -586,7 +673,8 @@ RVQ_API rvq_status rvq_beam_reorder(rvq_beam_dims dims, const int32_t *parents, 
   if (n_states < 0 || n_states > RVQ_BEAM_MAX_STATES || (n_states > 0 && !states)) return RVQ_ERR_INVALID_ARG;
   StateList move, swap;
   int moves = 0, swaps = 0;
-  int64_t slots = 0, bytes = 0, pieces = 0;
+  const int words = move_words(dims.select);
+  int64_t rows = 0, most = 0, pieces = 0;
   bool wide[3] = {false, false, false};
   for (int i = 0; i < n_states; ++i) {
     const rvq_beam_state &s = states[i];
@@ -598,26 +686,26 @@ RVQ_API rvq_status rvq_beam_reorder(rvq_beam_dims dims, const int32_t *parents, 
           s.src_group_stride != s.dst_group_stride || s.src_beam_stride != s.dst_beam_stride)
         return RVQ_ERR_INVALID_ARG;
       swap.s[swaps++] = s;
-      const uintptr_t all = reinterpret_cast<uintptr_t>(s.dst) | (uintptr_t)s.row_bytes |
-                            (uintptr_t)s.dst_layer_stride | (uintptr_t)s.dst_group_stride | (uintptr_t)s.dst_beam_stride;
-      const int w = (all & 15) == 0 ? 16 : (all & 3) == 0 ? 4 : 1;
+      const int w = state_word(s);
       wide[w == 16 ? 0 : w == 4 ? 1 : 2] = true;
       const int64_t p = s.layers * dims.groups * ((s.row_bytes / w + 31) / 32);
       pieces = p > pieces ? p : pieces;
     } else {
       move.s[moves++] = s;
-      slots = s.layers * dims.groups * dims.select > slots ? s.layers * dims.groups * dims.select : slots;
-      bytes = s.row_bytes > bytes ? s.row_bytes : bytes;
+      const int w = state_word(s);
+      const int64_t across = (s.row_bytes / w + words - 1) / words;
+      rows = s.layers * dims.groups > rows ? s.layers * dims.groups : rows;
+      most = across > most ? across : most;
     }
   }
   if (moves + swaps == 0) return RVQ_OK;
   if (!parents || !aligned_to(parents, 4)) return RVQ_ERR_INVALID_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (moves) {
-    int64_t across = (bytes / 16 + kMoveThreads * 4 - 1) / (kMoveThreads * 4);
-    across = across < 1 ? 1 : across > 64 ? 64 : across;
-    const dim3 grid((unsigned)(slots < (1 << 20) ? slots : (1 << 20)), (unsigned)across, (unsigned)moves);
-    k_beam_reorder<<<grid, kMoveThreads, 0, st>>>(move, parents, dims.groups, dims.beams, dims.select);
+    // neighbouring blocks take neighbouring pieces
+    const dim3 grid((unsigned)(most < (1 << 24) ? most : (1 << 24)), (unsigned)(rows < 65535 ? rows : 65535),
+                    (unsigned)moves);
+    k_beam_reorder<<<grid, kMoveThreads, 0, st>>>(move, parents, dims.groups, dims.beams, dims.select, words);
     if (cudaGetLastError() != cudaSuccess) return RVQ_ERR_CUDA;
   }
   if (swaps) {

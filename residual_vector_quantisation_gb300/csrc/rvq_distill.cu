@@ -248,15 +248,6 @@ struct Power {
   __device__ __forceinline__ float operator()(float z) const { return exp2_fast((z - m) * c); }
 };
 
-template <class T>
-__device__ __forceinline__ float largest(const uint4 &v, float m) {
-  float f[16 / sizeof(T)];
-  unpack16<T>(v, f);
-#pragma unroll
-  for (int i = 0; i < 16 / (int)sizeof(T); ++i) m = fmaxf(m, f[i]);
-  return m;
-}
-
 // A thread's share of a row in registers: the vectors t, t + threads, ... and
 // perhaps an edge element.
 template <class T, int NV>
@@ -273,7 +264,7 @@ struct Share {
   __device__ __forceinline__ float most() const {
     float m = edge;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) m = largest<T>(raw[j], m);
+    for (int j = 0; j < NV; ++j) m = fmaxf(m, largest_of<T>(raw[j]));
     return m;
   }
   // The powers in place of the values; the sum of those without a bit.
@@ -472,7 +463,7 @@ __global__ void __launch_bounds__(kLongThreads) k_distill_long(const DistillArgs
 #pragma unroll
       for (int j = 0; j < U; ++j) raw[j] = v0 + j * threads < r.full ? r.vector(v0 + j * threads) : all_low<T>();
 #pragma unroll
-      for (int j = 0; j < U; ++j) most = largest<T>(raw[j], most);
+      for (int j = 0; j < U; ++j) most = fmaxf(most, largest_of<T>(raw[j]));
       if (most > m) {
         s *= share(m, most, c);
         m = most;

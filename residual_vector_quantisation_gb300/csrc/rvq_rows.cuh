@@ -9,6 +9,8 @@
 #include <math_constants.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "rvq.h"
 
 namespace rvq {
@@ -75,6 +77,19 @@ __device__ __forceinline__ uint4 pack16(const float (&f)[16 / sizeof(T)]) {
     v = make_uint4(w[0], w[1], w[2], w[3]);
   }
   return v;
+}
+
+// The largest element of a vector (a NaN is passed over).
+template <class T>
+__device__ __forceinline__ float largest_of(const uint4 &v) {
+  if constexpr (sizeof(T) == 4) {
+    return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
+  } else {
+    using P = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+    const P *p = reinterpret_cast<const P *>(&v);
+    const P m = __hmax2(__hmax2(p[0], p[1]), __hmax2(p[2], p[3]));
+    return fmaxf(to_float(m.x), to_float(m.y));
+  }
 }
 
 // A row cut at 16-byte boundaries: `head` elements before the first, `full`
