@@ -11,6 +11,7 @@
 // lists a second kernel joins (k_beam_join).
 #include "rvq_internal.cuh"
 #include "rvq_rows.cuh"
+#include "sm103_ptx.cuh"
 
 namespace rvq {
 namespace {
@@ -232,17 +233,12 @@ __device__ __forceinline__ void warp_pieces(const CutRow<T> &in, int first, int 
 // i of beam i / per, sum[i] its part of the beam's sum; by all threads.
 struct Join {
   uint64_t room[2 * kRoom + kBeamMax], tie[2 * kRoom + kBeamMax];
-  float2 lse[kBeamMax];  // of a row: m, log s
-  uint64_t head[32];
+  float2 lse[kBeamMax];   // of a beam: m, log s
+  float score[kBeamMax];  // -inf: dead
+  bool done[kBeamMax];    // finished
   uint32_t bar;
   int count;
 };
-
-__device__ __forceinline__ uint32_t total_of(const BeamArgs &a, const Join &w, float score, int beam, uint64_t key) {
-  if (!key) return 0;
-  const float v = value_of((uint32_t)(key >> 32));
-  return order_of(a.dm.mode == RVQ_BEAM_RAW ? v : score + ((v - w.lse[beam].x) - w.lse[beam].y));
-}
 
 __device__ __forceinline__ void put_candidate(const BeamArgs &a, int64_t g, int place, uint32_t total, int beam,
                                               int code) {
@@ -291,49 +287,54 @@ __device__ __forceinline__ void join_in_warp(const BeamArgs &a, int64_t g, const
   for (int i = lane + 32; i < n; i += 32) put_candidate(a, g, i, 0, 0, 0);
 }
 
-__device__ void join_group(const BeamArgs &a, int64_t g, uint64_t *list, const float2 *sum, int per, Join &w) {
+__device__ __forceinline__ void join_group(const BeamArgs &a, int64_t g, const uint64_t *list, const float2 *sum, int per, Join &w) {
   const int B = a.dm.beams, n = a.dm.select, lists = B * per, tid = threadIdx.x, lane = tid & 31;
   if (lists * n <= 32) return join_in_warp(a, g, list, sum, per);
   for (int b = tid; b < B; b += blockDim.x) {
     const int64_t row = g * B + b;
-    float m = 0.f, s = 1.f;
-    if (beam_live(a, row)) {
-      if (a.dm.mode != RVQ_BEAM_RAW) {
-        m = -CUDART_INF_F, s = 0.f;
-        for (int i = 0; i < per; ++i) join_sum(m, s, sum[b * per + i].x, sum[b * per + i].y);
-      }
-    } else {
-      // a finished beam's one candidate, at its score; a dead one's none
-      const bool done = a.scores[row] > -CUDART_INF_F;
-      for (int i = 0; i < per * n; ++i) list[b * per * n + i] = 0;
-      if (done) list[b * per * n] = key_of(0.f, a.end_code);
-    }
+    const float score = a.scores[row];
+    const bool done = a.finished && a.finished[row];
+    float m = -CUDART_INF_F, s = 0.f;
+    if (a.dm.mode != RVQ_BEAM_RAW && !done)
+      for (int i = 0; i < per; ++i) join_sum(m, s, sum[b * per + i].x, sum[b * per + i].y);
     w.lse[b] = make_float2(m, logf(s));
+    w.score[b] = score > -CUDART_INF_F ? score : -CUDART_INF_F;
+    w.done[b] = done;
   }
   if (tid == 0) w.bar = 0, w.count = 0;
   __syncthreads();
-  auto total = [&](int i) -> uint32_t {  // of entry i
+  // Entry i's total and key.  A finished beam's one candidate is its first entry, a dead one has none; the
+  // lists of both were never written.
+  auto entry = [&](int i, uint64_t &key) -> uint32_t {
     const int b = i / n / per;
-    const int64_t row = g * B + b;
-    const uint64_t k = list[i];
-    if (k && a.finished && a.finished[row]) return order_of(a.scores[row]);
-    return k ? total_of(a, w, a.scores[row], b, k) : 0;
+    const float score = w.score[b];
+    key = 0;
+    if (score == -CUDART_INF_F) return 0;
+    if (w.done[b]) {
+      if (i != b * per * n) return 0;
+      key = key_of(0.f, a.end_code);
+      return order_of(score);
+    }
+    key = list[i];
+    if (!key || a.dm.mode == RVQ_BEAM_RAW) return (uint32_t)(key >> 32);
+    return order_of(score + ((value_of((uint32_t)(key >> 32)) - w.lse[b].x) - w.lse[b].y));
   };
   // the best of the lists' last entries is a bar that n entries reach
   uint32_t bar = 0;
-  for (int i = tid; i < lists; i += blockDim.x) bar = max(bar, total(i * n + n - 1));
+  uint64_t key;
+  for (int i = tid; i < lists; i += blockDim.x) bar = max(bar, entry(i * n + n - 1, key));
   bar = __reduce_max_sync(0xffffffffu, bar);
   if (lane == 0 && bar) atomicMax(&w.bar, bar);
   __syncthreads();
   bar = max(w.bar, 1u);
   constexpr int kTop = 2 * kRoom;
   for (int i = tid; i < lists * n; i += blockDim.x) {
-    const uint32_t t = total(i);
+    const uint32_t t = entry(i, key);
     if (t >= bar) {
       const int at = atomicAdd(&w.count, 1);
       if (at < kTop) {
         w.room[at] = (uint64_t)t << 32 | (uint32_t)~(i / n / per);
-        w.tie[at] = list[i];
+        w.tie[at] = key;
       }
     }
   }
@@ -356,9 +357,9 @@ __device__ void join_group(const BeamArgs &a, int64_t g, uint64_t *list, const f
     for (int c = 0; c < n; ++c) {
       uint64_t k = 0, t = 0;
       for (int i = lane; i < lists * n; i += 32) {
-        const uint32_t tot = total(i);
-        if (!tot) continue;
-        const uint64_t ki = (uint64_t)tot << 32 | (uint32_t)~(i / n / per), ti = list[i];
+        const uint32_t total = entry(i, key);
+        if (!total) continue;
+        const uint64_t ki = (uint64_t)total << 32 | (uint32_t)~(i / n / per), ti = key;
         if ((ki < k0 || (ki == k0 && ti < t0)) && (ki > k || (ki == k && ti > t))) k = ki, t = ti;
       }
 #pragma unroll
@@ -384,6 +385,7 @@ __global__ void __launch_bounds__(32 * kGroupWarps) k_beam_group(const BeamArgs 
   WarpRoom &room = reinterpret_cast<WarpRoom *>(sum + B * per)[threadIdx.x >> 5];
   const int64_t g = blockIdx.x;
   const bool raw = a.dm.mode == RVQ_BEAM_RAW;
+  ptx::griddep_launch_dependents();
   for (int i = threadIdx.x >> 5; i < B * per; i += warps) {
     const int64_t row = g * B + i / per;
     if (!beam_live(a, row)) continue;
@@ -411,6 +413,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) k_beam_rows(const BeamArgs a) 
   const bool raw = a.dm.mode == RVQ_BEAM_RAW;
   const int64_t row = blockIdx.x / a.splits;
   const int split = (int)(blockIdx.x % a.splits);
+  ptx::griddep_launch_dependents();
   if (!beam_live(a, row)) return;
   const CutRow<T> in(static_cast<const T *>(a.logits) + row * a.stride, a.dm.vocab);
   float m, s;
@@ -449,7 +452,8 @@ __global__ void __launch_bounds__(256) k_beam_join(const BeamArgs a) {
   const int lists = a.dm.beams * a.splits, n = a.dm.select;
   const int64_t g = blockIdx.x;
   float2 *sum = reinterpret_cast<float2 *>(smem + (size_t)lists * n);
-  // (dead and finished beams' entries are never written: join_group replaces them)
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
   for (int i = threadIdx.x; i < lists * n; i += blockDim.x) smem[i] = a.parts.list[g * lists * n + i];
   for (int i = threadIdx.x; i < lists; i += blockDim.x) sum[i] = a.parts.sum[g * lists + i];
   __syncthreads();
@@ -505,10 +509,13 @@ __host__ __device__ inline int state_word(const rvq_beam_state &s) {
                         (uintptr_t)s.dst_layer_stride | (uintptr_t)s.dst_group_stride | (uintptr_t)s.dst_beam_stride;
   return (all & 15) == 0 ? 16 : (all & 3) == 0 ? 4 : 1;
 }
-// Words of a row that a block moves for each slot, and pieces of a row.
-inline int move_words(int select) {
-  const int w = kMoveThreads * kMoveDepth / select;
-  return w < 32 ? 32 : w;
+// Words of a row that a block moves for each slot: 256 (4 KB; 2 KB measured 110
+// against 90 us at 4 x 16 x 8 rows of 768 KB), more where there are few slots,
+// fewer while the blocks do not fill the GPU.
+inline int move_words(int select, int64_t rows, int64_t words) {
+  int w = select < kMoveDepth ? kMoveThreads * kMoveDepth / select : kMoveThreads;
+  while (w > 32 && rows * ((words + w - 1) / w) < 2 * 152) w /= 2;
+  return w;
 }
 
 __global__ void __launch_bounds__(kMoveThreads)
@@ -517,6 +524,7 @@ __global__ void __launch_bounds__(kMoveThreads)
   const rvq_beam_state &s = list.s[blockIdx.z];
   const int word = state_word(s);
   const int64_t pieces = (s.row_bytes / word + piece_words - 1) / piece_words;
+  ptx::griddep_wait();
   for (int64_t lg = blockIdx.y; lg < s.layers * groups; lg += gridDim.y) {
     int64_t layer = 0, g = lg;
     if (s.layers > 1) layer = lg / groups, g = lg - layer * groups;
@@ -540,6 +548,7 @@ __global__ void __launch_bounds__(kMoveThreads)
   constexpr int kCols = 32;
   __shared__ W tile[kBeamMax][kCols];
   const rvq_beam_state s = list.s[blockIdx.z];
+  ptx::griddep_wait();  // by every block: a grid that ended without it would let the next one start too early
   if (state_word(s) != (int)sizeof(W)) return;
   const int64_t words = s.row_bytes / (int64_t)sizeof(W), pieces = (words + kCols - 1) / kCols;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = kMoveThreads / 32;
@@ -561,6 +570,23 @@ __global__ void __launch_bounds__(kMoveThreads)
   }
 }
 
+// A kernel that may be brought up while the one before it on the stream ends:
+// it waits (griddep_wait) before it reads or writes anything.
+template <class... P, class... A>
+cudaError_t launch_next(void (*kernel)(P...), dim3 grid, int block, size_t smem, cudaStream_t st, const A &...args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 rvq_status check_beam(const rvq_beam_dims &dm) {
   if (dm.groups < 0 || dm.beams <= 0 || dm.vocab <= 0 || dm.select <= 0 || !dtype_bytes(dm.dtype)) return RVQ_ERR_INVALID_ARG;
   if (dm.mode != RVQ_BEAM_LOGITS && dm.mode != RVQ_BEAM_RAW) return RVQ_ERR_INVALID_ARG;
@@ -570,7 +596,7 @@ rvq_status check_beam(const rvq_beam_dims &dm) {
 }
 
 // How a call runs.  A group of at most kGroupItems pieces: one block, `splits`
-// warps a row.  Else `splits` blocks a row: as many as fill the GPU twice, none
+// warps a row.  Else `splits` blocks a row: as many as fill the GPU, none
 // without a piece for each of its warps.
 struct BeamPlan {
   bool group;
@@ -623,8 +649,7 @@ cudaError_t launch_beam(const BeamArgs &a, const BeamPlan &p, cudaStream_t st) {
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess) e = beam_smem(k_beam_join, p.smem);
   if (e != cudaSuccess) return e;
-  k_beam_join<<<(unsigned)a.dm.groups, 256, p.smem, st>>>(a);
-  return cudaGetLastError();
+  return launch_next(k_beam_join, dim3((unsigned)a.dm.groups), 256, p.smem, st, a);
 }
 
 }  // namespace
@@ -673,8 +698,7 @@ RVQ_API rvq_status rvq_beam_reorder(rvq_beam_dims dims, const int32_t *parents, 
   if (n_states < 0 || n_states > RVQ_BEAM_MAX_STATES || (n_states > 0 && !states)) return RVQ_ERR_INVALID_ARG;
   StateList move, swap;
   int moves = 0, swaps = 0;
-  const int words = move_words(dims.select);
-  int64_t rows = 0, most = 0, pieces = 0;
+  int64_t rows = 0, longest = 0, pieces = 0;
   bool wide[3] = {false, false, false};
   for (int i = 0; i < n_states; ++i) {
     const rvq_beam_state &s = states[i];
@@ -692,10 +716,9 @@ RVQ_API rvq_status rvq_beam_reorder(rvq_beam_dims dims, const int32_t *parents, 
       pieces = p > pieces ? p : pieces;
     } else {
       move.s[moves++] = s;
-      const int w = state_word(s);
-      const int64_t across = (s.row_bytes / w + words - 1) / words;
+      const int64_t across = s.row_bytes / state_word(s);
       rows = s.layers * dims.groups > rows ? s.layers * dims.groups : rows;
-      most = across > most ? across : most;
+      longest = across > longest ? across : longest;
     }
   }
   if (moves + swaps == 0) return RVQ_OK;
@@ -703,17 +726,26 @@ RVQ_API rvq_status rvq_beam_reorder(rvq_beam_dims dims, const int32_t *parents, 
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (moves) {
     // neighbouring blocks take neighbouring pieces
+    const int words = move_words(dims.select, rows, longest);
+    const int64_t most = (longest + words - 1) / words;
     const dim3 grid((unsigned)(most < (1 << 24) ? most : (1 << 24)), (unsigned)(rows < 65535 ? rows : 65535),
                     (unsigned)moves);
-    k_beam_reorder<<<grid, kMoveThreads, 0, st>>>(move, parents, dims.groups, dims.beams, dims.select, words);
-    if (cudaGetLastError() != cudaSuccess) return RVQ_ERR_CUDA;
+    if (launch_next(k_beam_reorder, grid, kMoveThreads, 0, st, move, parents, dims.groups, dims.beams, dims.select,
+                    words) != cudaSuccess)
+      return RVQ_ERR_CUDA;
   }
   if (swaps) {
     const dim3 grid((unsigned)(pieces < (1 << 16) ? pieces : (1 << 16)), 1, (unsigned)swaps);
-    if (wide[0]) k_beam_reorder_in_place<uint4><<<grid, kMoveThreads, 0, st>>>(swap, parents, dims.groups, dims.beams);
-    if (wide[1]) k_beam_reorder_in_place<uint32_t><<<grid, kMoveThreads, 0, st>>>(swap, parents, dims.groups, dims.beams);
-    if (wide[2]) k_beam_reorder_in_place<uint8_t><<<grid, kMoveThreads, 0, st>>>(swap, parents, dims.groups, dims.beams);
-    if (cudaGetLastError() != cudaSuccess) return RVQ_ERR_CUDA;
+    cudaError_t e = cudaSuccess;
+    if (wide[0])
+      e = launch_next(k_beam_reorder_in_place<uint4>, grid, kMoveThreads, 0, st, swap, parents, dims.groups, dims.beams);
+    if (e == cudaSuccess && wide[1])
+      e = launch_next(k_beam_reorder_in_place<uint32_t>, grid, kMoveThreads, 0, st, swap, parents, dims.groups,
+                      dims.beams);
+    if (e == cudaSuccess && wide[2])
+      e = launch_next(k_beam_reorder_in_place<uint8_t>, grid, kMoveThreads, 0, st, swap, parents, dims.groups,
+                      dims.beams);
+    if (e != cudaSuccess) return RVQ_ERR_CUDA;
   }
   return RVQ_OK;
 }
