@@ -436,19 +436,27 @@ __global__ void __launch_bounds__(kRingThreads)
     k_norm_backward_ring(const T *dy, int64_t dys, const T *x, int64_t xs, const P *__restrict__ weight,
                          const float *__restrict__ mean, const float *__restrict__ rstd, int64_t rows, int width, T *dx,
                          int64_t dxs, float *part, int tpr_) {
-  constexpr int N = 16 / (int)sizeof(T), NV = C / N;
+  constexpr int N = 16 / (int)sizeof(T), NV = C / N, H = N / 2;
   extern __shared__ uint4 ring[];
   __shared__ float box[2 * kRingThreads / 64][2][16];
   const int tpr = WARP ? 32 : tpr_, group = threadIdx.x / tpr, groups = blockDim.x / tpr;
   const int64_t step = (int64_t)gridDim.x * groups, first = blockIdx.x + (int64_t)group * gridDim.x;
   const Columns<N, NV> c(x + (int64_t)blockIdx.x * xs, sizeof(T), width, tpr, threadIdx.x % tpr);
   const float inv = 1.f / (float)width;
-  float g[NV][N], ge, dw[NV][N], db[NV][N], dwe = 0.f, dbe = 0.f;
-  load_columns<P, N, NV>(weight, c, 1.f, g, ge);
+  const F2 zero = f2(0.f, 0.f);
+  F2 g[NV][H], dw[NV][H], db[NV][H];
+  float ge, dwe = 0.f, dbe = 0.f;
+  {
+    float w[NV][N];
+    load_columns<P, N, NV>(weight, c, 1.f, w, ge);
 #pragma unroll
-  for (int j = 0; j < NV; ++j)
+    for (int j = 0; j < NV; ++j)
 #pragma unroll
-    for (int i = 0; i < N; ++i) dw[j][i] = db[j][i] = 0.f;
+      for (int i = 0; i < H; ++i) {
+        g[j][i] = f2(w[j][2 * i], w[j][2 * i + 1]);
+        dw[j][i] = db[j][i] = zero;
+      }
+  }
   uint4 *slot = ring + threadIdx.x;  // [stage][x, dy][j][thread], then [stage][thread] of mean and rstd
   float2 *stat = reinterpret_cast<float2 *>(ring + STAGES * 2 * NV * blockDim.x) + threadIdx.x;
 #pragma unroll
@@ -482,44 +490,49 @@ __global__ void __launch_bounds__(kRingThreads)
     copies_wait<STAGES - 1>();
     const float2 ms = stat[stage * blockDim.x];
     const float r = ms.y;
+    const F2 mu2 = f2(-ms.x, -ms.x), r2 = f2(r, r);
     const uint4 *xv = slot + stage * 2 * NV * blockDim.x, *dv = xv + NV * blockDim.x;
-    float s[2] = {de * ge, de * ge * ((xe - ms.x) * r)};
-    if (c.edge >= 0) {
-      dwe = fmaf(de, (xe - ms.x) * r, dwe);
-      dbe += de;
-    }
+    F2 s0 = zero, s1 = zero;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      float f[N], d[N];
-      unpack16<T>(read16(xv + j * blockDim.x), f);
-      unpack16<T>(read16(dv + j * blockDim.x), d);
+      F2 f[H], d[H];
+      unpack_pairs<T>(read16(xv + j * blockDim.x), f);
+      unpack_pairs<T>(read16(dv + j * blockDim.x), d);
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const float h = (f[i] - ms.x) * r, a = d[i] * g[j][i];  // no column: d = 0
-        s[0] += a;
-        s[1] = fmaf(a, h, s[1]);
-        dw[j][i] = fmaf(d[i], h, dw[j][i]);
-        db[j][i] += d[i];
+      for (int i = 0; i < H; ++i) {
+        const F2 h = (f[i] + mu2) * r2, a = d[i] * g[j][i];  // no column: d = 0
+        s0 = s0 + a;
+        s1 = fma2(a, h, s1);
+        dw[j][i] = fma2(d[i], h, dw[j][i]);
+        db[j][i] = db[j][i] + d[i];
       }
     }
+    const float he = (xe - ms.x) * r;
+    if (c.edge >= 0) {
+      dwe = fmaf(de, he, dwe);
+      dbe += de;
+    }
     if (dx != nullptr) {
+      const float2 a0 = floats(s0), a1 = floats(s1);
+      float s[2] = {a0.x + a0.y, a1.x + a1.y};
+      if (c.edge >= 0) s[0] += de * ge, s[1] = fmaf(de * ge, he, s[1]);
       group_sum<2, WARP>(s, box, turn, group, tpr);
+      if constexpr (WARP) __syncwarp();  // the second reading of the row stays below: moved up, it spills
       const float m1 = s[0] * inv, m2 = s[1] * inv;
+      const F2 minus1 = f2(-m1, -m1), minus2 = f2(-m2, -m2);
       T *dxr = dx + row * dxs;
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         if (!c.has(j)) continue;
-        float f[N], d[N];
-        unpack16<T>(read16(xv + j * blockDim.x), f);
-        unpack16<T>(read16(dv + j * blockDim.x), d);
+        F2 f[H], d[H];
+        unpack_pairs<T>(read16(xv + j * blockDim.x), f);
+        unpack_pairs<T>(read16(dv + j * blockDim.x), d);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const float h = (f[i] - ms.x) * r;
-          f[i] = r * (fmaf(d[i], g[j][i], -m1) - h * m2);
-        }
-        *reinterpret_cast<uint4 *>(dxr + c.column(j)) = pack16<T>(f);
+        for (int i = 0; i < H; ++i)
+          f[i] = fma2((f[i] + mu2) * r2, minus2, fma2(d[i], g[j][i], minus1)) * r2;
+        *reinterpret_cast<uint4 *>(dxr + c.column(j)) = pack_pairs<T>(f);
       }
-      if (c.edge >= 0) dxr[c.edge] = from_float<T>(r * (fmaf(de, ge, -m1) - (xe - ms.x) * r * m2));
+      if (c.edge >= 0) dxr[c.edge] = from_float<T>(r * (fmaf(de, ge, -m1) - he * m2));
     }
     stage = (stage + 1) % STAGES;
   }
@@ -533,9 +546,10 @@ __global__ void __launch_bounds__(kRingThreads)
   for (int j = 0; j < NV; ++j)
     if (c.has(j))
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        own[c.column(j) + i] = dw[j][i];
-        own[width + c.column(j) + i] = db[j][i];
+      for (int i = 0; i < H; ++i) {
+        const float2 w = floats(dw[j][i]), b = floats(db[j][i]);
+        own[c.column(j) + 2 * i] = w.x, own[c.column(j) + 2 * i + 1] = w.y;
+        own[width + c.column(j) + 2 * i] = b.x, own[width + c.column(j) + 2 * i + 1] = b.y;
       }
   if (c.edge >= 0) own[c.edge] = dwe, own[width + c.edge] = dbe;
   if (groups == 1) return;

@@ -79,6 +79,54 @@ __device__ __forceinline__ uint4 pack16(const float (&f)[16 / sizeof(T)]) {
   return v;
 }
 
+// Two floats in one operation each (round to nearest, as the single ones).
+struct F2 {
+  unsigned long long v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 floats(F2 a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+  return r;
+}
+__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+// A vector as pairs of floats, and back.
+template <class T>
+__device__ __forceinline__ void unpack_pairs(const uint4 &v, F2 (&f)[8 / sizeof(T)]) {
+  float e[16 / sizeof(T)];
+  unpack16<T>(v, e);
+#pragma unroll
+  for (int i = 0; i < 8 / (int)sizeof(T); ++i) f[i] = f2(e[2 * i], e[2 * i + 1]);
+}
+template <class T>
+__device__ __forceinline__ uint4 pack_pairs(const F2 (&f)[8 / sizeof(T)]) {
+  float e[16 / sizeof(T)];
+#pragma unroll
+  for (int i = 0; i < 8 / (int)sizeof(T); ++i) {
+    const float2 p = floats(f[i]);
+    e[2 * i] = p.x, e[2 * i + 1] = p.y;
+  }
+  return pack16<T>(e);
+}
+
 // The largest element of a vector (a NaN is passed over).
 template <class T>
 __device__ __forceinline__ float largest_of(const uint4 &v) {
