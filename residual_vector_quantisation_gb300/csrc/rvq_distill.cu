@@ -32,6 +32,7 @@ struct DistillArgs {
   void *dlogits;
   int64_t dlogits_stride;
   int64_t *bad_codes;
+  float inv_t, c;  // 1 / T and log2(e) / T
 };
 
 __device__ __forceinline__ float load_any(const void *p, int32_t dtype, int64_t i) {
@@ -83,48 +84,100 @@ struct Row : CutRow<T> {
   }
 };
 
-// What a row's shared memory holds: the bits of the codes with an entry, by
-// place, and the entries: code (-1: empty), the teacher's logit t and the
-// student's z.
+// The bits that mark the codes with an entry.  By owner (rows in registers): a
+// word per thread, bit j * N + i for element i of its j-th vector, and a word
+// for the elements beside the vectors, a bit per thread.  By place (long rows):
+// a bit per element, place e - head + 8.
+struct Spot {
+  int word;
+  uint32_t bit;
+};
+template <class T>
+__device__ __forceinline__ Spot spot(const Row<T> &r, int e, int log_threads) {
+  constexpr int N = Row<T>::N;
+  if (log_threads < 0) return {r.place(e) >> 5, 1u << (r.place(e) & 31)};
+  const int k = e - r.head, v = k / N;
+  if (k >= 0 && v < r.full)
+    return {v & ((1 << log_threads) - 1), 1u << ((v >> log_threads) * N + (k & (N - 1)))};
+  return {1 << log_threads, 1u << (e < r.head ? e : N + k - r.full * N)};
+}
+inline int distill_words(int vocab, int threads) { return threads ? threads + 1 : (vocab + 8 + 31) / 32; }
+
+// A row's entries: code (-1: empty), the teacher's logit t, the student's z;
+// of one warp, in its registers (SMALL: at most 32) or in shared memory.
+template <bool SMALL>
 struct TopList {
   uint32_t *bits;
-  int32_t *code;
-  float *t, *z;
+  int32_t *codes;
+  float *ts, *zs;
+  int code;
+  float t, z;
+  __device__ __forceinline__ TopList(uint32_t *at, int words, int top) : bits(at) {
+    codes = reinterpret_cast<int32_t *>(at + words);
+    ts = reinterpret_cast<float *>(codes + top), zs = ts + top;
+    code = -1;
+  }
+  template <class F>
+  __device__ __forceinline__ void each(int top, F f) const {
+    if constexpr (SMALL) {
+      f(code, t, z);
+    } else {
+#pragma unroll 1
+      for (int j = threadIdx.x & 31; j < top; j += 32) f(codes[j], ts[j], zs[j]);
+    }
+  }
 };
-__host__ __device__ inline int distill_bit_words(int vocab) { return (vocab + 8 + 31) / 32; }
-inline size_t distill_smem(int vocab, int top) { return (size_t)(distill_bit_words(vocab) + 3 * top) * 4; }
-__device__ __forceinline__ TopList top_list(uint32_t *at, int words, int top) {
-  return {at, reinterpret_cast<int32_t *>(at + words), reinterpret_cast<float *>(at + words + top),
-          reinterpret_cast<float *>(at + words + 2 * top)};
-}
+inline size_t distill_smem(int words, int top, bool small) { return (size_t)(words + (small ? 0 : 3 * top)) * 4; }
+
+// The lane's first entry, asked for before anything else of the row is known.
+struct FirstEntry {
+  int code;
+  float t;
+  __device__ __forceinline__ FirstEntry(const DistillArgs &a, int64_t row) {
+    const int lane = threadIdx.x & 31;
+    const bool there = lane < a.dm.top;
+    code = there ? a.top_codes[row * a.dm.top + lane] : -1;
+    t = there ? load_any(a.top_logits, a.dm.top_dtype, row * a.dm.top + lane) : -CUDART_INF_F;
+  }
+};
 
 // One warp reads a row's entries (bits cleared before).  An entry counts where
 // its code is in range and stands for the first time, by the list's order.
-template <class T>
-__device__ __forceinline__ void read_top(const DistillArgs &a, int64_t row, const Row<T> &r, const TopList &l) {
+template <class T, bool SMALL>
+__device__ __forceinline__ void read_top(const DistillArgs &a, int64_t row, const Row<T> &r, int log_threads,
+                                         const FirstEntry &first, TopList<SMALL> &l) {
   const int lane = threadIdx.x & 31, top = a.dm.top;
   int bad = 0;
+#pragma unroll 1
   for (int j0 = 0; j0 < top; j0 += 32) {
     const int j = j0 + lane;
-    const int code = j < top ? a.top_codes[row * top + j] : -1;
+    int code = first.code;
+    float t = first.t;
+    if (!SMALL && j0) {
+      code = j < top ? a.top_codes[row * top + j] : -1;
+      t = j < top ? load_any(a.top_logits, a.dm.top_dtype, row * top + j) : -CUDART_INF_F;
+    }
     bool ok = code >= 0 && code < a.dm.vocab, seen = false;
+    const float z = ok ? to_float(r.z[code]) : -CUDART_INF_F;
     if (ok) {
-      const int p = r.place(code);
-      const uint32_t bit = 1u << (p & 31);
-      seen = atomicOr(&l.bits[p >> 5], bit) & bit;
+      const Spot p = spot(r, code, log_threads);
+      seen = atomicOr(&l.bits[p.word], p.bit) & p.bit;
     }
     const unsigned all_seen = __ballot_sync(0xffffffffu, seen);
     if (all_seen) {  // a code twice: the first of its lanes has it, unless an earlier 32 had
       const unsigned same = __match_any_sync(0xffffffffu, ok ? code : -1 - lane);
       ok = ok && __ffs(same) - 1 == lane && (same & ~all_seen);
     }
-    bad += j < top && code != -1 && !ok;
-    if (j < top) {
-      l.code[j] = ok ? code : -1;
-      l.t[j] = ok ? load_any(a.top_logits, a.dm.top_dtype, row * top + j) : -CUDART_INF_F;
-      l.z[j] = ok ? to_float(r.z[code]) : -CUDART_INF_F;
+    bad += code != -1 && !ok;
+    code = ok ? code : -1;
+    t = ok ? t : -CUDART_INF_F;
+    if constexpr (SMALL) {
+      l.code = code, l.t = t, l.z = ok ? z : -CUDART_INF_F;
+      break;
+    } else {
+      if (j < top) l.codes[j] = code, l.ts[j] = t, l.zs[j] = ok ? z : -CUDART_INF_F;
+      __syncwarp();
     }
-    __syncwarp();
   }
   if (a.bad_codes && __any_sync(0xffffffffu, bad)) {
     bad = __reduce_add_sync(0xffffffffu, bad);
@@ -147,38 +200,39 @@ __device__ __forceinline__ float entry_u(const TopSums &r, float t, float inv_t)
   return exp2_fast(fmaf(t - r.t_m, inv_t, -r.t_log) * kLog2e);
 }
 
-__device__ __forceinline__ TopSums top_sums(const DistillArgs &a, int64_t row, float inv_t, const TopList &l) {
-  const int lane = threadIdx.x & 31, top = a.dm.top;
+template <bool SMALL>
+__device__ __forceinline__ TopSums top_sums(const DistillArgs &a, float teacher_lse, const TopList<SMALL> &l) {
   const bool tail = a.teacher_lse != nullptr;
+  const float inv_t = a.inv_t;
   TopSums r;
   bool any = false;
   float tm = -CUDART_INF_F, zm = -CUDART_INF_F;
-  for (int j = lane; j < top; j += 32) {  // empty entries are -inf
-    any |= l.code[j] >= 0;
-    tm = fmaxf(tm, l.t[j]);
-    zm = fmaxf(zm, l.z[j]);
-  }
+  l.each(a.dm.top, [&](int code, float t, float z) {  // empty entries are -inf
+    any |= code >= 0;
+    tm = fmaxf(tm, t);
+    zm = fmaxf(zm, z);
+  });
   r.any = __any_sync(0xffffffffu, any);
   zm = warp_max_order(zm);
   r.z_m = zm == -CUDART_INF_F ? 0.f : zm;
   if (tail) {
-    r.t_m = 0.f, r.t_log = a.teacher_lse[row];
+    r.t_m = 0.f, r.t_log = teacher_lse;
   } else {
     tm = warp_max_order(tm);
     r.t_m = tm == -CUDART_INF_F ? 0.f : tm, r.t_log = 0.f;
   }
   r.on = r.u = r.ul = 0.f;
-  for (int j = lane; j < top; j += 32) {
-    if (l.code[j] < 0) continue;
-    const float zr = (l.z[j] - r.z_m) * inv_t, lt = fmaf(l.t[j] - r.t_m, inv_t, -r.t_log);
+  l.each(a.dm.top, [&](int code, float t, float z) {
+    if (code < 0) return;
+    const float zr = (z - r.z_m) * inv_t, lt = fmaf(t - r.t_m, inv_t, -r.t_log);
     const float u = exp2_fast(lt * kLog2e);
     r.on += exp2_fast(zr * kLog2e);
     r.u += u;
     if (u != 0.f) r.ul = fmaf(u * (1.f / kDistillMaxTop), lt - zr, r.ul);  // a NaN goes on
-  }
+  });
 #pragma unroll
   for (int o = 16; o; o >>= 1) {
-    r.on += __shfl_xor_sync(0xffffffffu, r.on, o);
+    if (tail) r.on += __shfl_xor_sync(0xffffffffu, r.on, o);
     r.u += __shfl_xor_sync(0xffffffffu, r.u, o);
     r.ul += __shfl_xor_sync(0xffffffffu, r.ul, o);
   }
@@ -228,12 +282,15 @@ __device__ __forceinline__ RowPlan plan_row(bool tail, float w, Sum sum, const T
   return r;
 }
 
-// Entry j's gradient.
-__device__ __forceinline__ float top_grad(const RowPlan &r, const TopSums &t, const TopList &l, int j, float c,
-                                          float inv_t) {
-  if (r.scale == 0.f) return 0.f;
-  const float p = r.all_r == 0.f ? 0.f : share(l.z[j], r.all_m, c) * r.all_r;
-  return (p - entry_u(t, l.t[j], inv_t) * r.u_r) * r.scale;
+// The entries' gradients, over what was written in their place.
+template <class T, bool SMALL>
+__device__ __forceinline__ void put_top(const DistillArgs &a, const Row<T> &r, const RowPlan &p, const TopSums &ts,
+                                        const TopList<SMALL> &l) {
+  l.each(a.dm.top, [&](int code, float t, float z) {
+    if (code < 0) return;
+    const float on = p.all_r == 0.f ? 0.f : share(z, p.all_m, a.c) * p.all_r;
+    r.d[code] = from_float<T>(p.scale == 0.f ? 0.f : (on - entry_u(ts, t, a.inv_t) * p.u_r) * p.scale);
+  });
 }
 
 // e^((z - m) / T).  m is subtracted first: as 2^(z c - m c), one operation less,
@@ -241,12 +298,34 @@ __device__ __forceinline__ float top_grad(const RowPlan &r, const TopSums &t, co
 // lowest value are large ms).
 struct Power {
   float m, c;
+  F2 minus, c2;
   __device__ __forceinline__ Power(float m_, float c_) {
     m = m_ == -CUDART_INF_F ? 0.f : m_;
     c = c_;
+    minus = f2(-m, -m), c2 = f2(c, c);
   }
   __device__ __forceinline__ float operator()(float z) const { return exp2_fast((z - m) * c); }
+  template <class T>
+  __device__ __forceinline__ void operator()(const uint4 &v, float (&e)[16 / sizeof(T)]) const {
+    F2 f[8 / sizeof(T)];
+    unpack_pairs<T>(v, f);
+#pragma unroll
+    for (int i = 0; i < 8 / (int)sizeof(T); ++i) {
+      const float2 y = floats((f[i] + minus) * c2);
+      e[2 * i] = exp2_fast(y.x), e[2 * i + 1] = exp2_fast(y.y);
+    }
+  }
 };
+// A vector of a gradient: the powers times `factor`.
+template <class T>
+__device__ __forceinline__ void put_scaled(const Row<T> &r, int v, float (&e)[16 / sizeof(T)], bool zero, F2 factor) {
+#pragma unroll
+  for (int i = 0; i < 8 / (int)sizeof(T); ++i) {
+    const float2 y = floats(f2(e[2 * i], e[2 * i + 1]) * factor);
+    e[2 * i] = zero ? 0.f : y.x, e[2 * i + 1] = zero ? 0.f : y.y;
+  }
+  r.put(v, e);
+}
 
 // A thread's share of a row in registers: the vectors t, t + threads, ... and
 // perhaps an edge element.
@@ -267,33 +346,24 @@ struct Share {
     for (int j = 0; j < NV; ++j) m = fmaxf(m, largest_of<T>(raw[j]));
     return m;
   }
-  // The powers in place of the values; the sum of those without a bit.
-  __device__ __forceinline__ float powers(const Row<T> &r, const Power &pw, const uint32_t *bits, int t, int threads) {
+  // The powers in place of the values; the sum of those without a bit (in `skip` and, for the edge, `skip_edge`).
+  __device__ __forceinline__ float powers(const Power &pw, uint32_t skip, bool skip_edge) {
     float s = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int v = t + j * threads, at = v * N + 8;
-      const uint32_t skip = bits && v < r.full ? bits[at >> 5] >> (at & 31) : 0;
-      unpack16<T>(raw[j], e[j]);
+      pw.template operator()<T>(raw[j], e[j]);
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        e[j][i] = pw(e[j][i]);
-        if (!(skip >> i & 1)) s += e[j][i];
-      }
+      for (int i = 0; i < N; ++i)
+        if (!(skip >> (j * N + i) & 1)) s += e[j][i];
     }
-    const int at = r.edge(t);
     edge = pw(edge);
-    if (at >= 0 && !(bits && bits[r.place(at) >> 5] >> (r.place(at) & 31) & 1)) s += edge;
-    return s;
+    return skip_edge ? s : s + edge;  // (without one it is 0)
   }
   __device__ __forceinline__ void put(const Row<T> &r, bool zero, float factor, int t, int threads) {
+    const F2 factors = f2(factor, factor);
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      if (t + j * threads >= r.full) continue;
-#pragma unroll
-      for (int i = 0; i < N; ++i) e[j][i] = zero ? 0.f : e[j][i] * factor;
-      r.put(t + j * threads, e[j]);
-    }
+    for (int j = 0; j < NV; ++j)
+      if (t + j * threads < r.full) put_scaled(r, t + j * threads, e[j], zero, factors);
     const int at = r.edge(t);
     if (at >= 0) r.d[at] = from_float<T>(zero ? 0.f : edge * factor);
   }
@@ -317,11 +387,13 @@ __device__ __forceinline__ Sum row_join(Sum v, float c, Sum *box) {
 // The sum over the codes without an entry, from its own largest value: where
 // the entries hold all but 1e-25 of the row.
 template <class T, bool WARP>
-__device__ __noinline__ Sum small_rest(const Row<T> &r, const uint32_t *bits, int t, int threads, float c, Sum *box) {
+__device__ __noinline__ Sum small_rest(const Row<T> &r, const uint32_t *bits, int log_threads, int t, int threads,
+                                       float c, Sum *box) {
   Sum sum = no_sum();
   for (int e = t; e < r.width; e += threads) {
-    const int p = r.place(e);
-    if (!(bits[p >> 5] >> (p & 31) & 1)) sum = join(sum, {to_float(r.z[e]), to_float(r.z[e]) == -CUDART_INF_F ? 0.f : 1.f}, c);
+    const Spot p = spot(r, e, log_threads);
+    const float z = to_float(r.z[e]);
+    if (!(bits[p.word] & p.bit)) sum = join(sum, {z, z == -CUDART_INF_F ? 0.f : 1.f}, c);
   }
   return row_join<WARP>(sum, c, box);
 }
@@ -344,50 +416,63 @@ __device__ __forceinline__ void skip_row(const DistillArgs &a, int64_t row, cons
 // A row in the registers of a warp (WARP: kRowWarps rows a block, no barrier)
 // or of a block: one read of the logits, one write of the gradient.
 constexpr int kRowWarps = 4, kMaxWarps = 16;
-template <class T, int NV, bool WARP>
+template <class T, int NV, bool WARP, bool SMALL>
 __global__ void __launch_bounds__(WARP ? 32 * kRowWarps : 32 * kMaxWarps) k_distill(const DistillArgs a) {
   extern __shared__ uint32_t smem[];
   __shared__ Sum box[kMaxWarps];
   __shared__ TopSums shared_top;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, top = a.dm.top, words = distill_bit_words(a.dm.vocab);
-  const int t = WARP ? lane : threadIdx.x, threads = WARP ? 32 : blockDim.x;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, top = a.dm.top;
+  const int t = WARP ? lane : threadIdx.x, threads = WARP ? 32 : blockDim.x, log_threads = 31 - __clz(threads);
   const int64_t row = WARP ? (int64_t)blockIdx.x * kRowWarps + warp : blockIdx.x;
   if (row >= a.dm.rows) return;
-  const Row<T> r(a, row);
+  const bool tail = a.teacher_lse != nullptr, known = a.sums_in != nullptr, lister = WARP || warp == 0;
+  const float c = a.c;
+  // what does not depend on anything is asked for first
   float w = a.weights ? a.weights[row] : 1.f;
+  const float teacher_lse = tail ? a.teacher_lse[row] : 0.f;
+  Sum sum = no_sum();
+  float up = 1.f;
+  if (known) {
+    sum = {a.sums_in[2 * row], a.sums_in[2 * row + 1]};
+    if (a.grad_loss) up = a.grad_loss[row];
+  }
+  const FirstEntry first(a, row);
+  const Row<T> r(a, row);
   if (w == 0.f) return skip_row(a, row, r, t, threads);
-  const bool tail = a.teacher_lse != nullptr, known = a.sums_in != nullptr;
-  const float inv_t = 1.f / a.dm.temperature, c = kLog2e * inv_t;
+  w *= up;
   Share<T, NV> x;
   x.load(r, t, threads);
-  const TopList l = top_list(smem + (WARP ? (size_t)warp * (words + 3 * top) : 0), words, top);
-  for (int i = t; i < words; i += threads) l.bits[i] = 0;
+  TopList<SMALL> l(smem + (WARP ? (size_t)warp * (33 + (SMALL ? 0 : 3 * top)) : 0), threads + 1, top);
+  l.bits[t] = 0;
+  if (t == 0) l.bits[threads] = 0;
   TopSums ts;
   if constexpr (WARP) {
     __syncwarp();
-    read_top(a, row, r, l);
-    ts = top_sums(a, row, inv_t, l);
+    read_top(a, row, r, 5, first, l);
+    __syncwarp();
+    ts = top_sums(a, teacher_lse, l);
   } else {
     __syncthreads();
-    if (warp == 0) {
-      read_top(a, row, r, l);
-      ts = top_sums(a, row, inv_t, l);
+    if (lister) {
+      read_top(a, row, r, log_threads, first, l);
+      __syncwarp();
+      ts = top_sums(a, teacher_lse, l);
       if (lane == 0) shared_top = ts;
     }
     __syncthreads();
     ts = shared_top;
   }
-  Sum sum;
-  float m;
-  if (known) {
-    sum = {a.sums_in[2 * row], a.sums_in[2 * row + 1]};
-    if (a.grad_loss) w *= a.grad_loss[row];
-    m = sum.m;
-  } else {
+  float m = sum.m;
+  uint32_t skip = 0;
+  bool skip_edge = false;
+  if (!known) {
     m = warp_max_order(x.most());
+    if (tail) {
+      skip = l.bits[t];
+      skip_edge = t < 32 && (l.bits[threads] >> t & 1);
+    }
   }
-  Power pw(m, c);
-  const float s = x.powers(r, pw, tail && !known ? l.bits : nullptr, t, threads);
+  const float s = x.powers(Power(m, c), skip, skip_edge);
   if (!known) {
     if constexpr (WARP) {
       sum = {m, warp_sum(s)};
@@ -398,52 +483,53 @@ __global__ void __launch_bounds__(WARP ? 32 * kRowWarps : 32 * kMaxWarps) k_dist
       sum = warp_join(lane < threads >> 5 ? box[lane] : no_sum(), c);
     }
     if (tail && sum.s < kSmallRest) {
-      sum = small_rest<T, WARP>(r, l.bits, t, threads, c, box);
+      sum = small_rest<T, WARP>(r, l.bits, log_threads, t, threads, c, box);
       m = sum.m;
-      pw = Power(m, c);
       x.load(r, t, threads);
-      x.powers(r, pw, nullptr, t, threads);
+      x.powers(Power(m, c), 0, false);
     }
   }
-  const RowPlan p = plan_row(tail, w, sum, ts, c, inv_t);
+  const RowPlan p = plan_row(tail, w, sum, ts, c, a.inv_t);
   if (!known && t == 0) {
     a.loss[row] = p.loss;
     if (a.sums) a.sums[2 * row] = sum.m, a.sums[2 * row + 1] = sum.s;
   }
   if (!r.d) return;
-  x.put(r, p.zero, p.rest_scale == 0.f ? 0.f : p.rest_scale * share(m, p.m, c), t, threads);
-  // the entries' gradients go over what was written in their place
+  float factor = p.rest_scale;
+  if (!WARP && factor != 0.f) factor *= share(m, p.m, c);  // a warp's powers are from its own largest value
+  x.put(r, p.zero, factor, t, threads);
   if constexpr (WARP)
     __syncwarp();
   else
     __syncthreads();
-  for (int j = t; j < top; j += threads)
-    if (l.code[j] >= 0) r.d[l.code[j]] = from_float<T>(top_grad(p, ts, l, j, c, inv_t));
+  if (lister) put_top(a, r, p, ts, l);
 }
 
 // Longer rows: a row per block, read twice (the second time from the L2), U
 // vectors of a thread at a time.
 constexpr int kLongThreads = 512;
-template <class T, int U>
+template <class T, int U, bool SMALL>
 __global__ void __launch_bounds__(kLongThreads) k_distill_long(const DistillArgs a) {
   constexpr int N = 16 / (int)sizeof(T);
   extern __shared__ uint32_t smem[];
   __shared__ Sum box[kMaxWarps];
   __shared__ TopSums shared_top;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, threads = blockDim.x;
-  const int top = a.dm.top, words = distill_bit_words(a.dm.vocab);
+  const int top = a.dm.top, words = (a.dm.vocab + 8 + 31) / 32;
   const int64_t row = blockIdx.x;
   const Row<T> r(a, row);
   float w = a.weights ? a.weights[row] : 1.f;
+  const FirstEntry first(a, row);
   if (w == 0.f) return skip_row(a, row, r, threadIdx.x, threads);
   const bool tail = a.teacher_lse != nullptr, known = a.sums_in != nullptr;
-  const float inv_t = 1.f / a.dm.temperature, c = kLog2e * inv_t;
-  const TopList l = top_list(smem, words, top);
+  const float c = a.c;
+  TopList<SMALL> l(smem, words, top);
   for (int i = threadIdx.x; i < words; i += threads) l.bits[i] = 0;
   __syncthreads();
   if (warp == 0) {
-    read_top(a, row, r, l);
-    const TopSums t = top_sums(a, row, inv_t, l);
+    read_top(a, row, r, -1, first, l);
+    __syncwarp();
+    const TopSums t = top_sums(a, tail ? a.teacher_lse[row] : 0.f, l);
     if (lane == 0) shared_top = t;
   }
   __syncthreads();
@@ -456,7 +542,10 @@ __global__ void __launch_bounds__(kLongThreads) k_distill_long(const DistillArgs
   } else {
     float m = edge >= 0 ? to_float(r.z[edge]) : -CUDART_INF_F, s = 0.f;
     Power pw(m, c);
-    if (edge >= 0 && !(tail && l.bits[r.place(edge) >> 5] >> (r.place(edge) & 31) & 1)) s = pw(to_float(r.z[edge]));
+    if (edge >= 0) {
+      const Spot p = spot(r, edge, -1);
+      if (!(tail && (l.bits[p.word] & p.bit))) s = pw(to_float(r.z[edge]));
+    }
     for (int v0 = threadIdx.x; v0 < r.full; v0 += U * threads) {
       uint4 raw[U];
       float most = m;
@@ -473,26 +562,24 @@ __global__ void __launch_bounds__(kLongThreads) k_distill_long(const DistillArgs
       for (int j = 0; j < U; ++j) {
         const int v = v0 + j * threads, at = v * N + 8;
         const uint32_t skip = tail && v < r.full ? l.bits[at >> 5] >> (at & 31) : 0;
-        float f[N];
-        unpack16<T>(raw[j], f);
+        float e[N];
+        pw.template operator()<T>(raw[j], e);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const float e = pw(f[i]);
-          if (!(skip >> i & 1)) s += e;
-        }
+        for (int i = 0; i < N; ++i)
+          if (!(skip >> i & 1)) s += e[i];
       }
     }
     sum = row_join<false>({m, s}, c, box);
-    if (tail && sum.s < kSmallRest) sum = small_rest<T, false>(r, l.bits, threadIdx.x, threads, c, box);
+    if (tail && sum.s < kSmallRest) sum = small_rest<T, false>(r, l.bits, -1, threadIdx.x, threads, c, box);
   }
-  const RowPlan p = plan_row(tail, w, sum, ts, c, inv_t);
+  const RowPlan p = plan_row(tail, w, sum, ts, c, a.inv_t);
   if (!known && threadIdx.x == 0) {
     a.loss[row] = p.loss;
     if (a.sums) a.sums[2 * row] = sum.m, a.sums[2 * row + 1] = sum.s;
   }
   if (!r.d) return;
   const Power pw(p.m, c);
-  const float factor = p.rest_scale;
+  const F2 factor = f2(p.rest_scale, p.rest_scale);
   for (int v0 = threadIdx.x; v0 < r.full; v0 += U * threads) {
     uint4 raw[U];
 #pragma unroll
@@ -500,17 +587,14 @@ __global__ void __launch_bounds__(kLongThreads) k_distill_long(const DistillArgs
 #pragma unroll
     for (int j = 0; j < U; ++j) {
       if (v0 + j * threads >= r.full) continue;
-      float f[N];
-      unpack16<T>(raw[j], f);
-#pragma unroll
-      for (int i = 0; i < N; ++i) f[i] = p.zero ? 0.f : pw(f[i]) * factor;
-      r.put(v0 + j * threads, f);
+      float e[N];
+      pw.template operator()<T>(raw[j], e);
+      put_scaled(r, v0 + j * threads, e, p.zero, factor);
     }
   }
-  if (edge >= 0) r.d[edge] = from_float<T>(p.zero ? 0.f : pw(to_float(r.z[edge])) * factor);
+  if (edge >= 0) r.d[edge] = from_float<T>(p.zero ? 0.f : pw(to_float(r.z[edge])) * p.rest_scale);
   __syncthreads();
-  for (int j = threadIdx.x; j < top; j += threads)
-    if (l.code[j] >= 0) r.d[l.code[j]] = from_float<T>(top_grad(p, ts, l, j, c, inv_t));
+  if (warp == 0) put_top(a, r, p, ts, l);
 }
 
 // How a row is laid over threads: at most 32 elements of its vectors a thread,
@@ -527,15 +611,19 @@ inline DistillShape distill_shape(int vocab, int n) {
   return {0, 1};
 }
 
-template <class T, int NV>
-cudaError_t launch_distill_shape(const DistillArgs &a, int threads, cudaStream_t st) {
-  const size_t smem = distill_smem(a.dm.vocab, a.dm.top);
+template <class T, int NV, bool SMALL>
+cudaError_t launch_distill_list(const DistillArgs &a, int threads, cudaStream_t st) {
+  const size_t smem = distill_smem(distill_words(a.dm.vocab, threads), a.dm.top, SMALL);
   if (threads == 32)
-    k_distill<T, NV, true>
+    k_distill<T, NV, true, SMALL>
         <<<(unsigned)((a.dm.rows + kRowWarps - 1) / kRowWarps), 32 * kRowWarps, smem * kRowWarps, st>>>(a);
   else
-    k_distill<T, NV, false><<<(unsigned)a.dm.rows, threads, smem, st>>>(a);
+    k_distill<T, NV, false, SMALL><<<(unsigned)a.dm.rows, threads, smem, st>>>(a);
   return cudaGetLastError();
+}
+template <class T, int NV>
+cudaError_t launch_distill_shape(const DistillArgs &a, int threads, cudaStream_t st) {
+  return a.dm.top <= 32 ? launch_distill_list<T, NV, true>(a, threads, st) : launch_distill_list<T, NV, false>(a, threads, st);
 }
 
 template <class T>
@@ -550,13 +638,13 @@ cudaError_t launch_distill_typed(const DistillArgs &a, cudaStream_t st) {
       default: return launch_distill_shape<T, 4 * U>(a, s.threads, st);
     }
   }
-  const size_t smem = distill_smem(a.dm.vocab, a.dm.top);
+  const auto kernel = a.dm.top <= 32 ? k_distill_long<T, 4, true> : k_distill_long<T, 4, false>;
+  const size_t smem = distill_smem(distill_words(a.dm.vocab, 0), a.dm.top, a.dm.top <= 32);
   if (smem > 40 * 1024) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(k_distill_long<T, 4>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
   }
-  k_distill_long<T, 4><<<(unsigned)a.dm.rows, kLongThreads, smem, st>>>(a);
+  kernel<<<(unsigned)a.dm.rows, kLongThreads, smem, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -571,6 +659,7 @@ cudaError_t launch_distill_rows(const DistillArgs &a, cudaStream_t st) {
 }
 
 cudaError_t launch_distill(DistillArgs a, cudaStream_t st) {
+  a.inv_t = 1.f / a.dm.temperature, a.c = kLog2e * a.inv_t;
   const int64_t rows = a.dm.rows;
   const int e = dtype_bytes(a.dm.dtype), te = dtype_bytes(a.dm.top_dtype);
   for (int64_t r0 = 0; r0 < rows; r0 += kDistillMaxRows) {
