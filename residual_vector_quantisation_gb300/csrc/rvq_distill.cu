@@ -318,11 +318,11 @@ struct Power {
 };
 // A vector of a gradient: the powers times `factor`.
 template <class T>
-__device__ __forceinline__ void put_scaled(const Row<T> &r, int v, float (&e)[16 / sizeof(T)], bool zero, F2 factor) {
+__device__ __forceinline__ void put_scaled(const Row<T> &r, int v, float (&e)[16 / sizeof(T)], F2 factor) {
 #pragma unroll
   for (int i = 0; i < 8 / (int)sizeof(T); ++i) {
     const float2 y = floats(f2(e[2 * i], e[2 * i + 1]) * factor);
-    e[2 * i] = zero ? 0.f : y.x, e[2 * i + 1] = zero ? 0.f : y.y;
+    e[2 * i] = y.x, e[2 * i + 1] = y.y;
   }
   r.put(v, e);
 }
@@ -359,13 +359,13 @@ struct Share {
     edge = pw(edge);
     return skip_edge ? s : s + edge;  // (without one it is 0)
   }
-  __device__ __forceinline__ void put(const Row<T> &r, bool zero, float factor, int t, int threads) {
+  __device__ __forceinline__ void put(const Row<T> &r, float factor, int t, int threads) {
     const F2 factors = f2(factor, factor);
 #pragma unroll
     for (int j = 0; j < NV; ++j)
-      if (t + j * threads < r.full) put_scaled(r, t + j * threads, e[j], zero, factors);
+      if (t + j * threads < r.full) put_scaled(r, t + j * threads, e[j], factors);
     const int at = r.edge(t);
-    if (at >= 0) r.d[at] = from_float<T>(zero ? 0.f : edge * factor);
+    if (at >= 0) r.d[at] = from_float<T>(edge * factor);
   }
 };
 
@@ -399,18 +399,21 @@ __device__ __noinline__ Sum small_rest(const Row<T> &r, const uint32_t *bits, in
 }
 constexpr float kSmallRest = 1e-25f;
 
-// A row without weight: thread t of `threads`.
+// A gradient of zeros, and a row without weight: thread t of `threads`.
+template <class T>
+__device__ __forceinline__ void put_zeros(const Row<T> &r, int t, int threads) {
+  const float zero[Row<T>::N] = {};
+  for (int v = t; v < r.full; v += threads) r.put(v, zero);
+  const int at = r.edge(t);
+  if (at >= 0) r.d[at] = from_float<T>(0.f);
+}
 template <class T>
 __device__ __forceinline__ void skip_row(const DistillArgs &a, int64_t row, const Row<T> &r, int t, int threads) {
   if (t == 0 && a.sums_in == nullptr) {
     a.loss[row] = 0.f;
     if (a.sums) a.sums[2 * row] = a.sums[2 * row + 1] = 0.f;
   }
-  if (!r.d) return;
-  const float zero[Row<T>::N] = {};
-  for (int v = t; v < r.full; v += threads) r.put(v, zero);
-  const int at = r.edge(t);
-  if (at >= 0) r.d[at] = from_float<T>(0.f);
+  if (r.d) put_zeros(r, t, threads);
 }
 
 // A row in the registers of a warp (WARP: kRowWarps rows a block, no barrier)
@@ -419,7 +422,7 @@ constexpr int kRowWarps = 4, kMaxWarps = 16;
 template <class T, int NV, bool WARP, bool SMALL>
 __global__ void __launch_bounds__(WARP ? 32 * kRowWarps : 32 * kMaxWarps) k_distill(const DistillArgs a) {
   extern __shared__ uint32_t smem[];
-  __shared__ Sum box[kMaxWarps];
+  __shared__ Sum box[32];
   __shared__ TopSums shared_top;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, top = a.dm.top;
   const int t = WARP ? lane : threadIdx.x, threads = WARP ? 32 : blockDim.x, log_threads = 31 - __clz(threads);
@@ -495,9 +498,10 @@ __global__ void __launch_bounds__(WARP ? 32 * kRowWarps : 32 * kMaxWarps) k_dist
     if (a.sums) a.sums[2 * row] = sum.m, a.sums[2 * row + 1] = sum.s;
   }
   if (!r.d) return;
+  if (p.zero) return put_zeros(r, t, threads);
   float factor = p.rest_scale;
   if (!WARP && factor != 0.f) factor *= share(m, p.m, c);  // a warp's powers are from its own largest value
-  x.put(r, p.zero, factor, t, threads);
+  x.put(r, factor, t, threads);
   if constexpr (WARP)
     __syncwarp();
   else
@@ -512,7 +516,7 @@ template <class T, int U, bool SMALL>
 __global__ void __launch_bounds__(kLongThreads) k_distill_long(const DistillArgs a) {
   constexpr int N = 16 / (int)sizeof(T);
   extern __shared__ uint32_t smem[];
-  __shared__ Sum box[kMaxWarps];
+  __shared__ Sum box[32];
   __shared__ TopSums shared_top;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, threads = blockDim.x;
   const int top = a.dm.top, words = (a.dm.vocab + 8 + 31) / 32;
@@ -523,6 +527,12 @@ __global__ void __launch_bounds__(kLongThreads) k_distill_long(const DistillArgs
   if (w == 0.f) return skip_row(a, row, r, threadIdx.x, threads);
   const bool tail = a.teacher_lse != nullptr, known = a.sums_in != nullptr;
   const float c = a.c;
+  uint4 raw[U];
+  auto load = [&](int v0) {
+#pragma unroll
+    for (int j = 0; j < U; ++j) raw[j] = v0 + j * threads < r.full ? r.vector(v0 + j * threads) : all_low<T>();
+  };
+  load(threadIdx.x);  // on its way while the entries are read
   TopList<SMALL> l(smem, words, top);
   for (int i = threadIdx.x; i < words; i += threads) l.bits[i] = 0;
   __syncthreads();
@@ -547,10 +557,7 @@ __global__ void __launch_bounds__(kLongThreads) k_distill_long(const DistillArgs
       if (!(tail && (l.bits[p.word] & p.bit))) s = pw(to_float(r.z[edge]));
     }
     for (int v0 = threadIdx.x; v0 < r.full; v0 += U * threads) {
-      uint4 raw[U];
       float most = m;
-#pragma unroll
-      for (int j = 0; j < U; ++j) raw[j] = v0 + j * threads < r.full ? r.vector(v0 + j * threads) : all_low<T>();
 #pragma unroll
       for (int j = 0; j < U; ++j) most = fmaxf(most, largest_of<T>(raw[j]));
       if (most > m) {
@@ -568,6 +575,7 @@ __global__ void __launch_bounds__(kLongThreads) k_distill_long(const DistillArgs
         for (int i = 0; i < N; ++i)
           if (!(skip >> i & 1)) s += e[i];
       }
+      load(v0 + U * threads);
     }
     sum = row_join<false>({m, s}, c, box);
     if (tail && sum.s < kSmallRest) sum = small_rest<T, false>(r, l.bits, -1, threadIdx.x, threads, c, box);
@@ -578,21 +586,20 @@ __global__ void __launch_bounds__(kLongThreads) k_distill_long(const DistillArgs
     if (a.sums) a.sums[2 * row] = sum.m, a.sums[2 * row + 1] = sum.s;
   }
   if (!r.d) return;
+  if (p.zero) return put_zeros(r, threadIdx.x, threads);
   const Power pw(p.m, c);
   const F2 factor = f2(p.rest_scale, p.rest_scale);
   for (int v0 = threadIdx.x; v0 < r.full; v0 += U * threads) {
-    uint4 raw[U];
-#pragma unroll
-    for (int j = 0; j < U; ++j) raw[j] = v0 + j * threads < r.full ? r.vector(v0 + j * threads) : all_low<T>();
+    load(v0);
 #pragma unroll
     for (int j = 0; j < U; ++j) {
       if (v0 + j * threads >= r.full) continue;
       float e[N];
       pw.template operator()<T>(raw[j], e);
-      put_scaled(r, v0 + j * threads, e, p.zero, factor);
+      put_scaled(r, v0 + j * threads, e, factor);
     }
   }
-  if (edge >= 0) r.d[edge] = from_float<T>(p.zero ? 0.f : pw(to_float(r.z[edge])) * p.rest_scale);
+  if (edge >= 0) r.d[edge] = from_float<T>(pw(to_float(r.z[edge])) * p.rest_scale);
   __syncthreads();
   if (warp == 0) put_top(a, r, p, ts, l);
 }
