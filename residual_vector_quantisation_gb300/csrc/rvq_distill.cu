@@ -568,12 +568,16 @@ __global__ void __launch_bounds__(kLongThreads) k_distill_long(const DistillArgs
 #pragma unroll
       for (int j = 0; j < U; ++j) {
         const int v = v0 + j * threads, at = v * N + 8;
-        const uint32_t skip = tail && v < r.full ? l.bits[at >> 5] >> (at & 31) : 0;
+        const uint32_t skip = tail && v < r.full ? l.bits[at >> 5] >> (at & 31) & ((1u << N) - 1) : 0;
         float e[N];
         pw.template operator()<T>(raw[j], e);
+        if (skip) {  // rare in a long row
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-          if (!(skip >> i & 1)) s += e[i];
+          for (int i = 0; i < N; ++i)
+            if (skip >> i & 1) e[i] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) s += e[i];
       }
       load(v0 + U * threads);
     }
