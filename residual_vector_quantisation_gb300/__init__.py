@@ -329,19 +329,28 @@ def _at(t: Optional[torch.Tensor], dtype, shape, name: str):
     """Address of a contiguous CUDA tensor of this dtype and shape (None: null)."""
     if t is None:
         return None
-    if not t.is_cuda or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous CUDA tensor of {dtype} and shape {tuple(shape)}")
-    return t.data_ptr()
+    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{name} must be a contiguous CUDA tensor of {dtype} and shape {tuple(shape)}")
 
 
 def _rows_at(t: torch.Tensor, dtype, shape, name: str):
     """Address and row stride of a 2-d CUDA tensor whose rows are contiguous."""
-    if not t.is_cuda or t.dtype is not dtype or t.shape != shape:
+    if t.dtype is not dtype or t.shape != shape or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor of {dtype} and shape {tuple(shape)}")
     stride, one = t.stride()
     if one != 1 and shape[1] > 1 and shape[0] > 0:
         raise ValueError(f"{name} must have contiguous rows")
     return t.data_ptr(), stride
+
+
+def _workspace(t: Optional[torch.Tensor]):
+    """Address and bytes of a workspace."""
+    if t is None:
+        return None, 0
+    if not (t.is_cuda and t.is_contiguous()):
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    return t.data_ptr(), t.nbytes
 
 
 def _dtype_code(t: torch.Tensor, name: str) -> int:
@@ -397,8 +406,7 @@ def rvq_layer_norm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, works
     _check("rvq_layer_norm_backward", load_library().rvq_layer_norm_backward(
         dims, dyp, dys, xp, xs, _at(weight, pd, params, "weight"), _at(mean, torch.float32, rows, "mean"),
         _at(rstd, torch.float32, rows, "rstd"), dxp, dxs, _at(dweight, pd, params, "dweight"),
-        _at(dbias, pd, params, "dbias"), None if workspace is None else _ptr(workspace),
-        0 if workspace is None else workspace.numel() * workspace.element_size(), _raw_stream(x, stream)))
+        _at(dbias, pd, params, "dbias"), *_workspace(workspace), _raw_stream(x, stream)))
 
 
 def _distill_args(logits, top_logits, top_codes, teacher_lse, weights, temperature):
@@ -466,7 +474,7 @@ def rvq_beam_select(dims: rvq_beam_dims, logits, scores, finished, end_code: int
         _at(out_scores, torch.float32, kept, "out_scores"), _at(parents, torch.int32, kept, "parents"),
         _at(codes, torch.int32, kept, "codes"),
         None if out_finished is None else _at(out_finished, out_finished.dtype, kept, "out_finished"),
-        _ptr(workspace), workspace.numel() * workspace.element_size(), _raw_stream(logits, stream)))
+        *_workspace(workspace), _raw_stream(logits, stream)))
 
 
 def rvq_beam_states(pairs, layered: bool = False):

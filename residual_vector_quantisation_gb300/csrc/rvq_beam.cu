@@ -631,23 +631,19 @@ size_t beam_list_at(const rvq_beam_dims &dm, int splits) {
   return align_up((size_t)(dm.groups * dm.beams) * splits * sizeof(float2));
 }
 
-template <class K>
-cudaError_t beam_smem(K kernel, size_t bytes) {
-  return bytes <= 24 * 1024 ? cudaSuccess
-                            : cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-}
-
 template <class T>
 cudaError_t launch_beam(const BeamArgs &a, const BeamPlan &p, cudaStream_t st) {
   if (p.group) {
-    const cudaError_t e = beam_smem(k_beam_group<T>, p.smem);
+    static std::atomic<int> allowed[64];
+    const cudaError_t e = p.smem > 24 * 1024 ? allow_smem(k_beam_group<T>, p.smem, allowed) : cudaSuccess;
     if (e != cudaSuccess) return e;
     k_beam_group<T><<<(unsigned)a.dm.groups, 32 * p.warps, p.smem, st>>>(a);
     return cudaGetLastError();
   }
   k_beam_rows<T><<<(unsigned)(a.dm.groups * a.dm.beams * p.splits), 32 * kRowWarps, 0, st>>>(a);
   cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess) e = beam_smem(k_beam_join, p.smem);
+  static std::atomic<int> allowed[64];
+  if (e == cudaSuccess && p.smem > 24 * 1024) e = allow_smem(k_beam_join, p.smem, allowed);
   if (e != cudaSuccess) return e;
   return launch_next(k_beam_join, dim3((unsigned)a.dm.groups), 256, p.smem, st, a);
 }

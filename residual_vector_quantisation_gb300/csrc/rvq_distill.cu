@@ -245,7 +245,6 @@ struct RowPlan {
   float m, rest_scale, scale, loss, all_m, all_r, u_r;
   bool zero;
 };
-__device__ __forceinline__ float log_fast(float x) { return __log2f(x) * 0.6931471805599453f; }
 
 // The plan from `sum`, the sum over every code (renormalised) or over the
 // codes without an entry (with the tail).
@@ -257,7 +256,7 @@ __device__ __forceinline__ RowPlan plan_row(bool tail, float w, Sum sum, const T
     r.zero = true;
     return r;
   }
-  const float log_all = log_fast(all.s);
+  const float log_all = logf(all.s);
   if (all.s != 0.f) r.all_r = __fdividef(1.f, all.s);
   // sum q_j (log q_j - log p_j), log p_j = log_p + (z_j - z_m) / T
   const float log_p = all.s == 0.f ? -CUDART_INF_F : (t.z_m - all.m) * inv_t - log_all;
@@ -266,15 +265,15 @@ __device__ __forceinline__ RowPlan plan_row(bool tail, float w, Sum sum, const T
     loss = t.u == 0.f ? 0.f : fmaf(-t.u, log_p, t.ul * kDistillMaxTop);
   } else {
     r.u_r = __fdividef(1.f, t.u);
-    loss = t.ul * r.u_r * kDistillMaxTop - log_fast(t.u) - log_p;
+    loss = t.ul * r.u_r * kDistillMaxTop - logf(t.u) - log_p;
   }
   if (t.u != t.u) loss = r.scale = t.u;
   r.rest_scale = __fdividef(r.scale, sum.s);
   if (tail) {
     float q_rest = 1.f - t.u;
     if (q_rest <= kTailFloor) q_rest = 0.f;
-    const float lp_rest = sum.s == 0.f ? -CUDART_INF_F : (sum.m - all.m) * inv_t + (log_fast(sum.s) - log_all);
-    if (q_rest != 0.f) loss = fmaf(q_rest, log_fast(q_rest) - lp_rest, loss);
+    const float lp_rest = sum.s == 0.f ? -CUDART_INF_F : (sum.m - all.m) * inv_t + (logf(sum.s) - log_all);
+    if (q_rest != 0.f) loss = fmaf(q_rest, logf(q_rest) - lp_rest, loss);
     r.rest_scale *= exp2_fast(lp_rest * kLog2e) - q_rest;
   }
   if (sum.s == 0.f) r.m = 0.f, r.rest_scale = 0.f;  // no code off the list has a share
@@ -652,7 +651,8 @@ cudaError_t launch_distill_typed(const DistillArgs &a, cudaStream_t st) {
   const auto kernel = a.dm.top <= 32 ? k_distill_long<T, 4, true> : k_distill_long<T, 4, false>;
   const size_t smem = distill_smem(distill_words(a.dm.vocab, 0), a.dm.top, a.dm.top <= 32);
   if (smem > 40 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static std::atomic<int> allowed[2][64];
+    const cudaError_t e = allow_smem(kernel, smem, allowed[a.dm.top <= 32]);
     if (e != cudaSuccess) return e;
   }
   kernel<<<(unsigned)a.dm.rows, kLongThreads, smem, st>>>(a);

@@ -9,6 +9,7 @@
 #include <math_constants.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "rvq.h"
@@ -23,6 +24,18 @@ inline bool aligned_to(const void *p, uintptr_t a) { return (reinterpret_cast<ui
 // Whether rows of `bytes`-sized elements at p, `stride` elements apart, all start on a 16-byte boundary.
 inline bool rows_aligned16(const void *p, int64_t stride, int64_t rows, int bytes) {
   return aligned_to(p, 16) && (rows <= 1 || (stride * bytes) % 16 == 0);
+}
+
+// Lets a kernel take `bytes` of dynamic shared memory: asked of the runtime once
+// per kernel (the template's instance), device and larger size, not per call.
+template <class K>
+cudaError_t allow_smem(K kernel, size_t bytes, std::atomic<int> (&done)[64]) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || done[dev & 63].load() >= (int)bytes) return e;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess) done[dev & 63].store((int)bytes);
+  return e;
 }
 
 __device__ __forceinline__ float to_float(float v) { return v; }
