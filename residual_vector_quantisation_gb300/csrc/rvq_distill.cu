@@ -418,8 +418,18 @@ __device__ __forceinline__ void skip_row(const DistillArgs &a, int64_t row, cons
 // A row in the registers of a warp (WARP: kRowWarps rows a block, no barrier)
 // or of a block: one read of the logits, one write of the gradient.
 constexpr int kRowWarps = 4, kMaxWarps = 16;
+//
+// What bounds it: the latency of a row's chain (entries, their logits, two
+// reductions) against the rows that an SM holds, so registers are held down to
+// let more rows in: for 96 000 rows of 1025 bf16 with 32 entries 110 us as the
+// compiler would have it (78 registers, 6 blocks an SM), 100 at 7 and 95 at 8
+// blocks; for 384 000 rows of 1024 f32 (two passes) 892 us at 5, 819 at 6, 848
+// at 7, 910 at 8 blocks.  The bytes alone would take 58 and 702 us.  Blocks of
+// more than 512 threads, for rows above 16384, were slower than two reads (89
+// against 73 us for 2000 rows of 30 000 bf16).
 template <class T, int NV, bool WARP, bool SMALL>
-__global__ void __launch_bounds__(WARP ? 32 * kRowWarps : 32 * kMaxWarps) k_distill(const DistillArgs a) {
+__global__ void __launch_bounds__(WARP ? 32 * kRowWarps : 32 * kMaxWarps, WARP ? (sizeof(T) == 4 ? 6 : 8) : 1)
+    k_distill(const DistillArgs a) {
   extern __shared__ uint32_t smem[];
   __shared__ Sum box[32];
   __shared__ TopSums shared_top;
