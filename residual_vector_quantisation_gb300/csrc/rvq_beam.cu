@@ -375,8 +375,12 @@ __device__ __forceinline__ void join_group(const BeamArgs &a, int64_t g, const u
 }
 
 // A block per group: `per` warps' shares of each beam's row, then the join.
+// Bound by the chain of one group (score, row, bar, order, join: about 5 us)
+// against the eight or so groups that an SM holds: 54 us for 12000 groups of 4
+// rows of 1024 floats, whose bytes alone would take 30; with registers held
+// down for more groups (3 and 4 blocks of 512 threads) it spills and loses.
 template <class T>
-__global__ void __launch_bounds__(32 * kGroupWarps) k_beam_group(const BeamArgs a) {
+__global__ void __launch_bounds__(32 * kGroupWarps, 2) k_beam_group(const BeamArgs a) {
   extern __shared__ uint64_t smem[];
   __shared__ Join join;
   const int n = a.dm.select, B = a.dm.beams, lane = threadIdx.x & 31, warps = blockDim.x >> 5, per = a.splits;
@@ -402,6 +406,9 @@ __global__ void __launch_bounds__(32 * kGroupWarps) k_beam_group(const BeamArgs 
 }
 
 // `splits` blocks per row; each leaves its best entries and its part of the sum.
+// 256 rows of 65536 bf16 (34 MB, 5 us of bandwidth) take 21 us here and 6 to 9
+// in the join: a warp reads its 4096 elements at once and then works on them
+// alone.  Half as many vectors a warp and twice the blocks took 25 us.
 template <class T>
 __global__ void __launch_bounds__(32 * kRowWarps) k_beam_rows(const BeamArgs a) {
   __shared__ WarpRoom room[kRowWarps];
