@@ -241,13 +241,13 @@ struct Join {
 };
 
 __device__ __forceinline__ void put_candidate(const BeamArgs &a, int64_t g, int place, uint32_t total, int beam,
-                                              int code) {
+                                              int code, bool done) {
   const int64_t o = g * a.dm.select + place;
   a.out_scores[o] = total ? value_of(total) : -CUDART_INF_F;
   a.parents[o] = total ? beam : -1;
   a.codes[o] = total ? code : -1;
   if (a.out_finished)
-    a.out_finished[o] = !total || (a.finished && a.finished[g * a.dm.beams + beam]) || code == a.end_code;
+    a.out_finished[o] = !total || done || code == a.end_code;
 }
 
 // At most 32 entries: a lane of the first warp has one each.
@@ -257,11 +257,13 @@ __device__ __forceinline__ void join_in_warp(const BeamArgs &a, int64_t g, const
   if (threadIdx.x >= 32) return;
   uint32_t total = 0;
   uint64_t key = 0;
+  bool done = false;
   const int b = lane / n / per;
   if (lane < entries) {
     const int64_t row = g * a.dm.beams + b;
     const float score = a.scores[row];
-    if (beam_live(a, row)) {
+    done = a.finished && a.finished[row];
+    if (score > -CUDART_INF_F && !done) {
       key = list[lane];
       const float v = value_of((uint32_t)(key >> 32));
       if (a.dm.mode == RVQ_BEAM_RAW) {
@@ -282,9 +284,9 @@ __device__ __forceinline__ void join_in_warp(const BeamArgs &a, int64_t g, const
     place += k > mine || (k == mine && t > key);
   }
   const int found = __popc(__ballot_sync(0xffffffffu, total != 0));
-  if (total && place < n) put_candidate(a, g, place, total, b, (int)~(uint32_t)key);
-  if (lane >= found && lane < n) put_candidate(a, g, lane, 0, 0, 0);
-  for (int i = lane + 32; i < n; i += 32) put_candidate(a, g, i, 0, 0, 0);
+  if (total && place < n) put_candidate(a, g, place, total, b, (int)~(uint32_t)key, done);
+  if (lane >= found && lane < n) put_candidate(a, g, lane, 0, 0, 0, true);
+  for (int i = lane + 32; i < n; i += 32) put_candidate(a, g, i, 0, 0, 0, true);
 }
 
 __device__ __forceinline__ void join_group(const BeamArgs &a, int64_t g, const uint64_t *list, const float2 *sum, int per, Join &w) {
@@ -341,7 +343,8 @@ __device__ __forceinline__ void join_group(const BeamArgs &a, int64_t g, const u
   __syncthreads();
   const int all = w.count;
   auto put = [&](int place, uint64_t k, uint64_t tie) {
-    put_candidate(a, g, place, (uint32_t)(k >> 32), (int)~(uint32_t)k, (int)~(uint32_t)tie);
+    const int beam = (int)~(uint32_t)k;
+    put_candidate(a, g, place, (uint32_t)(k >> 32), beam, (int)~(uint32_t)tie, w.done[beam]);
   };
   int found = min(all, n);
   if (all <= kTop) {
@@ -371,7 +374,7 @@ __device__ __forceinline__ void join_group(const BeamArgs &a, int64_t g, const u
       k0 = k, t0 = t;
     }
   }
-  for (int j = found + tid; j < n; j += blockDim.x) put_candidate(a, g, j, 0, 0, 0);
+  for (int j = found + tid; j < n; j += blockDim.x) put_candidate(a, g, j, 0, 0, 0, true);
 }
 
 // A block per group: `per` warps' shares of each beam's row, then the join.
@@ -638,19 +641,19 @@ size_t beam_list_at(const rvq_beam_dims &dm, int splits) {
   return align_up((size_t)(dm.groups * dm.beams) * splits * sizeof(float2));
 }
 
+std::atomic<bool> g_join_allowed[64];
 template <class T>
 cudaError_t launch_beam(const BeamArgs &a, const BeamPlan &p, cudaStream_t st) {
   if (p.group) {
-    static std::atomic<int> allowed[64];
-    const cudaError_t e = p.smem > 24 * 1024 ? allow_smem(k_beam_group<T>, p.smem, allowed) : cudaSuccess;
+    static std::atomic<bool> allowed[64];
+    const cudaError_t e = p.smem > 24 * 1024 ? allow_smem(k_beam_group<T>, allowed) : cudaSuccess;
     if (e != cudaSuccess) return e;
     k_beam_group<T><<<(unsigned)a.dm.groups, 32 * p.warps, p.smem, st>>>(a);
     return cudaGetLastError();
   }
   k_beam_rows<T><<<(unsigned)(a.dm.groups * a.dm.beams * p.splits), 32 * kRowWarps, 0, st>>>(a);
   cudaError_t e = cudaGetLastError();
-  static std::atomic<int> allowed[64];
-  if (e == cudaSuccess && p.smem > 24 * 1024) e = allow_smem(k_beam_join, p.smem, allowed);
+  if (e == cudaSuccess && p.smem > 24 * 1024) e = allow_smem(k_beam_join, g_join_allowed);
   if (e != cudaSuccess) return e;
   return launch_next(k_beam_join, dim3((unsigned)a.dm.groups), 256, p.smem, st, a);
 }

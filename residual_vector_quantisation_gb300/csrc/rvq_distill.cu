@@ -661,8 +661,8 @@ cudaError_t launch_distill_typed(const DistillArgs &a, cudaStream_t st) {
   const auto kernel = a.dm.top <= 32 ? k_distill_long<T, 4, true> : k_distill_long<T, 4, false>;
   const size_t smem = distill_smem(distill_words(a.dm.vocab, 0), a.dm.top, a.dm.top <= 32);
   if (smem > 40 * 1024) {
-    static std::atomic<int> allowed[2][64];
-    const cudaError_t e = allow_smem(kernel, smem, allowed[a.dm.top <= 32]);
+    static std::atomic<bool> allowed[2][64];
+    const cudaError_t e = allow_smem(kernel, allowed[a.dm.top <= 32]);
     if (e != cudaSuccess) return e;
   }
   kernel<<<(unsigned)a.dm.rows, kLongThreads, smem, st>>>(a);

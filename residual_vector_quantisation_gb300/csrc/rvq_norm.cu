@@ -536,7 +536,7 @@ __global__ void __launch_bounds__(kRingThreads)
     }
     stage = (stage + 1) % STAGES;
   }
-  if (part == nullptr) return;
+  if (part == nullptr || blockIdx.x >= rows) return;  // (a block without rows has no part in the workspace)
   copies_wait<0>();
   __syncthreads();
   // the groups' sums through shared memory, added in their order
@@ -656,16 +656,16 @@ cudaError_t launch_ring_shape(NormArgs &a, int threads, bool backward, cudaStrea
     const size_t smem = ring_bytes(block, kBackwardStages, 2, NV);
     const auto kernel = k_norm_backward_ring<T, P, C, WARP, kBackwardStages>;
     a.parts = (int)(blocks < a.dm.rows ? blocks : a.dm.rows);
-    static std::atomic<int> allowed[64];
-    if ((e = allow_smem(kernel, smem, allowed)) != cudaSuccess) return e;
+    static std::atomic<bool> allowed[64];
+    if ((e = allow_smem(kernel, allowed)) != cudaSuccess) return e;
     kernel<<<(unsigned)blocks, block, smem, st>>>(
         static_cast<const T *>(a.dy), a.dys, static_cast<const T *>(a.x), a.xs, static_cast<const P *>(a.weight),
         a.mean, a.rstd, a.dm.rows, a.dm.width, static_cast<T *>(a.out), a.outs, a.part, threads);
   } else {
     const size_t smem = ring_bytes(block, kForwardStages, 1, NV);
     const auto kernel = k_norm_ring<T, P, C, WARP, kForwardStages>;
-    static std::atomic<int> allowed[64];
-    if ((e = allow_smem(kernel, smem, allowed)) != cudaSuccess) return e;
+    static std::atomic<bool> allowed[64];
+    if ((e = allow_smem(kernel, allowed)) != cudaSuccess) return e;
     kernel<<<(unsigned)blocks, block, smem, st>>>(
         static_cast<const T *>(a.x), a.xs, static_cast<const P *>(a.weight), static_cast<const P *>(a.bias), a.dm.eps,
         a.dm.rows, a.dm.width, static_cast<T *>(a.out), a.outs, a.mean_out, a.rstd_out, threads);

@@ -26,15 +26,17 @@ inline bool rows_aligned16(const void *p, int64_t stride, int64_t rows, int byte
   return aligned_to(p, 16) && (rows <= 1 || (stride * bytes) % 16 == 0);
 }
 
-// Lets a kernel take `bytes` of dynamic shared memory: asked of the runtime once
-// per kernel (the template's instance), device and larger size, not per call.
+// Lets a kernel take up to kMostSmem bytes of dynamic shared memory: asked of
+// the runtime once per kernel and device, and always for the same size, so that
+// no call lowers what another one needs.
+constexpr int kMostSmem = 208 * 1024;  // of an SM's 227 KB; the rest is for static arrays
 template <class K>
-cudaError_t allow_smem(K kernel, size_t bytes, std::atomic<int> (&done)[64]) {
+cudaError_t allow_smem(K kernel, std::atomic<bool> (&done)[64]) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess || done[dev & 63].load() >= (int)bytes) return e;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-  if (e == cudaSuccess) done[dev & 63].store((int)bytes);
+  if (e != cudaSuccess || done[dev & 63].load()) return e;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem);
+  if (e == cudaSuccess) done[dev & 63].store(true);
   return e;
 }
 

@@ -10,6 +10,7 @@ from __future__ import annotations
 from typing import Optional
 
 import torch
+from torch.autograd.function import once_differentiable
 
 import residual_vector_quantisation_gb300 as _rq
 
@@ -34,6 +35,7 @@ class _LayerNorm(torch.autograd.Function):
         return y.view(x.shape)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         rows, weight, bias, mean, rstd = ctx.saved_tensors
         need = ctx.needs_input_grad
@@ -72,8 +74,9 @@ def _teacher(logits, top_logits, top_codes, teacher_lse, weights):
                 raise ValueError(f"{name} must have the logits' leading axes")
             t = t.to(torch.float32).reshape(-1).contiguous()
         flat.append(t)
-    return rows, (top_logits.reshape(-1, top).contiguous(), top_codes.to(torch.int32).reshape(-1, top).contiguous(),
-                  *flat)
+    if top_codes.dtype != torch.int32:  # a code past 32 bits stays out of range
+        top_codes = top_codes.clamp(-2, 2 ** 31 - 1).to(torch.int32)
+    return rows, (top_logits.reshape(-1, top).contiguous(), top_codes.reshape(-1, top).contiguous(), *flat)
 
 
 class _Distill(torch.autograd.Function):
@@ -88,6 +91,7 @@ class _Distill(torch.autograd.Function):
         return loss.view(logits.shape[:-1])
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad):
         rows, *teacher, lse = ctx.saved_tensors
         dlogits = torch.empty(rows.shape, dtype=rows.dtype, device=rows.device)
@@ -101,7 +105,8 @@ def distill_loss(logits, top_logits, top_codes, teacher_lse=None, weights=None, 
 
     top_logits, top_codes [...][top]: the teacher's largest logits and their codes (-1: empty); teacher_lse [...]:
     the log sum exp of all the teacher's logits / temperature, where the mass that the list leaves out is to count
-    (rvq_distill in include/rvq.h); weights [...]: a factor per row, 0 for padding.  Runs on the current stream."""
+    (rvq_distill in include/rvq.h); weights [...]: a factor per row, 0 for padding.  The teacher and the weights are
+    constants: no gradient goes to them.  Runs on the current stream."""
     return _Distill.apply(logits, top_logits, top_codes, teacher_lse, weights, float(temperature))
 
 
@@ -156,6 +161,10 @@ class BeamSearch:
         done = torch.empty(kept, dtype=torch.bool, device=self.device) if self.end_code >= 0 else None
         _rq.rvq_beam_select(self.dims, logits, scores, finished, self.end_code, out, parents, codes, done,
                             self.workspace, stream)
+        if stream is not None:
+            for t in (out, parents, codes, done):
+                if t is not None:
+                    t.record_stream(stream)
         return out, parents, codes, done
 
     def reorder(self, parents, state, out=None, layered: bool = False, stream=None):
@@ -167,4 +176,6 @@ class BeamSearch:
             shape[lead + 1] = self.dims.select
             out = torch.empty(shape, dtype=state.dtype, device=state.device)
         _rq.rvq_beam_reorder(self.dims, parents, _rq.rvq_beam_states([(state, out)], layered), stream)
+        if stream is not None:
+            out.record_stream(stream)
         return out

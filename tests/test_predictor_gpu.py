@@ -152,6 +152,25 @@ def test_norm_no_rows_and_parts():
         assert torch.equal(out[k], every[k]), k
 
 
+@pytest.mark.parametrize("rows", [1, 3, 9, 150, 700])
+@pytest.mark.parametrize("width,shift", [(64, 0), (200, 1), (1500, 0), (9000, 0), (9000, 1)])
+def test_norm_stays_in_its_workspace(rows, width, shift):
+    g = gen(rows)
+    x, dy = (rows_of(randn(g, rows, width), 3, shift) for _ in range(2))
+    w = 1 + 0.1 * randn(g, width)
+    mean, rstd = torch.empty(rows, device=DEV), torch.empty(rows, device=DEV)
+    rq.rvq_layer_norm(x, w, None, 1e-5, torch.empty((rows, width), device=DEV), mean, rstd)
+    need = rq.rvq_layer_norm_workspace_bytes(rows, width)
+    buffer = torch.full((need + (1 << 22),), 0xA5, dtype=torch.uint8, device=DEV)
+    dw, db = torch.empty_like(w), torch.empty_like(w)
+    rq.rvq_layer_norm_backward(dy, x, w, mean, rstd, rows_of(torch.zeros((rows, width), device=DEV), 3, shift), dw, db,
+                               buffer[:need])
+    assert bool((buffer[need:] == 0xA5).all())
+    val, tol = ref.norm(x, w, None, 1e-5, dy)
+    ref.check(dw, val["dweight"], tol["dweight"], "dweight")
+    ref.check(db, val["dbias"], tol["dbias"], "dbias")
+
+
 def test_norm_many_rows_and_repeats():
     g = gen(9)
     x, dy = randn(g, 20011, 192).to(BF16), randn(g, 20011, 192).to(BF16)
@@ -329,6 +348,17 @@ def test_distill_list_with_nearly_everything():
     check_distill(z, t, codes, lse, w)
 
 
+def test_distill_codes_past_32_bits_are_not_codes():
+    z, t, codes, lse, w = make_distill(33, 4, 300, 6, F32, False)
+    wide = codes.long()
+    wide[:, 2] += 1 << 32
+    bad = codes.clone()
+    bad[:, 2] = -7
+    want = torch.empty(4, device=DEV)
+    rq.rvq_distill(z, t, bad, None, w, 1.0, want)
+    assert torch.equal(rq.distill_loss(z, t, wide, None, w), want)
+
+
 def test_distill_no_rows_weights_and_repeats():
     z, t, codes, lse, _ = make_distill(31, 0, 100, 4, F32, True)
     run_distill(z, t, codes, lse, None, 1.0)
@@ -485,6 +515,24 @@ def test_beam_strides(pad, shift, dtype):
         got = search.select(view, scores)
         for a, b in zip(got[1:3], want[1:]):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("groups,beams,vocab,select", [(3, 4, 1025, 4), (2, 8, 4096, 8), (1, 4, 70000, 4),
+                                                       (5, 12, 9000, 12), (1, 64, 40000, 64)])
+def test_beam_workspace_and_outputs_over_inputs(groups, beams, vocab, select):
+    logits, scores = make_beam(vocab, groups, beams, vocab, F32)
+    finished = torch.zeros((groups, beams), dtype=torch.bool, device=DEV)
+    finished[0, 1] = True
+    search = rq.BeamSearch(groups, beams, vocab, select, end_code=3)
+    want = search.select(logits, scores, finished)
+    need = search.workspace.numel()
+    buffer = torch.full((need + (1 << 20),), 0xA5, dtype=torch.uint8, device=DEV)
+    parents, codes = (torch.empty((groups, select), dtype=torch.int32, device=DEV) for _ in range(2))
+    held, done = scores.clone(), finished.clone()
+    rq.rvq_beam_select(search.dims, logits, held, done, 3, held, parents, codes, done, buffer[:need])
+    for a, b in zip((held, parents, codes, done), want):
+        assert torch.equal(a, b)
+    assert bool((buffer[need:] == 0xA5).all())
 
 
 def test_beam_offsets_past_32_bits():
