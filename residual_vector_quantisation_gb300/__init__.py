@@ -353,11 +353,10 @@ def _workspace(t: Optional[torch.Tensor]):
     return t.data_ptr(), t.nbytes
 
 
-def _dtype_code(t: torch.Tensor, name: str) -> int:
-    code = DTYPES.get(t.dtype)
-    if code is None or t.dim() != 2:
+def _shape2(t: torch.Tensor, name: str):
+    if t.dim() != 2 or t.dtype not in DTYPES:
         raise ValueError(f"{name} must be a 2-d tensor of float32, bfloat16 or float16")
-    return code
+    return t.shape
 
 
 def _raw_stream(t: torch.Tensor, stream) -> int:
@@ -367,57 +366,53 @@ def _raw_stream(t: torch.Tensor, stream) -> int:
     return torch._C._cuda_getCurrentRawStream(t.device.index)
 
 
-def _norm_dims(x, weight, bias, eps) -> rvq_norm_dims:
-    code = _dtype_code(x, "x")
-    p = weight if weight is not None else bias
-    return rvq_norm_dims(x.shape[0], x.shape[1], code, 0 if p is None else DTYPES.get(p.dtype, -1), eps)
-
-
 def rvq_layer_norm_workspace_bytes(rows: int, width: int) -> int:
     return load_library().rvq_layer_norm_workspace_bytes(int(rows), int(width))
 
 
 def rvq_layer_norm(x, weight, bias, eps: float, y, mean=None, rstd=None, stream=None) -> None:
     """Layer norm of the rows of x [rows][width] into y (see rvq.h); mean and rstd [rows] are optional outputs."""
-    shape, dtype = x.shape, x.dtype
-    dims = _norm_dims(x, weight, bias, eps)
+    shape, dtype = _shape2(x, "x"), x.dtype
+    rows, width = shape
+    p = weight if weight is not None else bias
+    pd = torch.float32 if p is None else p.dtype
     xp, xs = _rows_at(x, dtype, shape, "x")
     yp, ys = _rows_at(y, dtype, shape, "y")
-    p = weight if weight is not None else bias
-    params, rows = shape[1:], shape[:1]
     _check("rvq_layer_norm", load_library().rvq_layer_norm(
-        dims, xp, xs, _at(weight, p.dtype if p is not None else None, params, "weight"),
-        _at(bias, p.dtype if p is not None else None, params, "bias"), yp, ys,
-        _at(mean, torch.float32, rows, "mean"), _at(rstd, torch.float32, rows, "rstd"), _raw_stream(x, stream)))
+        rvq_norm_dims(rows, width, DTYPES[dtype], DTYPES.get(pd, -1), eps), xp, xs, _at(weight, pd, (width,), "weight"),
+        _at(bias, pd, (width,), "bias"), yp, ys, _at(mean, torch.float32, (rows,), "mean"),
+        _at(rstd, torch.float32, (rows,), "rstd"), _raw_stream(x, stream)))
 
 
 def rvq_layer_norm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, workspace, stream=None) -> None:
     """Gradients of rvq_layer_norm; dx, dweight and dbias may each be None (not computed)."""
-    shape, dtype = x.shape, x.dtype
+    shape, dtype = _shape2(x, "x"), x.dtype
+    rows, width = shape
     p = weight if weight is not None else dweight if dweight is not None else dbias
-    dims = _norm_dims(x, p, None, 0.0)
+    pd = torch.float32 if p is None else p.dtype
     dyp, dys = _rows_at(dy, dtype, shape, "dy")
     xp, xs = _rows_at(x, dtype, shape, "x")
     dxp, dxs = (None, 0) if dx is None else _rows_at(dx, dtype, shape, "dx")
-    pd = None if p is None else p.dtype
-    params, rows = shape[1:], shape[:1]
     if mean is None or rstd is None:
         raise ValueError("rvq_layer_norm_backward needs the forward pass's mean and rstd")
     _check("rvq_layer_norm_backward", load_library().rvq_layer_norm_backward(
-        dims, dyp, dys, xp, xs, _at(weight, pd, params, "weight"), _at(mean, torch.float32, rows, "mean"),
-        _at(rstd, torch.float32, rows, "rstd"), dxp, dxs, _at(dweight, pd, params, "dweight"),
-        _at(dbias, pd, params, "dbias"), *_workspace(workspace), _raw_stream(x, stream)))
+        rvq_norm_dims(rows, width, DTYPES[dtype], DTYPES.get(pd, -1), 0.0), dyp, dys, xp, xs,
+        _at(weight, pd, (width,), "weight"), _at(mean, torch.float32, (rows,), "mean"),
+        _at(rstd, torch.float32, (rows,), "rstd"), dxp, dxs, _at(dweight, pd, (width,), "dweight"),
+        _at(dbias, pd, (width,), "dbias"), *_workspace(workspace), _raw_stream(x, stream)))
 
 
 def _distill_args(logits, top_logits, top_codes, teacher_lse, weights, temperature):
-    dims = rvq_distill_dims(logits.shape[0], logits.shape[1], top_logits.shape[-1], _dtype_code(logits, "logits"),
-                            _dtype_code(top_logits, "top_logits"), temperature)
-    entries, rows = (logits.shape[0], top_logits.shape[1]), logits.shape[:1]
-    zp, zs = _rows_at(logits, logits.dtype, logits.shape, "logits")
-    return dims, rows, zp, zs, (_at(top_logits, top_logits.dtype, entries, "top_logits"),
-                                _at(top_codes, torch.int32, entries, "top_codes"),
-                                _at(teacher_lse, torch.float32, rows, "teacher_lse"),
-                                _at(weights, torch.float32, rows, "weights"))
+    rows, vocab = shape = _shape2(logits, "logits")
+    entries = _shape2(top_logits, "top_logits")
+    if entries[0] != rows:
+        raise ValueError("top_logits must have the logits' rows")
+    dims = rvq_distill_dims(rows, vocab, entries[1], DTYPES[logits.dtype], DTYPES[top_logits.dtype], temperature)
+    zp, zs = _rows_at(logits, logits.dtype, shape, "logits")
+    return dims, (rows,), zp, zs, (_at(top_logits, top_logits.dtype, entries, "top_logits"),
+                                   _at(top_codes, torch.int32, entries, "top_codes"),
+                                   _at(teacher_lse, torch.float32, (rows,), "teacher_lse"),
+                                   _at(weights, torch.float32, (rows,), "weights"))
 
 
 def rvq_distill(logits, top_logits, top_codes, teacher_lse, weights, temperature: float, loss, lse=None, dlogits=None,
