@@ -111,7 +111,7 @@ struct TopList {
   int32_t *codes;
   float *ts, *zs;
   int code;
-  float t, z;
+  float t, z;  // SMALL
   __device__ __forceinline__ TopList(uint32_t *at, int words, int top) : bits(at) {
     codes = reinterpret_cast<int32_t *>(at + words);
     ts = reinterpret_cast<float *>(codes + top), zs = ts + top;
@@ -272,9 +272,11 @@ __device__ __forceinline__ RowPlan plan_row(bool tail, float w, Sum sum, const T
   if (tail) {
     float q_rest = 1.f - t.u;
     if (q_rest <= kTailFloor) q_rest = 0.f;
-    const float lp_rest = sum.s == 0.f ? -CUDART_INF_F : (sum.m - all.m) * inv_t + (logf(sum.s) - log_all);
-    if (q_rest != 0.f) loss = fmaf(q_rest, logf(q_rest) - lp_rest, loss);
-    r.rest_scale *= exp2_fast(lp_rest * kLog2e) - q_rest;
+    // log q_r - log p_r, p_r = (sum.s / all.s) e^((sum.m - all.m) / T)
+    const float ratio = sum.s == 0.f ? CUDART_INF_F
+                                     : logf(__fdividef(q_rest * all.s, sum.s)) - (sum.m - all.m) * inv_t;
+    if (q_rest != 0.f) loss = fmaf(q_rest, ratio, loss);
+    r.rest_scale *= sum.s * share(sum.m, all.m, c) * r.all_r - q_rest;
   }
   if (sum.s == 0.f) r.m = 0.f, r.rest_scale = 0.f;  // no code off the list has a share
   r.loss = loss * w;
@@ -332,12 +334,13 @@ template <class T, int NV>
 struct Share {
   static constexpr int N = 16 / (int)sizeof(T);
   float e[NV][N], edge;
+  int edge_at;
   uint4 raw[NV];
   __device__ __forceinline__ void load(const Row<T> &r, int t, int threads) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) raw[j] = t + j * threads < r.full ? r.vector(t + j * threads) : all_low<T>();
-    const int at = r.edge(t);
-    edge = at >= 0 ? to_float(r.z[at]) : -CUDART_INF_F;
+    edge_at = r.edge(t);
+    edge = edge_at >= 0 ? to_float(r.z[edge_at]) : -CUDART_INF_F;
   }
   __device__ __forceinline__ float most() const {
     float m = edge;
@@ -363,8 +366,7 @@ struct Share {
 #pragma unroll
     for (int j = 0; j < NV; ++j)
       if (t + j * threads < r.full) put_scaled(r, t + j * threads, e[j], factors);
-    const int at = r.edge(t);
-    if (at >= 0) r.d[at] = from_float<T>(edge * factor);
+    if (edge_at >= 0) r.d[edge_at] = from_float<T>(edge * factor);
   }
 };
 
