@@ -419,7 +419,6 @@ __device__ __forceinline__ void skip_row(const DistillArgs &a, int64_t row, cons
 
 // A row in the registers of a warp (WARP: kRowWarps rows a block, no barrier)
 // or of a block: one read of the logits, one write of the gradient.
-constexpr int kRowWarps = 4, kMaxWarps = 16;
 //
 // What bounds it: the latency of a row's chain (entries, their logits, two
 // reductions) against the rows that an SM holds, so registers are held down to
@@ -430,6 +429,7 @@ constexpr int kRowWarps = 4, kMaxWarps = 16;
 // row).  The bytes alone would take 58 and 702 us.  Blocks of
 // more than 512 threads, for rows above 16384, were slower than two reads (89
 // against 73 us for 2000 rows of 30 000 bf16).
+constexpr int kRowWarps = 4, kMaxWarps = 16;
 template <class T, int NV, bool WARP, bool SMALL>
 __global__ void __launch_bounds__(WARP ? 32 * kRowWarps : 32 * kMaxWarps, WARP ? (sizeof(T) == 4 ? 6 : 8) : 1)
     k_distill(const DistillArgs a) {
