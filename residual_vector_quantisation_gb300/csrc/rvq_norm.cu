@@ -1,8 +1,8 @@
 // Layer norm over rows, forward and backward (rvq_layer_norm,
 // rvq_layer_norm_backward).
 //
-// A row is read once: a warp per row up to 1024 columns, a group of 64 .. 512
-// threads per row above, up to 32 columns a thread.  The variance is the mean
+// A row is read once: 8, 16 or 32 lanes per row up to 1024 columns, a group of
+// 64 .. 512 threads per row above, up to 32 columns a thread.  The variance is the mean
 // square of the centred values, so a row with a large mean loses nothing.
 //
 // k_norm_ring and k_norm_backward_ring (up to 8192 columns) are what bandwidth
@@ -300,13 +300,16 @@ __device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_gro
 template <int LEFT>
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
 
-// The sum of K values over a row's group of `tpr` threads (a warp, or more
-// through `box`: two halves used in turn, one barrier of the group a call).
-template <int K, bool WARP>
+// The sum of K values over a row's group: LANES lanes of a warp, or (LANES 0)
+// `tpr` threads, whole warps, through `box` (two halves used in turn, one
+// barrier of the group a call).
+template <int K, int LANES>
 __device__ __forceinline__ void group_sum(float (&v)[K], float (*box)[K][16], int &turn, int group, int tpr) {
 #pragma unroll
-  for (int k = 0; k < K; ++k) v[k] = warp_sum(v[k]);
-  if constexpr (!WARP) {
+  for (int k = 0; k < K; ++k)
+#pragma unroll
+    for (int o = (LANES ? LANES : 32) / 2; o; o >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+  if constexpr (LANES == 0) {
     const int lane = threadIdx.x & 31, warp = (threadIdx.x % tpr) >> 5, warps = tpr >> 5;
     float(*at)[16] = box[group * 2 + (turn & 1)];
     ++turn;
@@ -355,14 +358,14 @@ inline size_t ring_bytes(int threads, int stages, int arrays, int nv) {
   return (size_t)threads * stages * (arrays * nv * 16 + (arrays > 1 ? 8 : 0));
 }
 
-template <class T, class P, int C, bool WARP, int STAGES>
+template <class T, class P, int C, int LANES, int STAGES>
 __global__ void __launch_bounds__(kRingForward, 2)
     k_norm_ring(const T *x, int64_t xs, const P *__restrict__ weight, const P *__restrict__ bias, float eps,
                 int64_t rows, int width, T *y, int64_t ys, float *mean, float *rstd, int tpr_) {
   constexpr int N = 16 / (int)sizeof(T), NV = C / N;
   extern __shared__ uint4 ring[];
   __shared__ float box[2 * kRingThreads / 64][1][16];
-  const int tpr = WARP ? 32 : tpr_, group = threadIdx.x / tpr, groups = blockDim.x / tpr;
+  const int tpr = LANES ? LANES : tpr_, group = threadIdx.x / tpr, groups = blockDim.x / tpr;
   const int64_t step = (int64_t)gridDim.x * groups, first = blockIdx.x + (int64_t)group * gridDim.x;
   const Columns<N, NV> c(x + (int64_t)blockIdx.x * xs, sizeof(T), width, tpr, threadIdx.x % tpr);
   const float inv = 1.f / (float)width;
@@ -378,6 +381,9 @@ __global__ void __launch_bounds__(kRingForward, 2)
 #pragma unroll
       for (int j = 0; j < NV; ++j)
         if (c.has(j)) copy16((uint32_t)__cvta_generic_to_shared(slot + (stage * NV + j) * blockDim.x), xr + c.column(j));
+    } else if (LANES) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) slot[(stage * NV + j) * blockDim.x] = make_uint4(0, 0, 0, 0);
     }
     copies_end();
   };
@@ -385,10 +391,14 @@ __global__ void __launch_bounds__(kRingForward, 2)
   for (int k = 0; k < STAGES - 1; ++k) fetch(first + k * step, k);
   float e_next = c.edge >= 0 && first < rows ? to_float(x[first * xs + c.edge]) : 0.f;
   int turn = 0, stage = 0;
-  for (int64_t row = first; row < rows; row += step) {
+  // the groups of a warp stay together: a row past the end holds zeros and leaves nothing
+  constexpr int kPerWarp = LANES ? 32 / (LANES ? LANES : 32) : 1;
+  const int64_t ahead = (int64_t)(group % kPerWarp) * gridDim.x;
+  for (int64_t row = first; row - ahead < rows; row += step) {
+    const bool there = row < rows;
     fetch(row + (STAGES - 1) * step, (stage + STAGES - 1) % STAGES);
     const float e = e_next;
-    if (c.edge >= 0 && row + step < rows) e_next = to_float(x[(row + step) * xs + c.edge]);
+    e_next = c.edge >= 0 && row + step < rows ? to_float(x[(row + step) * xs + c.edge]) : 0.f;
     copies_wait<STAGES - 1>();
     float f[NV][N], s[1] = {e};
 #pragma unroll
@@ -397,7 +407,7 @@ __global__ void __launch_bounds__(kRingForward, 2)
 #pragma unroll
       for (int i = 0; i < N; ++i) s[0] += f[j][i];
     }
-    group_sum<1, WARP>(s, box, turn, group, tpr);
+    group_sum<1, LANES>(s, box, turn, group, tpr);
     const float mu = s[0] * inv;
     s[0] = c.edge >= 0 ? (e - mu) * (e - mu) : 0.f;
 #pragma unroll
@@ -410,28 +420,28 @@ __global__ void __launch_bounds__(kRingForward, 2)
       }
       if (c.has(j)) s[0] += q;
     }
-    group_sum<1, WARP>(s, box, turn, group, tpr);
+    group_sum<1, LANES>(s, box, turn, group, tpr);
     const float r = 1.f / sqrtf(fmaf(s[0], inv, eps));
-    if (c.t == 0) {
+    if (c.t == 0 && there) {
       if (mean) mean[row] = mu;
       if (rstd) rstd[row] = r;
     }
     T *yr = y + row * ys;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      if (!c.has(j)) continue;
+      if (!c.has(j) || !there) continue;
 #pragma unroll
       for (int i = 0; i < N; ++i) f[j][i] = fmaf(f[j][i] * r, g[j][i], b[j][i]);
       *reinterpret_cast<uint4 *>(yr + c.column(j)) = pack16<T>(f[j]);
     }
-    if (c.edge >= 0) yr[c.edge] = from_float<T>(fmaf((e - mu) * r, ge, be));
+    if (c.edge >= 0 && there) yr[c.edge] = from_float<T>(fmaf((e - mu) * r, ge, be));
     stage = (stage + 1) % STAGES;
   }
 }
 
 // dx per row, and each block's sums of dy * h and dy over its rows into
 // part[block][2][width].
-template <class T, class P, int C, bool WARP, int STAGES>
+template <class T, class P, int C, int LANES, int STAGES>
 __global__ void __launch_bounds__(kRingThreads)
     k_norm_backward_ring(const T *dy, int64_t dys, const T *x, int64_t xs, const P *__restrict__ weight,
                          const float *__restrict__ mean, const float *__restrict__ rstd, int64_t rows, int width, T *dx,
@@ -439,7 +449,7 @@ __global__ void __launch_bounds__(kRingThreads)
   constexpr int N = 16 / (int)sizeof(T), NV = C / N, H = N / 2;
   extern __shared__ uint4 ring[];
   __shared__ float box[2 * kRingThreads / 64][2][16];
-  const int tpr = WARP ? 32 : tpr_, group = threadIdx.x / tpr, groups = blockDim.x / tpr;
+  const int tpr = LANES ? LANES : tpr_, group = threadIdx.x / tpr, groups = blockDim.x / tpr;
   const int64_t step = (int64_t)gridDim.x * groups, first = blockIdx.x + (int64_t)group * gridDim.x;
   const Columns<N, NV> c(x + (int64_t)blockIdx.x * xs, sizeof(T), width, tpr, threadIdx.x % tpr);
   const float inv = 1.f / (float)width;
@@ -473,6 +483,11 @@ __global__ void __launch_bounds__(kRingThreads)
       const uint32_t at = (uint32_t)__cvta_generic_to_shared(stat + stage * blockDim.x);
       copy4(at, mean + row);
       copy4(at + 4, rstd + row);
+    } else if (LANES) {
+      asm volatile("" ::: "memory");  // after the last reading of these slots
+#pragma unroll
+      for (int j = 0; j < 2 * NV; ++j) slot[(stage * 2 * NV + j) * blockDim.x] = make_uint4(0, 0, 0, 0);
+      stat[stage * blockDim.x] = make_float2(0.f, 0.f);
     }
     copies_end();
   };
@@ -482,9 +497,14 @@ __global__ void __launch_bounds__(kRingThreads)
   if (c.edge >= 0 && first < rows)
     xe_next = to_float(x[first * xs + c.edge]), de_next = to_float(dy[first * dys + c.edge]);
   int turn = 0, stage = 0;
-  for (int64_t row = first; row < rows; row += step) {
+  // the groups of a warp stay together: a row past the end holds zeros and leaves nothing
+  constexpr int kPerWarp = LANES ? 32 / (LANES ? LANES : 32) : 1;
+  const int64_t ahead = (int64_t)(group % kPerWarp) * gridDim.x;
+  for (int64_t row = first; row - ahead < rows; row += step) {
+    const bool there = row < rows;
     fetch(row + (STAGES - 1) * step, (stage + STAGES - 1) % STAGES);
     const float xe = xe_next, de = de_next;
+    xe_next = de_next = 0.f;
     if (c.edge >= 0 && row + step < rows)
       xe_next = to_float(x[(row + step) * xs + c.edge]), de_next = to_float(dy[(row + step) * dys + c.edge]);
     copies_wait<STAGES - 1>();
@@ -516,14 +536,14 @@ __global__ void __launch_bounds__(kRingThreads)
       const float2 a0 = floats(s0), a1 = floats(s1);
       float s[2] = {a0.x + a0.y, a1.x + a1.y};
       if (c.edge >= 0) s[0] += de * ge, s[1] = fmaf(de * ge, he, s[1]);
-      group_sum<2, WARP>(s, box, turn, group, tpr);
-      if constexpr (WARP) __syncwarp();  // the second reading of the row stays below: moved up, it spills
+      group_sum<2, LANES>(s, box, turn, group, tpr);
+      if constexpr (LANES != 0) __syncwarp();  // the second reading of the row stays below: moved up, it spills
       const float m1 = s[0] * inv, m2 = s[1] * inv;
       const F2 minus1 = f2(-m1, -m1), minus2 = f2(-m2, -m2);
       T *dxr = dx + row * dxs;
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        if (!c.has(j)) continue;
+        if (!c.has(j) || !there) continue;
         F2 f[H], d[H];
         unpack_pairs<T>(read16(xv + j * blockDim.x), f);
         unpack_pairs<T>(read16(dv + j * blockDim.x), d);
@@ -532,7 +552,7 @@ __global__ void __launch_bounds__(kRingThreads)
           f[i] = fma2((f[i] + mu2) * r2, minus2, fma2(d[i], g[j][i], minus1)) * r2;
         *reinterpret_cast<uint4 *>(dxr + c.column(j)) = pack_pairs<T>(f);
       }
-      if (c.edge >= 0) dxr[c.edge] = from_float<T>(r * (fmaf(de, ge, -m1) - he * m2));
+      if (c.edge >= 0 && there) dxr[c.edge] = from_float<T>(r * (fmaf(de, ge, -m1) - he * m2));
     }
     stage = (stage + 1) % STAGES;
   }
@@ -592,9 +612,9 @@ struct NormShape {
   int threads;  // of a row
   int columns;  // of a thread (C)
 };
-inline NormShape norm_shape(int width, int n) {
+inline NormShape norm_shape(int width, int n, int least = 32) {
   const int units = n == 1 ? width : width / n;  // (vectors: the columns beside them are extra)
-  int threads = 32;
+  int threads = least;
   while (threads * 32 < units * n) threads *= 2;
   const int c = ((units + threads - 1) / threads * n + 7) / 8 * 8;
   return {threads, c < 8 ? 8 : c};
@@ -639,7 +659,7 @@ cudaError_t launch_norm_shape(NormArgs &a, int threads, bool backward, cudaStrea
   return cudaGetLastError();
 }
 
-template <class T, class P, int C, bool WARP>
+template <class T, class P, int C, int LANES>  // LANES of a row, or 0: whole warps
 cudaError_t launch_ring_shape(NormArgs &a, int threads, bool backward, cudaStream_t st) {
   constexpr int NV = C * (int)sizeof(T) / 16;
   constexpr int kForwardStages = sizeof(T) == 4 ? 3 : 4, kBackwardStages = sizeof(T) == 4 ? 2 : 3;
@@ -648,13 +668,15 @@ cudaError_t launch_ring_shape(NormArgs &a, int threads, bool backward, cudaStrea
   const int sms = backward ? kSms : 2 * kSms, most = (backward ? kRingThreads : kRingForward) / threads;
   int64_t groups = (a.dm.rows + sms - 1) / sms;
   groups = groups > most ? most : groups;
+  constexpr int kPerWarp = LANES ? 32 / (LANES ? LANES : 32) : 1;
+  groups = (groups + kPerWarp - 1) / kPerWarp * kPerWarp;  // whole warps
   int64_t blocks = ((a.dm.rows + groups - 1) / groups + 7) / 8 * 8;
   blocks = blocks > sms ? sms : blocks;
   const int block = (int)groups * threads;
   cudaError_t e;
   if (backward) {
     const size_t smem = ring_bytes(block, kBackwardStages, 2, NV);
-    const auto kernel = k_norm_backward_ring<T, P, C, WARP, kBackwardStages>;
+    const auto kernel = k_norm_backward_ring<T, P, C, LANES, kBackwardStages>;
     a.parts = (int)(blocks < a.dm.rows ? blocks : a.dm.rows);
     static std::atomic<bool> allowed[64];
     if ((e = allow_smem(kernel, allowed)) != cudaSuccess) return e;
@@ -663,7 +685,7 @@ cudaError_t launch_ring_shape(NormArgs &a, int threads, bool backward, cudaStrea
         a.mean, a.rstd, a.dm.rows, a.dm.width, static_cast<T *>(a.out), a.outs, a.part, threads);
   } else {
     const size_t smem = ring_bytes(block, kForwardStages, 1, NV);
-    const auto kernel = k_norm_ring<T, P, C, WARP, kForwardStages>;
+    const auto kernel = k_norm_ring<T, P, C, LANES, kForwardStages>;
     static std::atomic<bool> allowed[64];
     if ((e = allow_smem(kernel, allowed)) != cudaSuccess) return e;
     kernel<<<(unsigned)blocks, block, smem, st>>>(
@@ -678,18 +700,31 @@ enum NormPath { kRing, kVectors, kElements };
 template <class T, class P>
 cudaError_t launch_norm_typed(NormArgs &a, NormPath path, bool backward, cudaStream_t st) {
   constexpr int N = 16 / (int)sizeof(T);
-  const NormShape s = norm_shape(a.dm.width, path == kElements ? 1 : N);
   if (path == kRing) {
+    // narrow rows share a warp: 8 or 16 lanes each.  The elements beside the vectors need 2 N threads.
+    const bool whole = rows_aligned16(a.x, a.xs, a.dm.rows, sizeof(T)) && a.dm.width % N == 0;
+    const NormShape s = norm_shape(a.dm.width, N, whole || N == 4 ? 8 : 16);
     if (s.threads > 32)  // a thread holds more than 16 columns
-      return s.columns <= 24 ? launch_ring_shape<T, P, 24, false>(a, s.threads, backward, st)
-                             : launch_ring_shape<T, P, 32, false>(a, s.threads, backward, st);
+      return s.columns <= 24 ? launch_ring_shape<T, P, 24, 0>(a, s.threads, backward, st)
+                             : launch_ring_shape<T, P, 32, 0>(a, s.threads, backward, st);
+    if (s.threads == 32)
+      return s.columns <= 24 ? launch_ring_shape<T, P, 24, 32>(a, 32, backward, st)
+                             : launch_ring_shape<T, P, 32, 32>(a, 32, backward, st);
+    if (s.threads == 16)
+      switch (s.columns) {
+        case 8: return launch_ring_shape<T, P, 8, 16>(a, 16, backward, st);
+        case 16: return launch_ring_shape<T, P, 16, 16>(a, 16, backward, st);
+        case 24: return launch_ring_shape<T, P, 24, 16>(a, 16, backward, st);
+        default: return launch_ring_shape<T, P, 32, 16>(a, 16, backward, st);
+      }
     switch (s.columns) {
-      case 8: return launch_ring_shape<T, P, 8, true>(a, 32, backward, st);
-      case 16: return launch_ring_shape<T, P, 16, true>(a, 32, backward, st);
-      case 24: return launch_ring_shape<T, P, 24, true>(a, 32, backward, st);
-      default: return launch_ring_shape<T, P, 32, true>(a, 32, backward, st);
+      case 8: return launch_ring_shape<T, P, 8, 8>(a, 8, backward, st);
+      case 16: return launch_ring_shape<T, P, 16, 8>(a, 8, backward, st);
+      case 24: return launch_ring_shape<T, P, 24, 8>(a, 8, backward, st);
+      default: return launch_ring_shape<T, P, 32, 8>(a, 8, backward, st);
     }
   }
+  const NormShape s = norm_shape(a.dm.width, path == kElements ? 1 : N);
   if (path == kVectors)  // above kRingWidth
     return s.columns <= 24 ? launch_norm_shape<T, P, N, 24, false>(a, s.threads, backward, st)
                            : launch_norm_shape<T, P, N, 32, false>(a, s.threads, backward, st);

@@ -171,6 +171,22 @@ def test_norm_stays_in_its_workspace(rows, width, shift):
     ref.check(db, val["dbias"], tol["dbias"], "dbias")
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("width", [1, 5, 8, 31, 48, 64, 96, 130, 248, 256, 257, 300, 352, 500, 512, 519])
+def test_norm_narrow_rows_share_a_warp(width, dtype):
+    """Row counts that leave a warp's last rows, and a block's, without work; rows that start inside a vector."""
+    g = gen(width)
+    w, b = 1 + 0.2 * randn(g, width), 0.3 * randn(g, width)
+    for rows, pad, shift in ((1, 0, 0), (7, 0, 0), (153, 3, 1), (1219, 8, 0), (5003, 1, 2)):
+        x, dy = randn(g, rows, width).to(dtype), randn(g, rows, width).to(dtype)
+        xv, dyv = rows_of(x, pad, shift), rows_of(dy, pad, shift)
+        out = [rows_of(torch.zeros_like(x), pad, shift) for _ in range(2)]
+        check_norm(run_norm(xv, w, b, 1e-5, dyv, out), x, w, b, 1e-5, dy)
+        for t in out:
+            buffer = torch.empty(0, dtype=dtype, device=DEV).set_(t.untyped_storage())
+            assert int(torch.isnan(buffer).sum()) == buffer.numel() - t.numel()
+
+
 def test_norm_many_rows_and_repeats():
     g = gen(9)
     x, dy = randn(g, 20011, 192).to(BF16), randn(g, 20011, 192).to(BF16)
