@@ -464,8 +464,9 @@ __global__ void __launch_bounds__(256) k_beam_join(const BeamArgs a) {
   float2 *sum = reinterpret_cast<float2 *>(smem + (size_t)lists * n);
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
-  for (int i = threadIdx.x; i < lists * n; i += blockDim.x) smem[i] = a.parts.list[g * lists * n + i];
-  for (int i = threadIdx.x; i < lists; i += blockDim.x) sum[i] = a.parts.sum[g * lists + i];
+  const auto *from = reinterpret_cast<const unsigned long long *>(a.parts.list) + g * lists * n;
+  for (int i = threadIdx.x; i < lists * n; i += blockDim.x) smem[i] = __ldcg(from + i);
+  for (int i = threadIdx.x; i < lists; i += blockDim.x) sum[i] = __ldcg(a.parts.sum + g * lists + i);
   __syncthreads();
   join_group(a, g, smem, sum, a.splits, join);
 }
@@ -529,8 +530,8 @@ inline int move_words(int select, int64_t rows, int64_t words) {
 }
 
 __global__ void __launch_bounds__(kMoveThreads)
-    k_beam_reorder(const __grid_constant__ StateList list, const int32_t *__restrict__ parents, int64_t groups,
-                   int beams, int select, int piece_words) {
+    k_beam_reorder(const __grid_constant__ StateList list, const int32_t *parents, int64_t groups, int beams,
+                   int select, int piece_words) {
   const rvq_beam_state &s = list.s[blockIdx.z];
   const int word = state_word(s);
   const int64_t pieces = (s.row_bytes / word + piece_words - 1) / piece_words;
@@ -553,8 +554,8 @@ __global__ void __launch_bounds__(kMoveThreads)
 // shared memory, W bytes a lane at a time.
 template <class W>
 __global__ void __launch_bounds__(kMoveThreads)
-    k_beam_reorder_in_place(const __grid_constant__ StateList list, const int32_t *__restrict__ parents,
-                            int64_t groups, int beams) {
+    k_beam_reorder_in_place(const __grid_constant__ StateList list, const int32_t *parents, int64_t groups,
+                            int beams) {
   constexpr int kCols = 32;
   __shared__ W tile[kBeamMax][kCols];
   const rvq_beam_state s = list.s[blockIdx.z];
@@ -581,7 +582,9 @@ __global__ void __launch_bounds__(kMoveThreads)
 }
 
 // A kernel that may be brought up while the one before it on the stream ends:
-// it waits (griddep_wait) before it reads or writes anything.
+// it waits (griddep_wait) before it reads or writes anything.  What the kernel
+// before it writes (the parents, the lists) is no read-only data of this one: its
+// pointers are neither __restrict__ nor read by the non-coherent path.
 template <class... P, class... A>
 cudaError_t launch_next(void (*kernel)(P...), dim3 grid, int block, size_t smem, cudaStream_t st, const A &...args) {
   cudaLaunchConfig_t cfg{};

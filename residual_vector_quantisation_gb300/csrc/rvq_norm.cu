@@ -582,11 +582,12 @@ __global__ void __launch_bounds__(kRingThreads)
 }
 
 // The blocks' sums, added in a fixed order: 32 columns a block, 32 lanes of
-// parts.  Brought up while the kernel before it ends.
+// parts.  Brought up while the kernel before it ends, which still writes `part`
+// then: not a read-only pointer, and read through the L2.
 constexpr int kSumRows = 32;
 template <class P>
 __global__ void __launch_bounds__(32 * kSumRows)
-    k_norm_params(const float *__restrict__ part, int parts, int width, P *dweight, P *dbias) {
+    k_norm_params(const float *part, int parts, int width, P *dweight, P *dbias) {
   __shared__ float box[kSumRows][33];
   P *out = blockIdx.y ? dbias : dweight;
   ptx::griddep_wait();
@@ -596,7 +597,7 @@ __global__ void __launch_bounds__(32 * kSumRows)
   float s = 0.f;
   if (c < width)
 #pragma unroll 4
-    for (int i = ty; i < parts; i += kSumRows) s += p[(int64_t)i * 2 * width];
+    for (int i = ty; i < parts; i += kSumRows) s += __ldcg(p + (int64_t)i * 2 * width);
   box[ty][lane] = s;
   __syncthreads();
   if (ty == 0 && c < width) {
