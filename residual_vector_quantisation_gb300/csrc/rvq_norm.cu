@@ -608,13 +608,15 @@ __global__ void __launch_bounds__(32 * kSumRows)
   }
 }
 
-// How a row is laid over threads: `n` elements a unit, at most 32 columns a thread.
+// How the `units` of a row, `n` elements each, are laid over threads: at most 32
+// columns a thread.  Every column that is not in a unit needs a place of its own:
+// the ring kernels have one beside the vectors (their units are the whole
+// vectors), k_norm and k_norm_backward have none (a partial vector is a unit).
 struct NormShape {
   int threads;  // of a row
   int columns;  // of a thread (C)
 };
-inline NormShape norm_shape(int width, int n, int least = 32) {
-  const int units = n == 1 ? width : width / n;  // (vectors: the columns beside them are extra)
+inline NormShape norm_shape(int units, int n, int least = 32) {
   int threads = least;
   while (threads * 32 < units * n) threads *= 2;
   const int c = ((units + threads - 1) / threads * n + 7) / 8 * 8;
@@ -704,7 +706,7 @@ cudaError_t launch_norm_typed(NormArgs &a, NormPath path, bool backward, cudaStr
   if (path == kRing) {
     // narrow rows share a warp: 8 or 16 lanes each.  The elements beside the vectors need 2 N threads.
     const bool whole = rows_aligned16(a.x, a.xs, a.dm.rows, sizeof(T)) && a.dm.width % N == 0;
-    const NormShape s = norm_shape(a.dm.width, N, whole || N == 4 ? 8 : 16);
+    const NormShape s = norm_shape(a.dm.width / N, N, whole || N == 4 ? 8 : 16);
     if (s.threads > 32)  // a thread holds more than 16 columns
       return s.columns <= 24 ? launch_ring_shape<T, P, 24, 0>(a, s.threads, backward, st)
                              : launch_ring_shape<T, P, 32, 0>(a, s.threads, backward, st);
@@ -725,7 +727,7 @@ cudaError_t launch_norm_typed(NormArgs &a, NormPath path, bool backward, cudaStr
       default: return launch_ring_shape<T, P, 32, 8>(a, 8, backward, st);
     }
   }
-  const NormShape s = norm_shape(a.dm.width, path == kElements ? 1 : N);
+  const NormShape s = path == kElements ? norm_shape(a.dm.width, 1) : norm_shape((a.dm.width + N - 1) / N, N);
   if (path == kVectors)  // above kRingWidth
     return s.columns <= 24 ? launch_norm_shape<T, P, N, 24, false>(a, s.threads, backward, st)
                            : launch_norm_shape<T, P, N, 32, false>(a, s.threads, backward, st);

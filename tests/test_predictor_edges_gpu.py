@@ -75,3 +75,53 @@ def test_beam_steps_without_a_pause(vocab):
             assert torch.equal(x, y), q
     p = torch.stack([k[1] for k in want])
     assert bool((p >= 0).all()) and bool((p != p[0]).any())
+
+
+# ---------------------------------------------------------------------------
+# layer norm
+# ---------------------------------------------------------------------------
+
+def rows_in(t, stride, shift):
+    """The same rows, `stride` elements apart, the first `shift` elements into a buffer of NaN."""
+    rows, width = t.shape
+    buffer = torch.full((rows * stride + shift + 16,), math.nan, dtype=t.dtype, device=t.device)
+    view = buffer.as_strided((rows, width), (stride, 1), shift)
+    view.copy_(t)
+    return view
+
+
+def untouched(view):
+    """What lies beside the rows of rows_in is NaN as before."""
+    buffer = torch.empty(0, dtype=view.dtype, device=DEV).set_(view.untyped_storage())
+    held = buffer.clone()
+    held.as_strided(view.shape, view.stride(), view.storage_offset()).fill_(math.nan)
+    return bool(torch.isnan(held).all())
+
+
+def check_norm(x, dy, w, b, places):
+    """places: (stride, shift) of x, dy, y and dx; outputs and workspace hold NaN before."""
+    rows, width = x.shape
+    xv, dyv = rows_in(x, *places[0]), rows_in(dy, *places[1])
+    y, dx = (rows_in(torch.full_like(x, math.nan), *p) for p in places[2:])
+    mean, rstd = (torch.full((rows,), math.nan, device=DEV) for _ in range(2))
+    rq.rvq_layer_norm(xv, w, b, 1e-5, y, mean, rstd)
+    dw, db = torch.full_like(w, math.nan), torch.full_like(b, math.nan)
+    ws = torch.full((rq.rvq_layer_norm_workspace_bytes(rows, width),), 0xFF, dtype=torch.uint8, device=DEV)
+    rq.rvq_layer_norm_backward(dyv, xv, w, mean, rstd, dx, dw, db, ws)
+    val, tol = ref.norm(x, w, b, 1e-5, dy)
+    for k, got in (("y", y), ("dx", dx), ("dweight", dw), ("dbias", db)):
+        ref.check(got, val[k], tol[k], k)
+    assert untouched(y) and untouched(dx)
+
+
+@pytest.mark.parametrize("dtype,pdtype", [(F32, F32), (BF16, BF16), (F16, F32)])
+@pytest.mark.parametrize("width", [8191, 8192, 8193, 8194, 8195, 8199, 8201, 12287, 12289, 12290, 12291, 12295, 12297,
+                                   16381, 16383])
+def test_norm_last_vector_of_wide_rows(width, dtype, pdtype):
+    """Rows on 16-byte boundaries whose width is no multiple of a vector: the last columns count like the others.
+    One row (its stride does not matter) and rows some vectors apart."""
+    g = gen(width)
+    w, b = (1 + 0.2 * randn(g, width)).to(pdtype), (0.3 * randn(g, width)).to(pdtype)
+    for rows, stride in ((1, width), (5, (width + 15) // 8 * 8), (160, (width + 7) // 8 * 8)):
+        x, dy = randn(g, rows, width).to(dtype), randn(g, rows, width).to(dtype)
+        check_norm(x, dy, w, b, [(stride, 0)] * 4)
