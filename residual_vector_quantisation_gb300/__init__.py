@@ -325,31 +325,39 @@ def rvq_stream_plan(dims: rvq_dims, n_q: int, n_frames: int) -> dict:
 # operators of a code predictor (layer norm, distillation loss, beam step)
 # ---------------------------------------------------------------------------
 
-def _at(t: Optional[torch.Tensor], dtype, shape, name: str):
-    """Address of a contiguous CUDA tensor of this dtype and shape (None: null)."""
+def _device(t: torch.Tensor, name: str) -> int:
+    """The GPU that a call's first tensor is on; the others have to be there too."""
+    on = t.get_device()
+    if on < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return on
+
+
+def _at(t: Optional[torch.Tensor], on: int, dtype, shape, name: str):
+    """Address of a contiguous tensor of this dtype and shape on GPU `on` (None: null)."""
     if t is None:
         return None
-    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+    if t.dtype is dtype and t.shape == shape and t.get_device() == on and t.is_contiguous():
         return t.data_ptr()
-    raise ValueError(f"{name} must be a contiguous CUDA tensor of {dtype} and shape {tuple(shape)}")
+    raise ValueError(f"{name} must be a contiguous tensor of {dtype} and shape {tuple(shape)} on cuda:{on}")
 
 
-def _rows_at(t: torch.Tensor, dtype, shape, name: str):
-    """Address and row stride of a 2-d CUDA tensor whose rows are contiguous."""
-    if t.dtype is not dtype or t.shape != shape or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor of {dtype} and shape {tuple(shape)}")
+def _rows_at(t: torch.Tensor, on: int, dtype, shape, name: str):
+    """Address and row stride of a 2-d tensor on GPU `on` whose rows are contiguous."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != on:
+        raise ValueError(f"{name} must be a tensor of {dtype} and shape {tuple(shape)} on cuda:{on}")
     stride, one = t.stride()
     if one != 1 and shape[1] > 1 and shape[0] > 0:
         raise ValueError(f"{name} must have contiguous rows")
     return t.data_ptr(), stride
 
 
-def _workspace(t: Optional[torch.Tensor]):
+def _workspace(t: Optional[torch.Tensor], on: int):
     """Address and bytes of a workspace."""
     if t is None:
         return None, 0
-    if not (t.is_cuda and t.is_contiguous()):
-        raise ValueError("workspace must be a contiguous CUDA tensor")
+    if t.get_device() != on or not t.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{on}")
     return t.data_ptr(), t.nbytes
 
 
@@ -359,11 +367,21 @@ def _shape2(t: torch.Tensor, name: str):
     return t.shape
 
 
-def _raw_stream(t: torch.Tensor, stream) -> int:
-    """The stream given, or the current one of t's device."""
-    if stream is not None:
-        return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(t.device.index)
+def _enqueue(name: str, on: int, stream, *args) -> None:
+    """Calls entry point `name` for tensors on GPU `on`, whichever device is current: with the stream given, which has
+    to be one of that GPU's, or with its current one."""
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(on)
+    elif stream.device.index == on:
+        handle = stream.cuda_stream
+    else:
+        raise ValueError(f"{name}: the stream must be one of cuda:{on}")
+    call = getattr(load_library(), name)
+    if torch._C._cuda_getDevice() == on:
+        _check(name, call(*args, handle))
+    else:
+        with torch.cuda.device(on):
+            _check(name, call(*args, handle))
 
 
 def rvq_layer_norm_workspace_bytes(rows: int, width: int) -> int:
@@ -372,70 +390,68 @@ def rvq_layer_norm_workspace_bytes(rows: int, width: int) -> int:
 
 def rvq_layer_norm(x, weight, bias, eps: float, y, mean=None, rstd=None, stream=None) -> None:
     """Layer norm of the rows of x [rows][width] into y (see rvq.h); mean and rstd [rows] are optional outputs."""
+    on = _device(x, "x")
     shape, dtype = _shape2(x, "x"), x.dtype
     rows, width = shape
     p = weight if weight is not None else bias
     pd = torch.float32 if p is None else p.dtype
-    xp, xs = _rows_at(x, dtype, shape, "x")
-    yp, ys = _rows_at(y, dtype, shape, "y")
-    _check("rvq_layer_norm", load_library().rvq_layer_norm(
-        rvq_norm_dims(rows, width, DTYPES[dtype], DTYPES.get(pd, -1), eps), xp, xs, _at(weight, pd, (width,), "weight"),
-        _at(bias, pd, (width,), "bias"), yp, ys, _at(mean, torch.float32, (rows,), "mean"),
-        _at(rstd, torch.float32, (rows,), "rstd"), _raw_stream(x, stream)))
+    xp, xs = _rows_at(x, on, dtype, shape, "x")
+    yp, ys = _rows_at(y, on, dtype, shape, "y")
+    _enqueue("rvq_layer_norm", on, stream, rvq_norm_dims(rows, width, DTYPES[dtype], DTYPES.get(pd, -1), eps), xp, xs,
+             _at(weight, on, pd, (width,), "weight"), _at(bias, on, pd, (width,), "bias"), yp, ys,
+             _at(mean, on, torch.float32, (rows,), "mean"), _at(rstd, on, torch.float32, (rows,), "rstd"))
 
 
 def rvq_layer_norm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, workspace, stream=None) -> None:
     """Gradients of rvq_layer_norm; dx, dweight and dbias may each be None (not computed)."""
+    on = _device(x, "x")
     shape, dtype = _shape2(x, "x"), x.dtype
     rows, width = shape
     p = weight if weight is not None else dweight if dweight is not None else dbias
     pd = torch.float32 if p is None else p.dtype
-    dyp, dys = _rows_at(dy, dtype, shape, "dy")
-    xp, xs = _rows_at(x, dtype, shape, "x")
-    dxp, dxs = (None, 0) if dx is None else _rows_at(dx, dtype, shape, "dx")
+    dyp, dys = _rows_at(dy, on, dtype, shape, "dy")
+    xp, xs = _rows_at(x, on, dtype, shape, "x")
+    dxp, dxs = (None, 0) if dx is None else _rows_at(dx, on, dtype, shape, "dx")
     if mean is None or rstd is None:
         raise ValueError("rvq_layer_norm_backward needs the forward pass's mean and rstd")
-    _check("rvq_layer_norm_backward", load_library().rvq_layer_norm_backward(
-        rvq_norm_dims(rows, width, DTYPES[dtype], DTYPES.get(pd, -1), 0.0), dyp, dys, xp, xs,
-        _at(weight, pd, (width,), "weight"), _at(mean, torch.float32, (rows,), "mean"),
-        _at(rstd, torch.float32, (rows,), "rstd"), dxp, dxs, _at(dweight, pd, (width,), "dweight"),
-        _at(dbias, pd, (width,), "dbias"), *_workspace(workspace), _raw_stream(x, stream)))
+    _enqueue("rvq_layer_norm_backward", on, stream, rvq_norm_dims(rows, width, DTYPES[dtype], DTYPES.get(pd, -1), 0.0),
+             dyp, dys, xp, xs, _at(weight, on, pd, (width,), "weight"), _at(mean, on, torch.float32, (rows,), "mean"),
+             _at(rstd, on, torch.float32, (rows,), "rstd"), dxp, dxs, _at(dweight, on, pd, (width,), "dweight"),
+             _at(dbias, on, pd, (width,), "dbias"), *_workspace(workspace, on))
 
 
 def _distill_args(logits, top_logits, top_codes, teacher_lse, weights, temperature):
+    on = _device(logits, "logits")
     rows, vocab = shape = _shape2(logits, "logits")
     entries = _shape2(top_logits, "top_logits")
     if entries[0] != rows:
         raise ValueError("top_logits must have the logits' rows")
     dims = rvq_distill_dims(rows, vocab, entries[1], DTYPES[logits.dtype], DTYPES[top_logits.dtype], temperature)
-    zp, zs = _rows_at(logits, logits.dtype, shape, "logits")
-    return dims, (rows,), zp, zs, (_at(top_logits, top_logits.dtype, entries, "top_logits"),
-                                   _at(top_codes, torch.int32, entries, "top_codes"),
-                                   _at(teacher_lse, torch.float32, (rows,), "teacher_lse"),
-                                   _at(weights, torch.float32, (rows,), "weights"))
+    zp, zs = _rows_at(logits, on, logits.dtype, shape, "logits")
+    return dims, on, (rows,), zp, zs, (_at(top_logits, on, top_logits.dtype, entries, "top_logits"),
+                                       _at(top_codes, on, torch.int32, entries, "top_codes"),
+                                       _at(teacher_lse, on, torch.float32, (rows,), "teacher_lse"),
+                                       _at(weights, on, torch.float32, (rows,), "weights"))
 
 
 def rvq_distill(logits, top_logits, top_codes, teacher_lse, weights, temperature: float, loss, lse=None, dlogits=None,
                 bad_codes=None, stream=None) -> None:
     """Distillation loss [rows] of logits [rows][vocab] from the teacher's entries [rows][top] (see rvq.h); with
     dlogits, the gradient in the same pass; with lse [rows][2], what rvq_distill_backward needs."""
-    dims, rows, zp, zs, teacher = _distill_args(logits, top_logits, top_codes, teacher_lse, weights, temperature)
-    dp, ds = (None, 0) if dlogits is None else _rows_at(dlogits, logits.dtype, logits.shape, "dlogits")
-    _check("rvq_distill", load_library().rvq_distill(
-        dims, zp, zs, *teacher, _at(loss, torch.float32, rows, "loss"),
-        None if lse is None else _at(lse, torch.float32, rows + (2,), "lse"), dp, ds,
-        None if bad_codes is None else _at(bad_codes, torch.int64, bad_codes.shape, "bad_codes"),
-        _raw_stream(logits, stream)))
+    dims, on, rows, zp, zs, teacher = _distill_args(logits, top_logits, top_codes, teacher_lse, weights, temperature)
+    dp, ds = (None, 0) if dlogits is None else _rows_at(dlogits, on, logits.dtype, logits.shape, "dlogits")
+    _enqueue("rvq_distill", on, stream, dims, zp, zs, *teacher, _at(loss, on, torch.float32, rows, "loss"),
+             None if lse is None else _at(lse, on, torch.float32, rows + (2,), "lse"), dp, ds,
+             None if bad_codes is None else _at(bad_codes, on, torch.int64, bad_codes.shape, "bad_codes"))
 
 
 def rvq_distill_backward(grad_loss, logits, top_logits, top_codes, teacher_lse, weights, temperature: float, lse,
                          dlogits, stream=None) -> None:
     """dlogits = grad_loss[row] * d loss[row] / d logits, with rvq_distill's lse; grad_loss None: ones."""
-    dims, rows, zp, zs, teacher = _distill_args(logits, top_logits, top_codes, teacher_lse, weights, temperature)
-    dp, ds = _rows_at(dlogits, logits.dtype, logits.shape, "dlogits")
-    _check("rvq_distill_backward", load_library().rvq_distill_backward(
-        dims, _at(grad_loss, torch.float32, rows, "grad_loss"), zp, zs, *teacher,
-        _at(lse, torch.float32, rows + (2,), "lse"), dp, ds, _raw_stream(logits, stream)))
+    dims, on, rows, zp, zs, teacher = _distill_args(logits, top_logits, top_codes, teacher_lse, weights, temperature)
+    dp, ds = _rows_at(dlogits, on, logits.dtype, logits.shape, "dlogits")
+    _enqueue("rvq_distill_backward", on, stream, dims, _at(grad_loss, on, torch.float32, rows, "grad_loss"), zp, zs,
+             *teacher, _at(lse, on, torch.float32, rows + (2,), "lse"), dp, ds)
 
 
 def rvq_beam_workspace_bytes(dims: rvq_beam_dims) -> int:
@@ -447,8 +463,9 @@ def rvq_beam_select(dims: rvq_beam_dims, logits, scores, finished, end_code: int
     """One selection step (see rvq.h): logits [groups][beams][vocab] (or [groups * beams][vocab]), scores and finished
     [groups][beams]; outputs [groups][select].  finished, out_finished: bool or uint8 tensors, or None."""
     groups, beams, vocab = dims.groups, dims.beams, dims.vocab
-    if not logits.is_cuda or DTYPES.get(logits.dtype) != dims.dtype:
-        raise ValueError("logits must be a CUDA tensor of the dtype in dims")
+    on = _device(logits, "logits")
+    if DTYPES.get(logits.dtype) != dims.dtype:
+        raise ValueError("logits must have the dtype in dims")
     if logits.dim() == 3:
         if logits.shape != (groups, beams, vocab) or (groups > 1 and logits.stride(0) != beams * logits.stride(1)):
             raise ValueError(f"logits must be {(groups, beams, vocab)} with evenly spaced rows")
@@ -463,13 +480,13 @@ def rvq_beam_select(dims: rvq_beam_dims, logits, scores, finished, end_code: int
     for t in (finished, out_finished):
         if t is not None and t.dtype is not torch.bool and t.dtype is not torch.uint8:
             raise ValueError("finished and out_finished must be bool or uint8")
-    _check("rvq_beam_select", load_library().rvq_beam_select(
-        dims, logits.data_ptr(), stride, _at(scores, torch.float32, held, "scores"),
-        None if finished is None else _at(finished, finished.dtype, held, "finished"), end_code,
-        _at(out_scores, torch.float32, kept, "out_scores"), _at(parents, torch.int32, kept, "parents"),
-        _at(codes, torch.int32, kept, "codes"),
-        None if out_finished is None else _at(out_finished, out_finished.dtype, kept, "out_finished"),
-        *_workspace(workspace), _raw_stream(logits, stream)))
+    _enqueue("rvq_beam_select", on, stream, dims, logits.data_ptr(), stride,
+             _at(scores, on, torch.float32, held, "scores"),
+             None if finished is None else _at(finished, on, finished.dtype, held, "finished"), end_code,
+             _at(out_scores, on, torch.float32, kept, "out_scores"), _at(parents, on, torch.int32, kept, "parents"),
+             _at(codes, on, torch.int32, kept, "codes"),
+             None if out_finished is None else _at(out_finished, on, out_finished.dtype, kept, "out_finished"),
+             *_workspace(workspace, on))
 
 
 def rvq_beam_states(pairs, layered: bool = False):
@@ -501,6 +518,7 @@ def rvq_beam_states(pairs, layered: bool = False):
         s.dst_group_stride, s.dst_beam_stride = b[-2:]
     out.shapes = [(src.shape[lead - 2:lead], dst.shape[lead - 2:lead]) for src, dst in pairs]
     out.tensors = pairs
+    out.devices = {t.get_device() for pair in pairs for t in pair}
     return out
 
 
@@ -510,8 +528,10 @@ def rvq_beam_reorder(dims: rvq_beam_dims, parents, states, stream=None) -> None:
     for shapes in states.shapes:
         if shapes != want:
             raise ValueError(f"states must have {want[0]} and {want[1]} groups and beams")
-    _check("rvq_beam_reorder", load_library().rvq_beam_reorder(
-        dims, _at(parents, torch.int32, want[1], "parents"), states, len(states), _raw_stream(parents, stream)))
+    on = _device(parents, "parents")
+    if not states.devices <= {on}:
+        raise ValueError(f"states must be on cuda:{on}, with their parents")
+    _enqueue("rvq_beam_reorder", on, stream, dims, _at(parents, on, torch.int32, want[1], "parents"), states, len(states))
 
 
 # ---------------------------------------------------------------------------

@@ -143,8 +143,8 @@ class BeamSearch:
         nbytes = _rq.rvq_beam_workspace_bytes(self.dims)
         if nbytes == 0:
             raise ValueError("unsupported beam search arguments")
-        self.device = torch.device(device)
-        self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+        self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        self.device = self.workspace.device
 
     def first_scores(self) -> torch.Tensor:
         """Scores before the first step: one live beam per group."""

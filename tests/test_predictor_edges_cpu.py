@@ -5,6 +5,9 @@ import os
 import re
 
 import pytest
+import torch
+
+import residual_vector_quantisation_gb300 as rq
 
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "residual_vector_quantisation_gb300",
                     "csrc")
@@ -30,3 +33,120 @@ def test_overlapping_kernels_take_no_read_only_pointers(name):
     for kernel, parameters, body in found:
         if "griddep_wait" in body:
             assert "__restrict__" not in parameters and "__ldg(" not in body, kernel
+
+
+# ---------------------------------------------------------------------------
+# the device of a call
+# ---------------------------------------------------------------------------
+
+class OnGpu:
+    """A tensor that says it is on GPU `index`; its data are never looked at."""
+
+    def __init__(self, index, *shape, dtype=torch.float32):
+        self.t, self.index = torch.zeros(shape, dtype=dtype), index
+
+    is_cuda = True
+    device = property(lambda self: torch.device("cuda", self.index))
+
+    def get_device(self):
+        return self.index
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+
+class Stream:
+    def __init__(self, index, handle):
+        self.device, self.cuda_stream = torch.device("cuda", index), handle
+
+
+@pytest.fixture
+def gpus(monkeypatch):
+    """A library that records (entry point, current device, stream) of each call, and two GPUs that torch makes
+    current; device 0 is."""
+    calls, current = [], [0]
+
+    class Library:
+        def __getattr__(self, name):
+            def call(*args):
+                calls.append((name, current[0], args[-1]))
+                return 0
+            return call
+
+    class Device:
+        def __init__(self, index):
+            self.index = index if isinstance(index, int) else index.index
+
+        def __enter__(self):
+            self.before, current[0] = current[0], self.index
+
+        def __exit__(self, *_):
+            current[0] = self.before
+
+    monkeypatch.setattr(rq, "load_library", lambda: Library())
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: current[0], raising=False)
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 100 + index, raising=False)
+    monkeypatch.setattr(torch.cuda, "current_stream",
+                        lambda d=None: Stream(current[0] if d is None else torch.device(d).index,
+                                              100 + (current[0] if d is None else torch.device(d).index)))
+    return calls
+
+
+F32, I32, U8 = torch.float32, torch.int32, torch.uint8
+BEAM = rq.rvq_beam_dims(2, 3, 10, 3, 0, 0)
+
+
+def operators(t):
+    """Each entry point with tensors from t(*shape, dtype): {name: (call, the tensors it takes)}."""
+    def with_tensors(call, *tensors):
+        return call, list(tensors)
+
+    rows, stats, w, ws = (lambda: t(4, 8)), (lambda: t(4)), (lambda: t(8)), (lambda: t(64, dtype=U8))
+    top, codes = (lambda: t(4, 2)), (lambda: t(4, 2, dtype=I32))
+    kept = lambda: t(2, 3, dtype=I32)  # noqa: E731
+    return {
+        "rvq_layer_norm": with_tensors(lambda x, w, b, y, m, r, **kw: rq.rvq_layer_norm(x, w, b, 1e-5, y, m, r, **kw),
+                                       rows(), w(), w(), rows(), stats(), stats()),
+        "rvq_layer_norm_backward": with_tensors(rq.rvq_layer_norm_backward, rows(), rows(), w(), stats(), stats(), rows(),
+                                                w(), w(), ws()),
+        "rvq_distill": with_tensors(lambda z, t, c, e, w, o, s, d, b, **kw: rq.rvq_distill(z, t, c, e, w, 1.0, o, s, d, b,
+                                                                                          **kw),
+                                    rows(), top(), codes(), stats(), stats(), stats(), t(4, 2), rows(),
+                                    t(1, dtype=torch.int64)),
+        "rvq_distill_backward": with_tensors(
+            lambda g, z, t, c, e, w, s, d, **kw: rq.rvq_distill_backward(g, z, t, c, e, w, 1.0, s, d, **kw),
+            stats(), rows(), top(), codes(), stats(), stats(), t(4, 2), rows()),
+        "rvq_beam_select": with_tensors(
+            lambda z, s, f, o, p, c, of, ws, **kw: rq.rvq_beam_select(BEAM, z, s, f, 1, o, p, c, of, ws, **kw),
+            t(2, 3, 10), t(2, 3), t(2, 3, dtype=U8), t(2, 3), kept(), kept(), t(2, 3, dtype=U8), ws()),
+        "rvq_beam_reorder": with_tensors(
+            lambda p, a, b, **kw: rq.rvq_beam_reorder(BEAM, p, rq.rvq_beam_states([(a, b)]), **kw),
+            kept(), t(2, 3, 4), t(2, 3, 4)),
+    }
+
+
+NAMES = sorted(operators(lambda *shape, dtype=F32: None))
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_operators_run_on_their_tensors_device(name, gpus):
+    for index in (0, 1):
+        call, tensors = operators(lambda *shape, dtype=F32: OnGpu(index, *shape, dtype=dtype))[name]
+        call(*tensors)
+        assert gpus.pop() == (name, index, 100 + index)
+        call(*tensors, stream=Stream(index, 7))
+        assert gpus.pop() == (name, index, 7)
+        with pytest.raises(ValueError):
+            call(*tensors, stream=Stream(1 - index, 7))
+    assert not gpus and torch._C._cuda_getDevice() == 0
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_operators_refuse_tensors_of_two_devices(name, gpus):
+    call, tensors = operators(lambda *shape, dtype=F32: OnGpu(0, *shape, dtype=dtype))[name]
+    for i, t in enumerate(tensors):
+        for other in (OnGpu(1, *t.shape, dtype=t.dtype), t.t):
+            with pytest.raises(ValueError):
+                call(*tensors[:i], other, *tensors[i + 1:])
+    assert not gpus
