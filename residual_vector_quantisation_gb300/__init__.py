@@ -173,20 +173,45 @@ def load_library(path: Optional[str] = None):
 # argument marshalling
 # ---------------------------------------------------------------------------
 
-def _ptr(t: Optional[torch.Tensor]):
+def _ptr(t: Optional[torch.Tensor], on: Optional[int] = None):
+    """Address of a contiguous CUDA tensor (on GPU `on`, where that is given)."""
     if t is None:
         return None
     if not t.is_cuda:
         raise ValueError("RVQ buffers must be CUDA tensors")
     if not t.is_contiguous():
         raise ValueError("RVQ buffers must be contiguous")
+    if on is not None and t.get_device() != on:
+        raise ValueError(f"RVQ buffers of one call must all be on cuda:{on}")
     return ctypes.c_void_p(t.data_ptr())
 
 
-def _stream(stream) -> ctypes.c_void_p:
+def _device(t: torch.Tensor, name: str) -> int:
+    """The GPU that a call's first tensor is on; the others have to be there too."""
+    on = t.get_device()
+    if on < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return on
+
+
+def _status(name: str, on: int, stream, *args) -> int:
+    """What entry point `name` returns for tensors on GPU `on`, whichever device is current: called with the stream
+    given, which has to be one of that GPU's, or with its current one."""
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+        handle = torch._C._cuda_getCurrentRawStream(on)
+    elif stream.device.index == on:
+        handle = stream.cuda_stream
+    else:
+        raise ValueError(f"{name}: the stream must be one of cuda:{on}")
+    call = getattr(load_library(), name)
+    if torch._C._cuda_getDevice() == on:
+        return call(*args, handle)
+    with torch.cuda.device(on):
+        return call(*args, handle)
+
+
+def _enqueue(name: str, on: int, stream, *args) -> None:
+    _check(name, _status(name, on, stream, *args))
 
 
 def _check(name: str, status: int):
@@ -216,38 +241,37 @@ def rvq_encode_min_scratch_bytes(dims: rvq_dims, n_q: int) -> int:
 
 def rvq_prepare(dims: rvq_dims, w_in, codebook, w_out, b_in, b_out, tables: torch.Tensor, stream=None,
                 fc_w=None, fc_b=None, fc2_w=None, fc2_b=None) -> None:
-    w = rvq_weights(_ptr(w_in), _ptr(b_in), _ptr(codebook), _ptr(w_out), _ptr(b_out), _ptr(fc_w), _ptr(fc_b),
-                    _ptr(fc2_w), _ptr(fc2_b))
-    _check("rvq_prepare", load_library().rvq_prepare(dims, ctypes.byref(w), _ptr(tables),
-                                                     tables.numel() * tables.element_size(), _stream(stream)))
+    on = _device(tables, "tables")
+    w = rvq_weights(*(_ptr(t, on) for t in (w_in, b_in, codebook, w_out, b_out, fc_w, fc_b, fc2_w, fc2_b)))
+    _enqueue("rvq_prepare", on, stream, dims, ctypes.byref(w), _ptr(tables, on), tables.numel() * tables.element_size())
 
 
 def rvq_encode(dims: rvq_dims, tables, x, n_q: int, codes, scratch, stream=None) -> None:
+    on = _device(tables, "tables")
     n = x.shape[0]
-    _check("rvq_encode", load_library().rvq_encode(dims, _ptr(tables), _ptr(x), n, int(n_q), _ptr(codes),
-                                                   _ptr(scratch), scratch.numel() * scratch.element_size(),
-                                                   _stream(stream)))
+    _enqueue("rvq_encode", on, stream, dims, _ptr(tables, on), _ptr(x, on), n, int(n_q), _ptr(codes, on),
+             _ptr(scratch, on), scratch.numel() * scratch.element_size())
 
 
 def rvq_decode(dims: rvq_dims, tables, codes, n_q: int, y, bad_codes=None, stream=None) -> None:
+    on = _device(tables, "tables")
     n = codes.shape[0]
-    _check("rvq_decode", load_library().rvq_decode(dims, _ptr(tables), _ptr(codes), n, int(n_q), _ptr(y),
-                                                   _ptr(bad_codes), _stream(stream)))
+    _enqueue("rvq_decode", on, stream, dims, _ptr(tables, on), _ptr(codes, on), n, int(n_q), _ptr(y, on),
+             _ptr(bad_codes, on))
 
 
 def rvq_reconstruct(dims: rvq_dims, tables, x, n_q: int, codes, x_hat, scratch, stream=None) -> None:
+    on = _device(tables, "tables")
     n = x.shape[0]
-    _check("rvq_reconstruct", load_library().rvq_reconstruct(dims, _ptr(tables), _ptr(x), n, int(n_q), _ptr(codes),
-                                                             _ptr(x_hat), _ptr(scratch),
-                                                             scratch.numel() * scratch.element_size(),
-                                                             _stream(stream)))
+    _enqueue("rvq_reconstruct", on, stream, dims, _ptr(tables, on), _ptr(x, on), n, int(n_q), _ptr(codes, on),
+             _ptr(x_hat, on), _ptr(scratch, on), scratch.numel() * scratch.element_size())
 
 
 def rvq_encode_static(dims: rvq_dims, tables, x, n_q: int, codes, stream=None) -> None:
     """Encode with the library's own fixed scratch (no scratch argument; see rvq.h)."""
+    on = _device(tables, "tables")
     n = x.shape[0]
-    _check("rvq_encode_static", load_library().rvq_encode_static(dims, _ptr(tables), _ptr(x), n, int(n_q),
-                                                                 _ptr(codes), _stream(stream)))
+    _enqueue("rvq_encode_static", on, stream, dims, _ptr(tables, on), _ptr(x, on), n, int(n_q), _ptr(codes, on))
 
 
 def rvq_pipeline_workspace_bytes(dims: rvq_dims, n_q: int, chunk_frames: int) -> int:
@@ -283,14 +307,15 @@ def rvq_read_status(scratch: Optional[torch.Tensor] = None, stream=None) -> int:
     """Synchronise `stream` and return the status (an rvq_status value, not
     raised) that the encode last enqueued with `scratch` left in its status
     word; scratch=None reads the library's own scratch (rvq_encode_static)."""
-    return int(load_library().rvq_read_status(_ptr(scratch), _stream(stream)))
+    on = torch.cuda.current_device() if scratch is None else _device(scratch, "scratch")
+    return int(_status("rvq_read_status", on, stream, _ptr(scratch, on)))
 
 
 def rvq_read_error_count(bad_codes: torch.Tensor, stream=None) -> int:
     """Synchronise `stream` and return rvq_decode's bad-code counter."""
     out = ctypes.c_int64(0)
-    _check("rvq_read_error_count", load_library().rvq_read_error_count(_ptr(bad_codes), ctypes.byref(out),
-                                                                       _stream(stream)))
+    on = _device(bad_codes, "bad_codes")
+    _enqueue("rvq_read_error_count", on, stream, _ptr(bad_codes, on), ctypes.byref(out))
     return int(out.value)
 
 
@@ -325,14 +350,6 @@ def rvq_stream_plan(dims: rvq_dims, n_q: int, n_frames: int) -> dict:
 # operators of a code predictor (layer norm, distillation loss, beam step)
 # ---------------------------------------------------------------------------
 
-def _device(t: torch.Tensor, name: str) -> int:
-    """The GPU that a call's first tensor is on; the others have to be there too."""
-    on = t.get_device()
-    if on < 0:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    return on
-
-
 def _at(t: Optional[torch.Tensor], on: int, dtype, shape, name: str):
     """Address of a contiguous tensor of this dtype and shape on GPU `on` (None: null)."""
     if t is None:
@@ -365,23 +382,6 @@ def _shape2(t: torch.Tensor, name: str):
     if t.dim() != 2 or t.dtype not in DTYPES:
         raise ValueError(f"{name} must be a 2-d tensor of float32, bfloat16 or float16")
     return t.shape
-
-
-def _enqueue(name: str, on: int, stream, *args) -> None:
-    """Calls entry point `name` for tensors on GPU `on`, whichever device is current: with the stream given, which has
-    to be one of that GPU's, or with its current one."""
-    if stream is None:
-        handle = torch._C._cuda_getCurrentRawStream(on)
-    elif stream.device.index == on:
-        handle = stream.cuda_stream
-    else:
-        raise ValueError(f"{name}: the stream must be one of cuda:{on}")
-    call = getattr(load_library(), name)
-    if torch._C._cuda_getDevice() == on:
-        _check(name, call(*args, handle))
-    else:
-        with torch.cuda.device(on):
-            _check(name, call(*args, handle))
 
 
 def rvq_layer_norm_workspace_bytes(rows: int, width: int) -> int:
@@ -568,6 +568,7 @@ class RVQ:
         _check("rvq_dims_supported", status)
         nbytes = rvq_tables_bytes(self.dims)
         self.tables = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        self.device = self.tables.device  # with its index: a "cuda" of later calls may be another one
         with torch.cuda.device(device):
             rvq_prepare(self.dims, w_in, codebook, w_out, b_in, b_out, self.tables, stream, fc_w, fc_b, fc2_w, fc2_b)
         self._scratch = None

@@ -126,13 +126,40 @@ def operators(t):
     }
 
 
-NAMES = sorted(operators(lambda *shape, dtype=F32: None))
+QUANTISER = rq.rvq_dims(8, 4, 16, 2, 0, 0, 0)
+
+
+def quantiser(t):
+    """The quantiser's own entry points, stated in the same way."""
+    tables, scratch = (lambda: t(64, dtype=U8)), (lambda: t(64, dtype=U8))
+    x, codes = (lambda: t(5, 8)), (lambda: t(5, 2, dtype=I32))
+    return {
+        "rvq_prepare": (lambda tab, a, b, c, d, e, **kw: rq.rvq_prepare(QUANTISER, a, b, c, d, e, tab, **kw),
+                        [tables(), t(2, 4, 8), t(2, 16, 4), t(2, 8, 4), t(2, 4), t(2, 8)]),
+        "rvq_encode": (lambda tab, a, c, s, **kw: rq.rvq_encode(QUANTISER, tab, a, 2, c, s, **kw),
+                       [tables(), x(), codes(), scratch()]),
+        "rvq_decode": (lambda tab, c, y, b, **kw: rq.rvq_decode(QUANTISER, tab, c, 2, y, b, **kw),
+                       [tables(), codes(), x(), t(1, dtype=torch.int64)]),
+        "rvq_reconstruct": (lambda tab, a, c, y, s, **kw: rq.rvq_reconstruct(QUANTISER, tab, a, 2, c, y, s, **kw),
+                            [tables(), x(), codes(), x(), scratch()]),
+        "rvq_encode_static": (lambda tab, a, c, **kw: rq.rvq_encode_static(QUANTISER, tab, a, 2, c, **kw),
+                              [tables(), x(), codes()]),
+        "rvq_read_status": (rq.rvq_read_status, [scratch()]),
+        "rvq_read_error_count": (rq.rvq_read_error_count, [t(1, dtype=torch.int64)]),
+    }
+
+
+def every_call(t):
+    return {**operators(t), **quantiser(t)}
+
+
+NAMES = sorted(every_call(lambda *shape, dtype=F32: None))
 
 
 @pytest.mark.parametrize("name", NAMES)
-def test_operators_run_on_their_tensors_device(name, gpus):
+def test_calls_run_on_their_tensors_device(name, gpus):
     for index in (0, 1):
-        call, tensors = operators(lambda *shape, dtype=F32: OnGpu(index, *shape, dtype=dtype))[name]
+        call, tensors = every_call(lambda *shape, dtype=F32: OnGpu(index, *shape, dtype=dtype))[name]
         call(*tensors)
         assert gpus.pop() == (name, index, 100 + index)
         call(*tensors, stream=Stream(index, 7))
@@ -143,9 +170,9 @@ def test_operators_run_on_their_tensors_device(name, gpus):
 
 
 @pytest.mark.parametrize("name", NAMES)
-def test_operators_refuse_tensors_of_two_devices(name, gpus):
-    call, tensors = operators(lambda *shape, dtype=F32: OnGpu(0, *shape, dtype=dtype))[name]
-    for i, t in enumerate(tensors):
+def test_calls_refuse_tensors_of_two_devices(name, gpus):
+    call, tensors = every_call(lambda *shape, dtype=F32: OnGpu(0, *shape, dtype=dtype))[name]
+    for i, t in enumerate(tensors if len(tensors) > 1 else []):
         for other in (OnGpu(1, *t.shape, dtype=t.dtype), t.t):
             with pytest.raises(ValueError):
                 call(*tensors[:i], other, *tensors[i + 1:])
