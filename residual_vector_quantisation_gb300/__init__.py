@@ -214,6 +214,14 @@ def _enqueue(name: str, on: int, stream, *args) -> None:
     _check(name, _status(name, on, stream, *args))
 
 
+def _used_on(stream, *tensors) -> None:
+    """Tells torch's allocator that work on `stream` uses these tensors: their memory is given to nobody else before
+    that work has ended, whenever they are dropped."""
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+
+
 def _check(name: str, status: int):
     if status != RVQ_OK:
         raise RVQError(name, status)

@@ -154,28 +154,44 @@ class BeamSearch:
 
     def select(self, logits, scores, finished=None, stream=None):
         """(scores, parents, codes, finished), each [groups][select], best first; finished is None where no code
-        ends a beam."""
+        ends a beam.  stream: where the step runs (None: the current stream); the inputs have to be ready there, and
+        the results are."""
+        if stream is None:
+            return self._select(logits, scores, finished, None)
+        # allocated on the stream that writes them: a block that the current stream freed may still be in use there
+        with torch.cuda.stream(stream):
+            out = self._select(logits, scores, finished, stream)
+        _rq._used_on(stream, logits, scores, finished, self.workspace)
+        _rq._used_on(torch.cuda.current_stream(self.device), *out)
+        return out
+
+    def _select(self, logits, scores, finished, stream):
         kept = (self.dims.groups, self.dims.select)
         out = torch.empty(kept, dtype=torch.float32, device=self.device)
         parents, codes = torch.empty((2,) + kept, dtype=torch.int32, device=self.device).unbind(0)
         done = torch.empty(kept, dtype=torch.bool, device=self.device) if self.end_code >= 0 else None
         _rq.rvq_beam_select(self.dims, logits, scores, finished, self.end_code, out, parents, codes, done,
                             self.workspace, stream)
-        if stream is not None:
-            for t in (out, parents, codes, done):
-                if t is not None:
-                    t.record_stream(stream)
         return out, parents, codes, done
 
     def reorder(self, parents, state, out=None, layered: bool = False, stream=None):
         """state [groups][beams][...] (or [layers][groups][beams][...]) by the beams' parents: a new tensor, `out`,
-        or in place where out is state."""
+        or in place where out is state.  stream: as in select."""
+        if stream is None:
+            return self._reorder(parents, state, out, layered, None)
+        given = out
+        with torch.cuda.stream(stream):
+            out = self._reorder(parents, state, out, layered, stream)
+        _rq._used_on(stream, parents, state, given)
+        if given is None:
+            _rq._used_on(torch.cuda.current_stream(self.device), out)
+        return out
+
+    def _reorder(self, parents, state, out, layered, stream):
         if out is None:
             lead = 1 if layered else 0
             shape = list(state.shape)
             shape[lead + 1] = self.dims.select
             out = torch.empty(shape, dtype=state.dtype, device=state.device)
         _rq.rvq_beam_reorder(self.dims, parents, _rq.rvq_beam_states([(state, out)], layered), stream)
-        if stream is not None:
-            out.record_stream(stream)
         return out

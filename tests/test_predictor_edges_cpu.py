@@ -177,3 +177,80 @@ def test_calls_refuse_tensors_of_two_devices(name, gpus):
             with pytest.raises(ValueError):
                 call(*tensors[:i], other, *tensors[i + 1:])
     assert not gpus
+
+
+# ---------------------------------------------------------------------------
+# a stream of the caller's
+# ---------------------------------------------------------------------------
+
+@pytest.fixture
+def streams(monkeypatch):
+    """The stream that torch would allocate on, and who told the allocator of which stream."""
+    class Log:
+        now, used, allocated = "current", [], {}
+
+        def of(self, stream):
+            return {p for p, s in self.used if s == stream}
+
+    log = Log()
+    log.used, log.allocated = [], {}
+
+    class Scope:
+        def __init__(self, stream):
+            self.stream = stream
+
+        def __enter__(self):
+            self.before, log.now = log.now, self.stream
+
+        def __exit__(self, *_):
+            log.now = self.before
+
+    empty = torch.empty
+
+    def allocate(*args, **kw):
+        t = empty(*args, **kw)
+        log.allocated[t.untyped_storage().data_ptr()] = log.now
+        return t
+
+    monkeypatch.setattr(torch, "empty", allocate)
+    monkeypatch.setattr(torch.cuda, "stream", Scope)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: log.now)
+    monkeypatch.setattr(torch.Tensor, "record_stream",
+                        lambda t, s: log.used.append((t.untyped_storage().data_ptr(), s)))
+    return log
+
+
+def storage(t):
+    return t.untyped_storage().data_ptr()
+
+
+def test_beam_search_on_a_stream(monkeypatch, streams):
+    """What a step on a stream of the caller's writes is allocated there (a block freed by the current stream may still
+    be in use by it), and nothing that it touches is given away before it has run."""
+    ran = []
+    monkeypatch.setattr(rq, "rvq_beam_select", lambda *a: ran.append((a[-1], streams.now)))
+    monkeypatch.setattr(rq, "rvq_beam_reorder", lambda *a: ran.append((a[-1], streams.now)))
+    monkeypatch.setattr(rq, "rvq_beam_states", lambda pairs, layered: pairs)
+    search = rq.BeamSearch(2, 3, 10, end_code=1, device="cpu")
+    logits, scores, finished = torch.zeros(2, 3, 10), torch.zeros(2, 3), torch.zeros((2, 3), dtype=torch.bool)
+    out = search.select(logits, scores, finished, stream="side")
+    assert ran.pop() == ("side", "side")
+    assert {streams.allocated[storage(t)] for t in out} == {"side"}
+    assert streams.of("side") == {storage(t) for t in (logits, scores, finished, search.workspace)}
+    assert streams.of("current") == {storage(t) for t in out}
+
+    streams.used.clear()
+    state = torch.zeros(2, 3, 4)
+    moved = search.reorder(out[1], state, stream="side")
+    assert ran.pop() == ("side", "side") and streams.allocated[storage(moved)] == "side"
+    assert streams.of("side") == {storage(out[1]), storage(state)} and streams.of("current") == {storage(moved)}
+
+    streams.used.clear()
+    place = torch.zeros(2, 3, 4)
+    assert search.reorder(out[1], state, place, stream="side") is place
+    assert streams.of("side") == {storage(out[1]), storage(state), storage(place)} and not streams.of("current")
+
+    assert ran.pop() == ("side", "side") and not ran
+    streams.used.clear()
+    search.reorder(search.select(logits, scores)[1], state)
+    assert not streams.used and {s for s, _ in ran} == {None}

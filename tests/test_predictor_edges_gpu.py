@@ -125,3 +125,48 @@ def test_norm_last_vector_of_wide_rows(width, dtype, pdtype):
     for rows, stride in ((1, width), (5, (width + 15) // 8 * 8), (160, (width + 7) // 8 * 8)):
         x, dy = randn(g, rows, width).to(dtype), randn(g, rows, width).to(dtype)
         check_norm(x, dy, w, b, [(stride, 0)] * 4)
+
+
+# ---------------------------------------------------------------------------
+# streams
+# ---------------------------------------------------------------------------
+
+def busy(n=30):
+    big = torch.ones((4096, 4096), device=DEV)
+    for _ in range(n):
+        big = big @ big * 1e-4
+    return big
+
+
+def test_beam_search_on_a_stream_of_its_own():
+    """The caller's stream runs beside a current stream that has freed memory which it still writes, and takes what is
+    freed as soon as the calls return."""
+    g = gen(3)
+    logits, scores = (randn(g, 5, 4, 300) * 48).round() / 16, -(randn(g, 5, 4) * 24).round().abs() / 8
+    state = randn(g, 5, 4, 1000)
+    finished = torch.zeros((5, 4), dtype=torch.bool, device=DEV)
+    search = rq.BeamSearch(5, 4, 300, end_code=7)
+    want = search.select(logits, scores, finished)
+    moved = search.reorder(want[1], state)
+    want, moved = [t.clone() for t in want], moved.clone()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        other = rq.BeamSearch(5, 4, 300, end_code=7)
+        held = [t.clone() for t in (logits, scores, finished, state)]
+        torch.cuda.synchronize()
+        busy()
+        for t in [torch.empty_like(t) for t in (*want, moved) for _ in range(4)]:
+            t.fill_(1)                           # still to come when the memory is free again
+        del t
+        with torch.cuda.stream(side):
+            busy(10)                             # the step waits while the current stream goes on
+        got = other.select(*held[:3], stream=side)
+        after = other.reorder(got[1], held[3], stream=side)
+        del other, held
+        junk = [torch.full((4096,), 3, dtype=torch.uint8, device=DEV) for _ in range(64)]
+        torch.cuda.current_stream().wait_stream(side)
+        for a, b in zip((*want, moved), (*got, after)):
+            assert torch.equal(a, b)
+        del junk
+    torch.cuda.synchronize()
