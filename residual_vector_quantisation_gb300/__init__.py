@@ -218,8 +218,20 @@ def _used_on(stream, *tensors) -> None:
     """Tells torch's allocator that work on `stream` uses these tensors: their memory is given to nobody else before
     that work has ended, whenever they are dropped."""
     for t in tensors:
-        if t is not None:
+        if t is not None and t.is_cuda:
             t.record_stream(stream)
+
+
+def _run_on(stream, device, call, touched):
+    """call() with `stream` current (None: as it is), so that what it allocates is that stream's: a block that another
+    stream freed may still be in use there.  touched(): the other tensors that its work uses."""
+    if stream is None:
+        return call()
+    with torch.cuda.stream(stream):
+        out = call()
+    _used_on(stream, *touched())
+    _used_on(torch.cuda.current_stream(device), *(out if isinstance(out, tuple) else (out,)))
+    return out
 
 
 def _check(name: str, status: int):
@@ -556,6 +568,10 @@ class RVQ:
     fc_w [D][D_in], fc_b [D] (optional): a Linear layer applied to each frame
     before the quantizer; fc2_w [D_out][D], fc2_b [D_out] (optional): one
     applied to the decoded sum.  Both are folded into the tables.
+
+    The calls run on the current stream, or on `stream`, where their inputs
+    have to be ready.  The object owns a scratch buffer; one object serves one
+    stream at a time.
     """
 
     def __init__(self, w_in, codebook, w_out, b_in=None, b_out=None, device=None, stream=None,
@@ -593,31 +609,40 @@ class RVQ:
         return x.to(device=self.device, dtype=torch.float32).contiguous()
 
     def encode(self, x, n_q: Optional[int] = None, codes=None, stream=None):
-        n_q = self.Q if n_q is None else int(n_q)
-        x = self._frames(x)
-        if codes is None:
-            codes = torch.empty((x.shape[0], n_q), dtype=torch.int32, device=self.device)
-        rvq_encode(self.dims, self.tables, x, n_q, codes, self.scratch_for(x.shape[0], n_q), stream)
-        return codes
+        def call():
+            depth, frames = self.Q if n_q is None else int(n_q), self._frames(x)
+            out = codes
+            if out is None:
+                out = torch.empty((frames.shape[0], depth), dtype=torch.int32, device=self.device)
+            rvq_encode(self.dims, self.tables, frames, depth, out, self.scratch_for(frames.shape[0], depth), stream)
+            return out
+
+        return _run_on(stream, self.device, call, lambda: (x, codes, self.tables, self._scratch))
 
     def decode(self, codes, n_q: Optional[int] = None, y=None, bad_codes=None, stream=None):
-        codes = codes.to(device=self.device, dtype=torch.int32).contiguous()
-        n_q = codes.shape[1] if n_q is None else int(n_q)
-        if y is None:
-            y = torch.empty((codes.shape[0], self.D_out), dtype=torch.float32, device=self.device)
-        rvq_decode(self.dims, self.tables, codes, n_q, y, bad_codes, stream)
-        return y
+        def call():
+            c = codes.to(device=self.device, dtype=torch.int32).contiguous()
+            out = y
+            if out is None:
+                out = torch.empty((c.shape[0], self.D_out), dtype=torch.float32, device=self.device)
+            rvq_decode(self.dims, self.tables, c, c.shape[1] if n_q is None else int(n_q), out, bad_codes, stream)
+            return out
+
+        return _run_on(stream, self.device, call, lambda: (codes, y, bad_codes, self.tables))
 
     def reconstruct(self, x, n_q: Optional[int] = None, codes=None, x_hat=None, stream=None):
-        n_q = self.Q if n_q is None else int(n_q)
-        x = self._frames(x)
-        n = x.shape[0]
-        if codes is None:
-            codes = torch.empty((n, n_q), dtype=torch.int32, device=self.device)
-        if x_hat is None:
-            x_hat = torch.empty((n, self.D_out), dtype=torch.float32, device=self.device)
-        rvq_reconstruct(self.dims, self.tables, x, n_q, codes, x_hat, self.scratch_for(n, n_q), stream)
-        return codes, x_hat
+        def call():
+            depth, frames = self.Q if n_q is None else int(n_q), self._frames(x)
+            n = frames.shape[0]
+            c, y = codes, x_hat
+            if c is None:
+                c = torch.empty((n, depth), dtype=torch.int32, device=self.device)
+            if y is None:
+                y = torch.empty((n, self.D_out), dtype=torch.float32, device=self.device)
+            rvq_reconstruct(self.dims, self.tables, frames, depth, c, y, self.scratch_for(n, depth), stream)
+            return c, y
+
+        return _run_on(stream, self.device, call, lambda: (x, codes, x_hat, self.tables, self._scratch))
 
 
 class RVQPipeline:

@@ -156,14 +156,8 @@ class BeamSearch:
         """(scores, parents, codes, finished), each [groups][select], best first; finished is None where no code
         ends a beam.  stream: where the step runs (None: the current stream); the inputs have to be ready there, and
         the results are."""
-        if stream is None:
-            return self._select(logits, scores, finished, None)
-        # allocated on the stream that writes them: a block that the current stream freed may still be in use there
-        with torch.cuda.stream(stream):
-            out = self._select(logits, scores, finished, stream)
-        _rq._used_on(stream, logits, scores, finished, self.workspace)
-        _rq._used_on(torch.cuda.current_stream(self.device), *out)
-        return out
+        return _rq._run_on(stream, self.device, lambda: self._select(logits, scores, finished, stream),
+                           lambda: (logits, scores, finished, self.workspace))
 
     def _select(self, logits, scores, finished, stream):
         kept = (self.dims.groups, self.dims.select)
@@ -177,15 +171,8 @@ class BeamSearch:
     def reorder(self, parents, state, out=None, layered: bool = False, stream=None):
         """state [groups][beams][...] (or [layers][groups][beams][...]) by the beams' parents: a new tensor, `out`,
         or in place where out is state.  stream: as in select."""
-        if stream is None:
-            return self._reorder(parents, state, out, layered, None)
-        given = out
-        with torch.cuda.stream(stream):
-            out = self._reorder(parents, state, out, layered, stream)
-        _rq._used_on(stream, parents, state, given)
-        if given is None:
-            _rq._used_on(torch.cuda.current_stream(self.device), out)
-        return out
+        return _rq._run_on(stream, self.device, lambda: self._reorder(parents, state, out, layered, stream),
+                           lambda: (parents, state, out))
 
     def _reorder(self, parents, state, out, layered, stream):
         if out is None:

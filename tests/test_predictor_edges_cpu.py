@@ -1,6 +1,7 @@
 """The code predictor's operators where calls can go wrong, as far as that shows
 without a GPU."""
 
+import contextlib
 import os
 import re
 
@@ -215,6 +216,7 @@ def streams(monkeypatch):
     monkeypatch.setattr(torch, "empty", allocate)
     monkeypatch.setattr(torch.cuda, "stream", Scope)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: log.now)
+    monkeypatch.setattr(torch.Tensor, "is_cuda", True, raising=False)
     monkeypatch.setattr(torch.Tensor, "record_stream",
                         lambda t, s: log.used.append((t.untyped_storage().data_ptr(), s)))
     return log
@@ -248,9 +250,37 @@ def test_beam_search_on_a_stream(monkeypatch, streams):
     streams.used.clear()
     place = torch.zeros(2, 3, 4)
     assert search.reorder(out[1], state, place, stream="side") is place
-    assert streams.of("side") == {storage(out[1]), storage(state), storage(place)} and not streams.of("current")
+    assert streams.of("side") == {storage(out[1]), storage(state), storage(place)}
 
     assert ran.pop() == ("side", "side") and not ran
     streams.used.clear()
     search.reorder(search.select(logits, scores)[1], state)
     assert not streams.used and {s for s, _ in ran} == {None}
+
+
+def test_quantiser_on_a_stream(monkeypatch, streams):
+    """The quantiser's own calls in the same way, conversions of what they are given among them."""
+    ran = []
+    for name, value in (("rvq_dims_supported", 0), ("rvq_tables_bytes", 64), ("rvq_encode_scratch_bytes", 64)):
+        monkeypatch.setattr(rq, name, lambda *a, value=value: value)
+    monkeypatch.setattr(rq, "rvq_prepare", lambda *a: None)
+    monkeypatch.setattr(torch.cuda, "device", lambda d: contextlib.nullcontext())
+    for name in ("rvq_encode", "rvq_decode", "rvq_reconstruct"):
+        monkeypatch.setattr(rq, name, lambda *a: ran.append((a[-1], streams.now)))
+    rvq = rq.RVQ(torch.zeros(2, 4, 8), torch.zeros(2, 16, 4), torch.zeros(2, 8, 4), device="cpu")
+    converted = []
+    frames = rvq._frames
+    monkeypatch.setattr(rvq, "_frames", lambda x: (converted.append(streams.now), frames(x))[1])
+    x, codes = torch.zeros(5, 8, dtype=torch.float64), torch.zeros(5, 2, dtype=torch.int64)
+    for call, given in ((rvq.encode, x), (rvq.decode, codes), (rvq.reconstruct, x)):
+        streams.used.clear()
+        out = call(given, stream="side")
+        out = out if isinstance(out, tuple) else (out,)
+        assert ran.pop() == ("side", "side") and set(converted) == {"side"}
+        assert {streams.allocated[storage(t)] for t in out} == {"side"}
+        kept = {storage(given), storage(rvq.tables)} | ({storage(rvq._scratch)} if given is x else set())
+        assert kept <= streams.of("side") and {storage(t) for t in out} <= streams.of("current")
+        streams.used.clear()
+        call(given)
+        assert ran.pop() == (None, "current") and not streams.used
+        converted[:] = ["side"]
