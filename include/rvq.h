@@ -481,8 +481,13 @@ RVQ_API rvq_status rvq_beam_select(rvq_beam_dims dims, const void *logits, int64
 /* One state tensor that follows the beams: `layers` x groups x beams rows of
  * row_bytes contiguous bytes (layers 1 where the tensor has no such axis);
  * strides in bytes.  dst holds `select` rows per group.  dst == src (and equal
- * strides) reorders in place and needs select == beams; other overlaps are
- * not allowed. */
+ * strides) reorders in place and needs select == beams.  Other overlaps are
+ * refused (RVQ_ERR_INVALID_ARG): rows of a dst that overlap one another (a
+ * stride of 0), another dst of the call, a src or the parents; only the src of
+ * a state that is moved may be a state that the same call reorders in place,
+ * and is read before that.  Rows that lie between one another are told apart;
+ * strides that interleave so that this takes too long are refused with
+ * RVQ_ERR_UNSUPPORTED. */
 typedef struct rvq_beam_state {
   const void *src;
   void *dst;

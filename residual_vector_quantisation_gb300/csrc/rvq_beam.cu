@@ -10,6 +10,7 @@
 // (k_beam_group); larger ones spread a row over blocks (k_beam_rows), whose
 // lists a second kernel joins (k_beam_join).
 #include "rvq_internal.cuh"
+#include "rvq_overlap.h"
 #include "rvq_rows.cuh"
 #include "sm103_ptx.cuh"
 
@@ -640,6 +641,34 @@ BeamPlan beam_plan(const rvq_beam_dims &dm) {
   return p;
 }
 
+RowSet source_rows(const rvq_beam_dims &dm, const rvq_beam_state &s) {
+  return {s.src, s.row_bytes, {{s.layers, s.src_layer_stride}, {dm.groups, s.src_group_stride}, {dm.beams, s.src_beam_stride}}};
+}
+RowSet target_rows(const rvq_beam_dims &dm, const rvq_beam_state &s) {
+  return {s.dst, s.row_bytes, {{s.layers, s.dst_layer_stride}, {dm.groups, s.dst_group_stride}, {dm.select, s.dst_beam_stride}}};
+}
+
+// Blocks take rows in any order, and the states of a call at the same time: what
+// one writes must meet nothing else that is written, and nothing that is read
+// but the source of a move by the state that a later kernel reorders in place.
+rvq_status check_states(const rvq_beam_dims &dm, const int32_t *parents, const StateList &move, int moves,
+                        const StateList &swap, int swaps) {
+  bool some = false, unknown = false;
+  auto apart = [&](Overlap o) { some |= o == Overlap::kSome, unknown |= o == Overlap::kUnknown; };
+  const int n = moves + swaps;
+  auto state = [&](int i) -> const rvq_beam_state & { return i < moves ? move.s[i] : swap.s[i - moves]; };
+  const RowSet from = row_set(parents, dm.groups * dm.select * (int64_t)sizeof(int32_t), 1, 0);
+  for (int i = 0; i < n && !some; ++i) {
+    const RowSet to = target_rows(dm, state(i));
+    apart(overlaps_itself(to));
+    apart(overlap(to, from));
+    for (int j = 0; j < moves; ++j)
+      if (i < moves) apart(overlap(to, source_rows(dm, state(j))));
+    for (int j = i + 1; j < n; ++j) apart(overlap(to, target_rows(dm, state(j))));
+  }
+  return some ? RVQ_ERR_INVALID_ARG : unknown ? RVQ_ERR_UNSUPPORTED : RVQ_OK;
+}
+
 size_t beam_list_at(const rvq_beam_dims &dm, int splits) {
   return align_up((size_t)(dm.groups * dm.beams) * splits * sizeof(float2));
 }
@@ -732,6 +761,8 @@ RVQ_API rvq_status rvq_beam_reorder(rvq_beam_dims dims, const int32_t *parents, 
   }
   if (moves + swaps == 0) return RVQ_OK;
   if (!parents || !aligned_to(parents, 4)) return RVQ_ERR_INVALID_ARG;
+  const rvq_status apart = check_states(dims, parents, move, moves, swap, swaps);
+  if (apart != RVQ_OK) return apart;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (moves) {
     // neighbouring blocks take neighbouring pieces

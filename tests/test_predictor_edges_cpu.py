@@ -2,16 +2,27 @@
 without a GPU."""
 
 import contextlib
+import ctypes
+import itertools
 import os
+import random
 import re
+import subprocess
 
 import pytest
 import torch
 
 import residual_vector_quantisation_gb300 as rq
+from residual_vector_quantisation_gb300 import build as rqb
 
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "residual_vector_quantisation_gb300",
                     "csrc")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    rqb.build_library()
+    return rq.load_library()
 
 
 def kernels(name):
@@ -284,3 +295,95 @@ def test_quantiser_on_a_stream(monkeypatch, streams):
         call(given)
         assert ran.pop() == (None, "current") and not streams.used
         converted[:] = ["side"]
+
+
+# ---------------------------------------------------------------------------
+# overlapping memory
+# ---------------------------------------------------------------------------
+
+WRAPPER = """
+#include "rvq_overlap.h"
+static rvq::RowSet set(const int64_t *v) {
+  return {reinterpret_cast<const void *>(v[0]), v[1], {{v[2], v[3]}, {v[4], v[5]}, {v[6], v[7]}}};
+}
+extern "C" int itself(const int64_t *a) { return (int)rvq::overlaps_itself(set(a)); }
+extern "C" int both(const int64_t *a, const int64_t *b) { return (int)rvq::overlap(set(a), set(b)); }
+"""
+
+
+@pytest.fixture(scope="module")
+def regions(tmp_path_factory):
+    where = tmp_path_factory.mktemp("overlap")
+    source, library = where / "overlap.cpp", where / "overlap.so"
+    source.write_text(WRAPPER)
+    subprocess.run(["g++", "-std=c++17", "-O1", "-shared", "-fPIC", "-I", CSRC, str(source), "-o", str(library)], check=True)
+    lib = ctypes.CDLL(str(library))
+    return lambda *sets: (lib.itself if len(sets) == 1 else lib.both)(*((ctypes.c_int64 * 8)(*s) for s in sets))
+
+
+def every_byte(base, row, *axes):
+    counts, strides = axes[0::2], axes[1::2]
+    return [base + sum(i * s for i, s in zip(index, strides)) + b
+            for index in itertools.product(*(range(n) for n in counts)) for b in range(row)]
+
+
+def test_overlaps_byte_by_byte(regions):
+    """Random sets of rows, nested, interleaved and crossing, with negative strides and strides of 0."""
+    r = random.Random(1)
+    seen = set()
+    for _ in range(6000):
+        sets = []
+        for _ in range(2):
+            s = [1000 + r.randint(0, 60), r.randint(1, 6)]
+            for _ in range(3):
+                s += [r.choice([1, 1, 2, 3, 5]), r.choice([0, 1, 2, 3, 4, 6, 8, 12, 16, 24, 25, 48, -4, -12])]
+            sets.append(s)
+        if r.random() < 0.4:
+            sets[1][3::2] = sets[0][3::2]
+        bytes_of = [every_byte(*s) for s in sets]
+        alone = int(len(set(bytes_of[0])) < len(bytes_of[0]))
+        common = int(bool(set(bytes_of[0]) & set(bytes_of[1])))
+        assert regions(sets[0]) == alone, sets[0]
+        assert regions(*sets) == common and regions(*sets[::-1]) == common, sets
+        seen.add((alone, common))
+    assert len(seen) == 4
+
+
+def test_overlaps_of_large_layouts(regions):
+    g, t, w = 1 << 20, 4096, 1024
+    keys = [1 << 40, w, 48, 2 * g * 8 * w, g, 2 * 8 * w, 8, 2 * w]       # [layer][group][beam][key, value][w]
+    values = [(1 << 40) + w] + keys[1:]
+    assert regions(keys) == 0 and regions(keys, values) == 0
+    assert regions(keys, [(1 << 40) + w - 1] + keys[1:]) == 1
+    assert regions([1 << 40, w, 48, 0, g, 8 * w, 8, w]) == 1
+    # a part of one buffer to another part of it, with another number of slots and other strides
+    assert regions([0, w, 48, g * 16 * t, g, 16 * t, 4, t], [w, w, 48, g * 16 * t, g, 16 * t, 16, t]) == 0
+    assert regions([0, w, 48, g * 16 * t, g, 16 * t, 4, t], [w, t, 48, g * 16 * t, g, 16 * t, 16, t]) == 1
+    # strides that do not nest are given up after a bounded number of steps, or told apart
+    assert regions([0, 2, g, 3 << 30, g, 5 << 20, g, 7 << 10]) in (1, 2)
+    assert regions([0, 1, 1 << 40, 2, 1, 0, 1, 0], [1, 1, 1 << 40, 4, 1, 0, 1, 0]) in (0, 2)
+
+
+INVALID = -1
+
+
+def test_reorder_refuses_overlaps(lib):
+    """All of these are refused on the host: none reaches a launch."""
+    dims = rq.rvq_beam_dims(3, 4, 100, 4, 0, 1)
+    a, b, parents = 1 << 20, 2 << 20, ctypes.c_void_p(3 << 20)
+
+    def state(src=a, dst=b, layers=2, row=16, ls=192, gs=64, bs=16, dls=192, dgs=64, dbs=16):
+        return rq.rvq_beam_state(src, dst, layers, row, ls, gs, bs, dls, dgs, dbs)
+
+    def run(*states, where=parents):
+        return lib.rvq_beam_reorder(dims, where, (rq.rvq_beam_state * len(states))(*states), len(states), None)
+
+    for bad in (state(dbs=0), state(dgs=0), state(dls=0), state(dbs=15), state(dgs=48), state(dls=176),     # in itself
+                state(dst=a + 16), state(dst=a - 16), state(dst=a + 383), state(src=a, dst=a, bs=0, dbs=0),
+                state(dst=a, gs=128, dgs=64)):
+        assert run(bad) == INVALID
+    assert run(state(), state(dst=b + 64)) == INVALID                          # two destinations
+    assert run(state(), state(src=b, dst=4 << 20)) == INVALID                  # a chain
+    assert run(state(src=a, dst=a), state(src=b, dst=a + 16)) == INVALID       # into what is reordered in place
+    assert run(state(src=a, dst=a), state(src=a, dst=a)) == INVALID            # in place twice
+    assert run(state(), where=ctypes.c_void_p(b + 380)) == INVALID             # over the parents

@@ -170,3 +170,52 @@ def test_beam_search_on_a_stream_of_its_own():
             assert torch.equal(a, b)
         del junk
     torch.cuda.synchronize()
+
+
+# ---------------------------------------------------------------------------
+# reordering
+# ---------------------------------------------------------------------------
+
+def follow(state, parents):
+    """[layers][groups][beams][...] by the parents."""
+    groups = torch.arange(state.shape[1], device=DEV)[:, None]
+    return state[:, groups, parents.long()]
+
+
+def test_reorder_states_that_lie_between_one_another():
+    """The keys and values of one cache in place, and halves of one buffer moved to one another's other halves: their
+    address ranges overlap, their rows do not."""
+    g = gen(5)
+    layers, groups, beams = 3, 6, 4
+    parents = torch.randint(0, beams, (groups, beams), generator=g, device=DEV, dtype=torch.int32)
+    dims = rq.rvq_beam_dims(groups, beams, 10, beams, rq.RVQ_BEAM_RAW, 0)
+    cache = randn(g, layers, groups, beams, 2, 24, 8)
+    want = follow(cache, parents)
+    both = [(cache[:, :, :, i], cache[:, :, :, i]) for i in range(2)]
+    rq.rvq_beam_reorder(dims, parents, rq.rvq_beam_states(both, layered=True))
+    assert torch.equal(cache, want)
+
+    buffer = randn(g, layers, groups, beams, 2, 5)
+    want = buffer.clone()
+    want[..., 1, :] = follow(buffer[..., 0, :], parents)
+    rq.rvq_beam_reorder(dims, parents, rq.rvq_beam_states([(buffer[..., 0, :], buffer[..., 1, :])], layered=True))
+    assert torch.equal(buffer, want)
+
+    # kept as it was and reordered in place by one call: the move is first
+    state, held = randn(g, layers, groups, beams, 40), torch.zeros((layers, groups, beams, 40), device=DEV)
+    want = follow(state, parents)
+    rq.rvq_beam_reorder(dims, parents, rq.rvq_beam_states([(state, state), (state, held)], layered=True))
+    assert torch.equal(held, want) and torch.equal(state, want)
+
+
+def test_reorder_python_refuses_overlaps():
+    search = rq.BeamSearch(3, 4, 10)
+    parents = torch.zeros((3, 4), dtype=torch.int32, device=DEV)
+    state = torch.zeros((3, 4, 16), device=DEV)
+    with pytest.raises(rq.RVQError):
+        search.reorder(parents, state, torch.zeros((3, 1, 16), device=DEV).expand(3, 4, 16))
+    wide = torch.zeros(3 * 4 * 16 + 4, device=DEV)
+    with pytest.raises(rq.RVQError):
+        search.reorder(parents, wide[4:].view(3, 4, 16), wide[:-4].view(3, 4, 16))
+    # a source may be expanded: it is only read
+    assert search.reorder(parents, torch.ones((3, 1, 16), device=DEV).expand(3, 4, 16)).eq(1).all()
