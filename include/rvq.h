@@ -472,7 +472,8 @@ RVQ_API size_t rvq_beam_workspace_bytes(rvq_beam_dims dims);
  * not NULL, out_finished (bytes: the parent was finished, or the code is
  * end_code).  A slot for which no candidate is left gets -inf, -1, -1 and
  * finished 1.  Where select == beams, out_scores may be scores and
- * out_finished may be finished. */
+ * out_finished may be finished; other overlaps of what is written with one
+ * another or with the inputs are refused (RVQ_ERR_INVALID_ARG). */
 RVQ_API rvq_status rvq_beam_select(rvq_beam_dims dims, const void *logits, int64_t logits_stride, const float *scores,
                                    const uint8_t *finished, int32_t end_code, float *out_scores, int32_t *parents,
                                    int32_t *codes, uint8_t *out_finished, void *workspace, size_t workspace_bytes,

@@ -673,6 +673,31 @@ size_t beam_list_at(const rvq_beam_dims &dm, int splits) {
   return align_up((size_t)(dm.groups * dm.beams) * splits * sizeof(float2));
 }
 
+// Groups are chosen in any order: what one writes must meet nothing that another
+// still reads.  Over the scores and flags that they come from, the outputs must
+// be a group's own.
+rvq_status check_outputs(const BeamArgs &a, bool group, const void *workspace, size_t workspace_bytes) {
+  const rvq_beam_dims &dm = a.dm;
+  const int64_t held = dm.groups * dm.beams, kept = dm.groups * dm.select;
+  auto flat = [](const void *p, int64_t bytes) { return row_set(p, bytes, 1, 0); };
+  const RowSet out[5] = {flat(a.out_scores, kept * 4), flat(a.parents, kept * 4), flat(a.codes, kept * 4),
+                         flat(a.out_finished, a.out_finished ? kept : 0),
+                         flat(workspace, group ? 0 : (int64_t)workspace_bytes)};
+  const RowSet in[3] = {flat(a.scores, held * 4), flat(a.finished, a.finished ? held : 0),
+                        row_set(a.logits, (int64_t)dm.vocab * dtype_bytes(dm.dtype), held, a.stride * dtype_bytes(dm.dtype))};
+  const bool own = dm.select == dm.beams;
+  for (int i = 0; i < 5; ++i) {
+    if (out[i].row == 0) continue;
+    for (int j = i + 1; j < 5; ++j)
+      if (out[j].row && overlap(out[i], out[j]) != Overlap::kNone) return RVQ_ERR_INVALID_ARG;
+    for (int j = 0; j < 3; ++j) {
+      if (own && ((i == 0 && j == 0) || (i == 3 && j == 1)) && out[i].base == in[j].base) continue;
+      if (in[j].row && overlap(out[i], in[j]) != Overlap::kNone) return RVQ_ERR_INVALID_ARG;
+    }
+  }
+  return RVQ_OK;
+}
+
 std::atomic<bool> g_join_allowed[64];
 template <class T>
 cudaError_t launch_beam(const BeamArgs &a, const BeamPlan &p, cudaStream_t st) {
@@ -721,6 +746,8 @@ RVQ_API rvq_status rvq_beam_select(rvq_beam_dims dims, const void *logits, int64
   const BeamPlan p = beam_plan(dims);
   const BeamArgs a{dims, logits, logits_stride, scores, finished, end_code, out_scores, parents, codes, out_finished,
                    p.splits, {at<float2>(workspace, 0), at<uint64_t>(workspace, beam_list_at(dims, p.splits))}};
+  const rvq_status apart = check_outputs(a, p.group, workspace, rvq_beam_workspace_bytes(dims));
+  if (apart != RVQ_OK) return apart;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = dims.dtype == RVQ_DTYPE_F32    ? launch_beam<float>(a, p, st)
                         : dims.dtype == RVQ_DTYPE_BF16 ? launch_beam<__nv_bfloat16>(a, p, st)

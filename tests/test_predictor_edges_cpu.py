@@ -387,3 +387,31 @@ def test_reorder_refuses_overlaps(lib):
     assert run(state(src=a, dst=a), state(src=b, dst=a + 16)) == INVALID       # into what is reordered in place
     assert run(state(src=a, dst=a), state(src=a, dst=a)) == INVALID            # in place twice
     assert run(state(), where=ctypes.c_void_p(b + 380)) == INVALID             # over the parents
+
+
+@pytest.mark.parametrize("vocab", [100, 70000])
+def test_select_refuses_overlaps(lib, vocab):
+    """Refused on the host; 3 groups, 4 beams in, 5 out."""
+    a = 1 << 24
+    place = {"z": a, "s": 2 * a, "f": 3 * a, "o": 4 * a, "p": 5 * a, "c": 6 * a, "of": 7 * a, "ws": 8 * a}
+
+    def run(select, **kw):
+        dims = rq.rvq_beam_dims(3, 4, vocab, select, 0, 1)
+        at = {k: ctypes.c_void_p(v) for k, v in {**place, **kw}.items()}
+        nbytes = lib.rvq_beam_workspace_bytes(dims)
+        return lib.rvq_beam_select(dims, at["z"], vocab, at["s"], at["f"], 7, at["o"], at["p"], at["c"], at["of"],
+                                   at["ws"], nbytes, None)
+
+    assert run(5, o=place["s"]) == INVALID and run(5, of=place["f"]) == INVALID      # not the same number of slots
+    for select, kept in ((4, 12), (5, 15)):
+        assert run(select, o=place["s"] + 4) == INVALID and run(select, of=place["f"] + 11) == INVALID
+        for out, size in (("o", 4), ("p", 4), ("c", 4), ("of", 1)):
+            for other, bytes_of in (("s", 48), ("f", 12), ("z", 12 * vocab * 2), ("o", 4 * kept), ("p", 4 * kept),
+                                    ("c", 4 * kept), ("of", kept)):
+                if other in (out, {"o": "s", "of": "f"}.get(out)):
+                    continue
+                assert run(select, **{out: place[other] + (bytes_of - 1) // size * size}) == INVALID, (out, other)
+                assert run(select, **{out: place[other] - (kept - 1) * size}) == INVALID, (out, other)
+    if vocab > 1000:                                                                  # a workspace that is used
+        for name in ("z", "s", "f", "o", "p", "c", "of"):
+            assert run(4, ws=place[name]) == INVALID
