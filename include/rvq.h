@@ -367,7 +367,8 @@ typedef struct rvq_norm_dims {
 /* y = (x - mean) * rstd * weight + bias per row, with mean and
  * rstd = 1 / sqrt(var + eps) of the row (var: the mean squared deviation).
  * weight and bias are nullable (one and zero).  mean and rstd ([rows],
- * nullable) are kept for the backward pass.  y may be x. */
+ * nullable) are kept for the backward pass.  y may be x (same stride); rows
+ * that overlap in another way are refused (RVQ_ERR_INVALID_ARG). */
 RVQ_API rvq_status rvq_layer_norm(rvq_norm_dims dims, const void *x, int64_t x_stride, const void *weight,
                                   const void *bias, void *y, int64_t y_stride, float *mean, float *rstd,
                                   rvq_stream_t stream);
@@ -378,7 +379,8 @@ RVQ_API size_t rvq_layer_norm_workspace_bytes(int64_t rows, int32_t width);
 /* Gradients of rvq_layer_norm: with h = (x - mean) * rstd and g = dy * weight,
  *   dx = rstd * (g - mean(g) - h * mean(g * h)),
  *   dweight = sum over rows of dy * h,  dbias = sum over rows of dy.
- * dx, dweight and dbias are each nullable (not computed); dx may be dy or x.
+ * dx, dweight and dbias are each nullable (not computed); dx may be dy or x
+ * (same stride); rows that overlap in another way are refused.
  * With zero rows dweight and dbias are set to zero.  The workspace (16-byte
  * aligned) is needed for dweight and dbias; its contents mean nothing before
  * and after the call. */
@@ -422,7 +424,8 @@ typedef struct rvq_distill_dims {
  * Writes loss [rows]; if not NULL, lse [rows][2] for rvq_distill_backward (the
  * largest logit m and the sum of exp((logit - m) / T) over all codes, or, with
  * teacher_lse, over the codes without an entry; zeros where w = 0); if not
- * NULL, dlogits = d loss / d logits in the same pass.  dlogits may be logits itself (same stride). */
+ * NULL, dlogits = d loss / d logits in the same pass.  dlogits may be logits
+ * itself (same stride); rows that overlap in another way are refused. */
 RVQ_API rvq_status rvq_distill(rvq_distill_dims dims, const void *logits, int64_t logits_stride,
                                const void *top_logits, const int32_t *top_codes, const float *teacher_lse,
                                const float *weights, float *loss, float *lse, void *dlogits, int64_t dlogits_stride,

@@ -11,6 +11,7 @@
 // a sum, not 1 minus a sum, and keeps its digits when the list holds nearly
 // everything.
 #include "rvq_internal.cuh"
+#include "rvq_overlap.h"
 #include "rvq_rows.cuh"
 
 namespace rvq {
@@ -721,6 +722,9 @@ rvq_status check_distill(const DistillArgs &a) {
       !aligned_to(a.bad_codes, 8))
     return RVQ_ERR_INVALID_ARG;
   if (dm.rows > 1 && (a.logits_stride < dm.vocab || (a.dlogits && a.dlogits_stride < dm.vocab)))
+    return RVQ_ERR_INVALID_ARG;
+  // blocks take rows in any order
+  if (a.dlogits && !rows_apart(a.dlogits, a.dlogits_stride * e, a.logits, a.logits_stride * e, dm.rows, (int64_t)dm.vocab * e))
     return RVQ_ERR_INVALID_ARG;
   return RVQ_OK;
 }

@@ -17,6 +17,7 @@
 // a boundary in each row; else, and above 8192 columns, k_norm and
 // k_norm_backward hold a row in registers.
 #include "rvq_internal.cuh"
+#include "rvq_overlap.h"
 #include "rvq_rows.cuh"
 #include "sm103_ptx.cuh"
 
@@ -795,6 +796,11 @@ rvq_status check_norm(const rvq_norm_dims &dm) {
 bool rows_ok(const void *p, int64_t stride, const rvq_norm_dims &dm) {
   return p && aligned_to(p, dtype_bytes(dm.dtype)) && (stride >= dm.width || dm.rows <= 1);
 }
+// Rows that may be written where the rows of `in` are read: blocks take rows in any order.
+bool apart(const void *out, int64_t out_stride, const void *in, int64_t in_stride, const rvq_norm_dims &dm) {
+  const int e = dtype_bytes(dm.dtype);
+  return rows_apart(out, out_stride * e, in, in_stride * e, dm.rows, (int64_t)dm.width * e);
+}
 
 }  // namespace
 }  // namespace rvq
@@ -808,7 +814,8 @@ RVQ_API rvq_status rvq_layer_norm(rvq_norm_dims dims, const void *x, int64_t x_s
   const rvq_status s = check_norm(dims);
   if (s != RVQ_OK || dims.rows == 0) return s;
   const int pe = dtype_bytes(dims.param_dtype);
-  if (!rows_ok(x, x_stride, dims) || !rows_ok(y, y_stride, dims)) return RVQ_ERR_INVALID_ARG;
+  if (!rows_ok(x, x_stride, dims) || !rows_ok(y, y_stride, dims) || !apart(y, y_stride, x, x_stride, dims))
+    return RVQ_ERR_INVALID_ARG;
   if (!aligned_to(weight, pe) || !aligned_to(bias, pe) || !aligned_to(mean, 4) || !aligned_to(rstd, 4))
     return RVQ_ERR_INVALID_ARG;
   NormArgs a{};
@@ -839,6 +846,8 @@ RVQ_API rvq_status rvq_layer_norm_backward(rvq_norm_dims dims, const void *dy, i
     return RVQ_OK;
   }
   if (!rows_ok(dy, dy_stride, dims) || !rows_ok(x, x_stride, dims) || (dx && !rows_ok(dx, dx_stride, dims)))
+    return RVQ_ERR_INVALID_ARG;
+  if (dx && (!apart(dx, dx_stride, dy, dy_stride, dims) || !apart(dx, dx_stride, x, x_stride, dims)))
     return RVQ_ERR_INVALID_ARG;
   if (!mean || !rstd || !aligned_to(mean, 4) || !aligned_to(rstd, 4)) return RVQ_ERR_INVALID_ARG;
   const bool params = dweight || dbias;

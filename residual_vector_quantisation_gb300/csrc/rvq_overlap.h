@@ -106,4 +106,11 @@ inline Overlap overlap(const RowSet &s, const RowSet &t) {
   return r.find(start, s.row, t.row, false);
 }
 
+// Whether rows that are written may lie where rows of the same number and size
+// are read (strides in bytes): they are the same ones, or meet none of them.
+inline bool rows_apart(const void *out, int64_t out_stride, const void *in, int64_t in_stride, int64_t rows, int64_t row) {
+  if (out == in && (rows <= 1 || out_stride == in_stride)) return true;
+  return overlap(row_set(out, row, rows, out_stride), row_set(in, row, rows, in_stride)) == Overlap::kNone;
+}
+
 }  // namespace rvq

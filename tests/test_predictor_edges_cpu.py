@@ -415,3 +415,21 @@ def test_select_refuses_overlaps(lib, vocab):
     if vocab > 1000:                                                                  # a workspace that is used
         for name in ("z", "s", "f", "o", "p", "c", "of"):
             assert run(4, ws=place[name]) == INVALID
+
+
+def test_norm_and_distill_refuse_overlaps(lib):
+    """Outputs that meet their inputs anywhere but row by row; refused on the host."""
+    at = 1 << 24
+    norm = rq.rvq_norm_dims(4, 64, 1, 0, 1e-5)                       # rows of 128 bytes
+    distill = rq.rvq_distill_dims(4, 64, 8, 1, 0, 1.0)
+    far = ctypes.c_void_p(1 << 26)
+    for stride, to, to_stride in ((64, at, 65), (64, at + 2, 64), (64, at - 128, 64), (64, at + 3 * 128 + 126, 64),
+                                  (96, at + 64 * 2 - 2, 96), (200, at + 128 + 2, 130)):
+        x, y = ctypes.c_void_p(at), ctypes.c_void_p(to)
+        assert lib.rvq_layer_norm(norm, x, stride, None, None, y, to_stride, None, None, None) == INVALID
+        for dy, other in ((x, far), (far, x)):
+            strides = (stride, 64) if dy is x else (64, stride)
+            assert lib.rvq_layer_norm_backward(norm, dy, strides[0], other, strides[1], None, far, far, y, to_stride, None,
+                                               None, None, 0, None) == INVALID
+        assert lib.rvq_distill(distill, x, stride, far, far, None, None, far, None, y, to_stride, None, None) == INVALID
+        assert lib.rvq_distill_backward(distill, None, x, stride, far, far, None, None, far, y, to_stride, None) == INVALID

@@ -219,3 +219,26 @@ def test_reorder_python_refuses_overlaps():
         search.reorder(parents, wide[4:].view(3, 4, 16), wide[:-4].view(3, 4, 16))
     # a source may be expanded: it is only read
     assert search.reorder(parents, torch.ones((3, 1, 16), device=DEV).expand(3, 4, 16)).eq(1).all()
+
+
+def test_norm_and_distill_side_by_side_in_one_buffer():
+    """Outputs in the other half of their inputs' rows, and between the inputs' rows: nothing is shared."""
+    g = gen(7)
+    rows, width = 50, 96
+    w = 1 + 0.2 * randn(g, width)
+    buffer = randn(g, rows, 3 * width)
+    x, dy, out = buffer.split(width, 1)
+    val, tol = ref.norm(x, w, None, 1e-5, dy)
+    mean, rstd = torch.empty(rows, device=DEV), torch.empty(rows, device=DEV)
+    rq.rvq_layer_norm(x, w, None, 1e-5, out, mean, rstd)
+    ref.check(out, val["y"], tol["y"], "y")
+    rq.rvq_layer_norm_backward(dy, x, w, mean, rstd, out, None, None, None)
+    ref.check(out, val["dx"], tol["dx"], "dx")
+    buffer = randn(g, 2 * rows, width)
+    z, d = buffer[0::2], buffer[1::2]
+    t, codes = torch.topk(randn(g, rows, width), 8, dim=1)
+    loss = torch.empty(rows, device=DEV)
+    val, tol, _ = ref.distill(z, t, codes.to(torch.int32), None, None, 1.0)
+    rq.rvq_distill(z, t, codes.to(torch.int32), None, None, 1.0, loss, dlogits=d)
+    ref.check(loss, val["loss"], tol["loss"], "loss")
+    ref.check(d, val["dlogits"], tol["dlogits"], "dlogits")
