@@ -461,8 +461,10 @@ RVQ_API size_t rvq_beam_workspace_bytes(rvq_beam_dims dims);
 /* Per group, the `select` best candidates (beam b, code v) by
  *   total = scores[b] + logits[b][v] - log sum exp(logits[b])   (RVQ_BEAM_LOGITS)
  *   total = scores[b] + logits[b][v]                            (RVQ_BEAM_RAW)
- * in float32, best first; equal totals: the lower beam first, then (of one
- * beam) the larger logit, then the lower code.
+ * in float32, best first; equal totals: the lower beam first, then, of one
+ * beam, in RVQ_BEAM_LOGITS the larger logit, and then the lower code.  (In
+ * RVQ_BEAM_RAW the total is one rounded sum: values that it does not tell apart
+ * are equal, and the lower code is first whichever was the larger.)
  *   logits [groups * beams] rows of vocab, logits_stride apart;
  *   scores [groups][beams]; a beam whose score is -inf or NaN has no
  *     candidates and its row is not read (the first step of a search: one

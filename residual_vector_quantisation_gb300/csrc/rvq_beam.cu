@@ -27,8 +27,8 @@ constexpr int kLane = 32;              // elements of a lane in a piece of a gro
 constexpr int kRowVectors = 16;        // 16-byte vectors of a lane in a piece of a block that shares a row
 constexpr int kRoom = 128;             // entries that a warp puts in order at once, beside those it holds
 
-// An entry's place in the order: the larger value first, then the lower code.
-// 0 is no entry (NaN and -inf have none).
+// An entry's place in the order: the larger value (of raw values: value + score,
+// rounded) first, then the lower code.  0 is no entry (NaN and -inf have none).
 __device__ __forceinline__ uint32_t order_of(float v) {
   if (!(v > -CUDART_INF_F)) return 0;
   const uint32_t b = __float_as_uint(v + 0.f);  // -0 becomes 0

@@ -242,3 +242,27 @@ def test_norm_and_distill_side_by_side_in_one_buffer():
     rq.rvq_distill(z, t, codes.to(torch.int32), None, None, 1.0, loss, dlogits=d)
     ref.check(loss, val["loss"], tol["loss"], "loss")
     ref.check(d, val["dlogits"], tol["dlogits"], "dlogits")
+
+
+# ---------------------------------------------------------------------------
+# the beam step's order
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("vocab,select", [(40, 3), (1025, 5), (70000, 4), (70000, 40)])
+def test_beam_ties_of_rounded_totals(vocab, select):
+    """Scores so large that a total's rounding swallows what tells the values apart.  Raw values: their totals are
+    equal, the lower code is first.  Log probabilities: within a beam the larger logit is first all the same."""
+    rising = (torch.arange(vocab, device=DEV) % 97).float() / 1024                     # the larger ones are not the first ones
+    scores = torch.tensor([[1048576.0, 1048576.0]], device=DEV)        # an ulp of 1/8
+    logits = torch.stack([rising, rising.flip(0)])[None].contiguous()
+    for raw in (True, False):
+        search = rq.BeamSearch(1, 2, vocab, select, "raw" if raw else "logits")
+        out, parents, codes, _ = search.select(logits, scores)
+        total = scores.double()[:, :, None] + (logits.double() if raw else torch.log_softmax(logits.double(), 2))
+        total = total.float()                             # few values, of many candidates each
+        assert len(total.unique()) < len(rising.unique())
+        values, z = total[0].tolist(), logits[0].tolist()
+        best = sorted((-values[b][v], b, 0.0 if raw else -z[b][v], v) for b in range(2) for v in range(vocab))[:select]
+        assert parents[0].tolist() == [c[1] for c in best]
+        assert codes[0].tolist() == [c[3] for c in best], raw
+        assert out[0].tolist() == [-c[0] for c in best]
