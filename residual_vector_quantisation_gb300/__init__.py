@@ -487,9 +487,9 @@ def rvq_beam_select(dims: rvq_beam_dims, logits, scores, finished, end_code: int
     if DTYPES.get(logits.dtype) != dims.dtype:
         raise ValueError("logits must have the dtype in dims")
     if logits.dim() == 3:
-        if logits.shape != (groups, beams, vocab) or (groups > 1 and logits.stride(0) != beams * logits.stride(1)):
+        stride = logits.stride(0 if beams == 1 else 1)  # (an axis of size one may have any)
+        if logits.shape != (groups, beams, vocab) or (groups > 1 and logits.stride(0) != beams * stride):
             raise ValueError(f"logits must be {(groups, beams, vocab)} with evenly spaced rows")
-        stride = logits.stride(1)
     else:
         if logits.shape != (groups * beams, vocab):
             raise ValueError(f"logits must be {(groups, beams, vocab)} or {(groups * beams, vocab)}")

@@ -433,3 +433,32 @@ def test_norm_and_distill_refuse_overlaps(lib):
                                                None, None, 0, None) == INVALID
         assert lib.rvq_distill(distill, x, stride, far, far, None, None, far, None, y, to_stride, None, None) == INVALID
         assert lib.rvq_distill_backward(distill, None, x, stride, far, far, None, None, far, y, to_stride, None) == INVALID
+
+
+def test_select_takes_one_beam_of_longer_rows(monkeypatch, gpus):
+    """The last position's logits of [groups][length][vocab]: rows evenly spaced, the beams' axis of size one having a
+    stride of its own."""
+    strides = []
+    monkeypatch.setattr(rq, "_enqueue", lambda name, on, stream, dims, p, stride, *rest: strides.append(stride))
+    dims = rq.rvq_beam_dims(2, 1, 10, 1, 0, 0)
+    kept = OnGpu(0, 2, 1, dtype=I32)
+
+    def run(view):
+        logits = OnGpu(0)
+        logits.t = view
+        rq.rvq_beam_select(dims, logits, OnGpu(0, 2, 1), None, -1, OnGpu(0, 2, 1), kept, kept, None,
+                           OnGpu(0, 64, dtype=U8))
+        return strides.pop()
+
+    wide = torch.zeros(2, 5, 12)
+    assert run(wide[:, -1:, :10]) == 60 and run(wide[:, -1, :10][:, None]) == 60 and run(wide[:, 0, :10]) == 60
+    assert run(torch.zeros(2, 1, 10)) == 10
+    dims = rq.rvq_beam_dims(2, 5, 10, 1, 0, 0)
+    rows = OnGpu(0)
+    rows.t = wide[..., :10]
+    held, one = OnGpu(0, 2, 5), OnGpu(0, 2, 1)
+    rq.rvq_beam_select(dims, rows, held, None, -1, one, kept, kept, None, OnGpu(0, 64, dtype=U8))
+    assert strides.pop() == 12
+    rows.t = torch.zeros(2, 6, 12)[:, :5, :10]
+    with pytest.raises(ValueError):
+        rq.rvq_beam_select(dims, rows, held, None, -1, one, kept, kept, None, OnGpu(0, 64, dtype=U8))

@@ -266,3 +266,15 @@ def test_beam_ties_of_rounded_totals(vocab, select):
         assert parents[0].tolist() == [c[1] for c in best]
         assert codes[0].tolist() == [c[3] for c in best], raw
         assert out[0].tolist() == [-c[0] for c in best]
+
+
+def test_beam_of_one_from_the_last_position():
+    g = gen(8)
+    logits = (randn(g, 6, 3, 1030) * 48).round() / 16
+    scores = -(randn(g, 6, 1) * 24).round().abs() / 8
+    search = rq.BeamSearch(6, 1, 1025, 1)
+    out, parents, codes, _ = search.select(logits[:, -1:, :1025], scores)
+    assert torch.equal(codes, logits[:, -1, :1025].argmax(1, keepdim=True).int()) and not bool(parents.any())
+    want = scores.double() + torch.log_softmax(logits[:, -1, :1025].double(), 1).amax(1, keepdim=True)
+    # as for every step: 16 roundings of the largest term
+    ref.check(out, want, 16 * ref.U * (want.abs().cpu() + logits.abs().max().item() + math.log(1025)), "scores")
