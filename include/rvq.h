@@ -392,7 +392,7 @@ RVQ_API rvq_status rvq_layer_norm_backward(rvq_norm_dims dims, const void *dy, i
 /* Distillation of `rows` rows of `vocab` student logits from each row's `top`
  * teacher entries (1 <= vocab <= 2^20, 1 <= top <= 256).  dtype: of logits and
  * dlogits; top_dtype: of the teacher's logits; temperature T > 0 divides both
- * sides' logits. */
+ * sides' logits (log2(e) / T has to be a float32: T of at least 4.3e-39). */
 typedef struct rvq_distill_dims {
   int64_t rows;
   int32_t vocab;

@@ -712,7 +712,9 @@ rvq_status check_distill(const DistillArgs &a) {
   const rvq_distill_dims &dm = a.dm;
   const int e = dtype_bytes(dm.dtype), te = dtype_bytes(dm.top_dtype);
   if (dm.rows < 0 || dm.vocab <= 0 || dm.top <= 0 || !e || !te) return RVQ_ERR_INVALID_ARG;
-  if (!(dm.temperature > 0.f) || dm.temperature > 3.402823466e38f) return RVQ_ERR_INVALID_ARG;
+  constexpr float kMost = 3.402823466e38f;  // of a temperature, and of what launch_distill makes of it
+  if (!(dm.temperature > 0.f) || dm.temperature > kMost || !(kLog2e * (1.f / dm.temperature) <= kMost))
+    return RVQ_ERR_INVALID_ARG;
   if (dm.vocab > kDistillMaxVocab || dm.top > kDistillMaxTop) return RVQ_ERR_UNSUPPORTED;
   if (dm.rows == 0) return RVQ_OK;
   if (!a.logits || !a.top_logits || !a.top_codes) return RVQ_ERR_INVALID_ARG;

@@ -462,3 +462,17 @@ def test_select_takes_one_beam_of_longer_rows(monkeypatch, gpus):
     rows.t = torch.zeros(2, 6, 12)[:, :5, :10]
     with pytest.raises(ValueError):
         rq.rvq_beam_select(dims, rows, held, None, -1, one, kept, kept, None, OnGpu(0, 64, dtype=U8))
+
+
+def test_distill_refuses_temperatures_without_an_inverse(lib):
+    """1 / T, or log2(e) / T, past float32 (the temperature itself a positive number)."""
+    far = ctypes.c_void_p(1 << 26)
+
+    def run(rows, temperature):
+        dims = rq.rvq_distill_dims(rows, 64, 8, 1, 0, temperature)
+        return lib.rvq_distill(dims, ctypes.c_void_p(1 << 24), 64, far, far, None, None, far, None, None, 0, None, None)
+
+    for temperature in (1.5e-45, 1e-39, 2.9e-39, 4.2e-39):
+        assert run(4, temperature) == INVALID and run(0, temperature) == INVALID
+    for temperature in (4.3e-39, 1.2e-38, 1.0, 3.4e38):      # no rows: nothing is launched
+        assert run(0, temperature) == 0

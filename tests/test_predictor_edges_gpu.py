@@ -278,3 +278,20 @@ def test_beam_of_one_from_the_last_position():
     want = scores.double() + torch.log_softmax(logits[:, -1, :1025].double(), 1).amax(1, keepdim=True)
     # as for every step: 16 roundings of the largest term
     ref.check(out, want, 16 * ref.U * (want.abs().cpu() + logits.abs().max().item() + math.log(1025)), "scores")
+
+
+# ---------------------------------------------------------------------------
+# distillation
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("vocab", [100, 3000, 20000])
+def test_distill_lowest_temperature(vocab, tail):
+    """At the lowest temperature that is taken both sides are all on their largest logit: no loss, no gradient."""
+    g = gen(vocab)
+    z = randn(g, 5, vocab)
+    t, codes = torch.topk(z, 4, dim=1)
+    t, codes, lse = t - t[:, :1], codes.to(torch.int32), torch.zeros(5, device=DEV) if tail else None
+    loss, d = torch.full((5,), math.nan, device=DEV), torch.full_like(z, math.nan)
+    rq.rvq_distill(z, t, codes, lse, None, 4.3e-39, loss, dlogits=d)
+    assert bool((loss == 0).all()) and bool((d == 0).all())
