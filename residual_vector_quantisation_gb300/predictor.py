@@ -11,6 +11,7 @@ from typing import Optional
 
 import torch
 from torch.autograd.function import once_differentiable
+from torch.autograd.graph import increment_version
 
 import residual_vector_quantisation_gb300 as _rq
 
@@ -124,6 +125,7 @@ def distill_loss_and_grad(logits, top_logits, top_codes, teacher_lse=None, weigh
         dlogits = out if out.dim() == 2 else out.view(-1, out.shape[-1])
     loss = torch.empty(rows.shape[0], dtype=torch.float32, device=rows.device)
     _rq.rvq_distill(rows, *teacher, float(temperature), loss, dlogits=dlogits)
+    increment_version(out)  # written behind autograd's back: a backward pass that saved it has to notice
     return loss.view(logits.shape[:-1]), out
 
 
@@ -181,4 +183,5 @@ class BeamSearch:
             shape[lead + 1] = self.dims.select
             out = torch.empty(shape, dtype=state.dtype, device=state.device)
         _rq.rvq_beam_reorder(self.dims, parents, _rq.rvq_beam_states([(state, out)], layered), stream)
+        increment_version(out)
         return out

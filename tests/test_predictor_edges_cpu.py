@@ -476,3 +476,23 @@ def test_distill_refuses_temperatures_without_an_inverse(lib):
         assert run(4, temperature) == INVALID and run(0, temperature) == INVALID
     for temperature in (4.3e-39, 1.2e-38, 1.0, 3.4e38):      # no rows: nothing is launched
         assert run(0, temperature) == 0
+
+
+def test_autograd_notices_what_is_written_in_place(monkeypatch):
+    """The gradient over the logits, and states reordered in place: a backward pass that saved them must not use what
+    was written over them."""
+    monkeypatch.setattr(rq, "rvq_distill", lambda *a, **kw: None)
+    monkeypatch.setattr(rq, "rvq_beam_reorder", lambda *a: None)
+    monkeypatch.setattr(rq, "rvq_beam_states", lambda pairs, layered: pairs)
+    leaf = torch.ones(2, 3, 8, requires_grad=True)
+    logits = leaf * 2
+    squared = logits * logits
+    entries = torch.zeros(2, 3, 4)
+    _, out = rq.distill_loss_and_grad(logits.detach(), entries, entries.int(), out=logits.detach())
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        squared.sum().backward()
+    state = leaf * 3
+    squared = state * state
+    rq.BeamSearch(2, 3, 10, device="cpu").reorder(None, state.detach(), state.detach())
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        squared.sum().backward()
