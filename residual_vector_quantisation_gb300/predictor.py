@@ -76,7 +76,7 @@ def _teacher(logits, top_logits, top_codes, teacher_lse, weights):
             t = t.to(torch.float32).reshape(-1).contiguous()
         flat.append(t)
     if top_codes.dtype != torch.int32:  # a code past 32 bits stays out of range
-        top_codes = top_codes.clamp(-2, 2 ** 31 - 1).to(torch.int32)
+        top_codes = top_codes.to(torch.int64).clamp(-2, 2 ** 31 - 1).to(torch.int32)
     return rows, (top_logits.reshape(-1, top).contiguous(), top_codes.reshape(-1, top).contiguous(), *flat)
 
 

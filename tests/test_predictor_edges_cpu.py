@@ -13,7 +13,7 @@ import pytest
 import torch
 
 import residual_vector_quantisation_gb300 as rq
-from residual_vector_quantisation_gb300 import build as rqb
+from residual_vector_quantisation_gb300 import build as rqb, predictor
 
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "residual_vector_quantisation_gb300",
                     "csrc")
@@ -496,3 +496,16 @@ def test_autograd_notices_what_is_written_in_place(monkeypatch):
     rq.BeamSearch(2, 3, 10, device="cpu").reorder(None, state.detach(), state.detach())
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         squared.sum().backward()
+
+
+@pytest.mark.parametrize("dtype", [torch.int8, torch.uint8, torch.int16, torch.int32, torch.int64])
+def test_teacher_codes_of_any_integer_type(dtype):
+    """Narrow types (codes of 256 entries as bytes) hold no bound of 32 bits; a code past 32 bits stays out of range."""
+    codes = [[5, 0, 100], [127, 7, 3]] + ([[-1, -7, 2]] if dtype != torch.uint8 else [])
+    if dtype == torch.int64:
+        codes.append([(1 << 32) + 5, -(1 << 40), 2 ** 31 - 1])
+    given = torch.tensor(codes, dtype=dtype)
+    entries = torch.zeros(len(codes), 3)
+    _, (_, got, _, _) = predictor._teacher(torch.zeros(len(codes), 200), entries, given, None, None)
+    want = codes if dtype == torch.int32 else [[min(max(c, -2), 2 ** 31 - 1) for c in row] for row in codes]
+    assert got.dtype == torch.int32 and got.tolist() == want
