@@ -524,14 +524,14 @@ def rvq_beam_states(pairs, layered: bool = False):
             raise ValueError("a state and its destination differ in more than the number of beams")
         size = src.element_size()
         row = size
-        for t in (src, dst):
+        for t in (src, dst) if src.numel() else ():
             row = size
             for n, step in zip(reversed(t.shape[lead:]), reversed(t.stride()[lead:])):
                 if n != 1 and step * size != row:
                     raise ValueError("the axes of a state after the beams' must be contiguous")
                 row *= n
         a, b = ([st * size for st in t.stride()[:lead]] for t in (src, dst))
-        s.src, s.dst, s.row_bytes = src.data_ptr(), dst.data_ptr(), row
+        s.src, s.dst, s.row_bytes = src.data_ptr(), dst.data_ptr(), row if src.numel() else 0
         s.layers = src.shape[0] if layered else 1
         s.src_layer_stride, s.dst_layer_stride = (a[0], b[0]) if layered else (0, 0)
         s.src_group_stride, s.src_beam_stride = a[-2:]

@@ -509,3 +509,14 @@ def test_teacher_codes_of_any_integer_type(dtype):
     _, (_, got, _, _) = predictor._teacher(torch.zeros(len(codes), 200), entries, given, None, None)
     want = codes if dtype == torch.int32 else [[min(max(c, -2), 2 ** 31 - 1) for c in row] for row in codes]
     assert got.dtype == torch.int32 and got.tolist() == want
+
+
+def test_states_without_elements():
+    """A cache before its first entry, wherever its axis of length zero is: nothing to move, nothing to refuse."""
+    for row in ((0, 64), (4, 0, 64), (4, 2, 0), (0,)):
+        states = rq.rvq_beam_states([(OnGpu(0, 2, 3, *row), OnGpu(0, 2, 5, *row))])
+        assert states[0].row_bytes == 0
+    states = rq.rvq_beam_states([(OnGpu(0, 2, 3, 4, 2), OnGpu(0, 2, 5, 4, 2))])
+    assert states[0].row_bytes == 32
+    with pytest.raises(ValueError):
+        rq.rvq_beam_states([(OnGpu(0, 2, 3, 0, 64), OnGpu(0, 2, 5, 0, 65))])
