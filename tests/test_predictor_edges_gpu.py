@@ -295,3 +295,97 @@ def test_distill_lowest_temperature(vocab, tail):
     loss, d = torch.full((5,), math.nan, device=DEV), torch.full_like(z, math.nan)
     rq.rvq_distill(z, t, codes, lse, None, 4.3e-39, loss, dlogits=d)
     assert bool((loss == 0).all()) and bool((d == 0).all())
+
+
+# ---------------------------------------------------------------------------
+# kernels that a call reaches only by where its tensors lie, or by its counts
+# ---------------------------------------------------------------------------
+
+def places_of(width):
+    """(stride, shift) of x, dy, y and dx."""
+    return {"all": [(width + 1, 0), (width + 3, 1), (width + 2, 5), (width, 3)],
+            "dense results": [(width + 3, 0), (width, 0), (width, 0), (width, 0)],
+            "y": [(width + 8, 0), (width + 8, 0), (width + 8, 1), (width + 8, 0)],
+            "dx": [(width + 8, 0), (width + 8, 0), (width + 8, 0), (width + 9, 0)],
+            "dy": [(width + 8, 2), (width + 8, 1), (width + 8, 2), (width + 8, 2)]}
+
+
+@pytest.mark.parametrize("dtype,pdtype", [(F32, F32), (BF16, F32), (BF16, BF16), (F16, F32), (F16, F16)])
+@pytest.mark.parametrize("width", [1, 40, 256, 300, 700, 1000, 1024])
+def test_norm_tensors_that_lie_differently(width, dtype, pdtype):
+    """Up to 1024 columns element by element: a warp's rows, its sums added to the other warps' in shared memory.  Rows
+    that leave warps, and blocks' last rounds, without work; several rounds."""
+    g = gen(width)
+    w, b = (1 + 0.2 * randn(g, width)).to(pdtype), (0.3 * randn(g, width)).to(pdtype)
+    for rows in (1, 3, 37, 2600):
+        x, dy = randn(g, rows, width).to(dtype), randn(g, rows, width).to(dtype)
+        for places in places_of(width).values():
+            check_norm(x, dy, w, b, places)
+
+
+@pytest.mark.parametrize("dtype,pdtype", [(F32, F32), (BF16, F32), (F16, F16)])
+@pytest.mark.parametrize("width", [1025, 1500, 4097, 8192, 9001, 12289, 16384])
+def test_norm_wide_tensors_that_lie_differently(width, dtype, pdtype):
+    g = gen(width)
+    w, b = (1 + 0.2 * randn(g, width)).to(pdtype), (0.3 * randn(g, width)).to(pdtype)
+    for rows, kinds in ((1, ("all",)), (161, ("all", "dense results", "dx"))):
+        x, dy = randn(g, rows, width).to(dtype), randn(g, rows, width).to(dtype)
+        for kind in kinds:
+            check_norm(x, dy, w, b, places_of(width)[kind])
+
+
+@pytest.mark.parametrize("dtype", [F32, F16])
+@pytest.mark.parametrize("width,stride", [(768, 771), (1025, 1031), (96, 100)])
+def test_layer_norm_of_a_slice(width, stride, dtype):
+    """The differentiable function on part of wider rows: its results and gradients are dense."""
+    g = gen(stride)
+    x, dy = randn(g, 300, width).to(dtype), randn(g, 300, width).to(dtype)
+    w, b = 1 + 0.2 * randn(g, width), 0.3 * randn(g, width)
+    wide = rows_in(x, stride, 0)
+    leaf = [t.detach().requires_grad_() for t in (wide, w, b)]
+    y = rq.layer_norm(*leaf)
+    y.backward(dy)
+    val, tol = ref.norm(x, w, b, 1e-5, dy)
+    for k, got in (("y", y.detach()), ("dx", leaf[0].grad), ("dweight", leaf[1].grad), ("dbias", leaf[2].grad)):
+        ref.check(got, val[k], tol[k], k)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("groups,beams,vocab,select", [(1, 2, 70000, 64), (2, 3, 65536, 48), (1, 1, 140000, 33),
+                                                       (1, 64, 40000, 64), (3, 5, 20000, 64)])
+def test_beam_many_kept_of_long_rows(groups, beams, vocab, select, dtype):
+    """A row over several blocks with more than 32 entries kept: the bar comes from the halves of the lanes."""
+    g = gen(vocab + select)
+    logits = ((randn(g, groups, beams, vocab) * 48).round() / 16).to(dtype)
+    scores = -(randn(g, groups, beams) * 24).round().abs() / 8
+    finished = torch.zeros((groups, beams), dtype=torch.bool, device=DEV)
+    finished[0, -1] = beams > 1
+    for raw in (True, False):
+        for z in (logits, (logits * 0.25).round()):         # the second: many equal totals
+            if not raw and beams > 1:
+                # equal totals of different beams are told apart by rounding that the 64-bit statement does not have:
+                # one beam a group alive
+                scores = torch.where(torch.arange(beams, device=DEV) == beams // 2 - 1, scores, -INF)
+            search = rq.BeamSearch(groups, beams, vocab, select, "raw" if raw else "logits", dtype, vocab - 1)
+            out, parents, codes, done = search.select(z, scores, finished)
+            want = ref_beam(z, scores, finished, vocab - 1, select, raw)
+            assert torch.equal(parents.long(), want[1]) and torch.equal(codes.long(), want[2])
+            size = z.float().abs().max().item() + math.log(vocab)
+            there = torch.isfinite(want[0])
+            ref.check(out, want[0], 0.0 if raw else 16 * ref.U * torch.where(there, want[0].abs() + size, 0.0), "scores")
+            ended = (want[1] < 0) | (want[2] == vocab - 1)
+            assert torch.equal(done, ended | finished.gather(1, want[1].clamp(min=0)))
+
+
+def ref_beam(logits, scores, finished, end_code, select, raw):
+    """predictor_ref.beam's rule by one stable sort a group (its lists take long for millions of candidates)."""
+    groups, beams, vocab = logits.shape
+    x = logits.float() if raw else logits.double()
+    total = scores[:, :, None] + x if raw else scores.double()[:, :, None] + torch.log_softmax(x, 2)
+    only = torch.arange(vocab, device=DEV) == end_code
+    total = torch.where(finished[:, :, None], torch.where(only, scores[:, :, None].to(total.dtype), -INF), total)
+    # equal totals of one beam: in log probabilities the larger logit, which in 64 bits has the larger total
+    value, at = torch.sort(total.reshape(groups, -1), dim=1, descending=True, stable=True)
+    value, at = value[:, :select], at[:, :select]
+    there = value > -INF
+    return torch.where(there, value.double(), -INF), torch.where(there, at // vocab, -1), torch.where(there, at % vocab, -1)
