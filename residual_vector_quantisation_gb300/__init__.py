@@ -199,10 +199,10 @@ def _status(name: str, on: int, stream, *args) -> int:
     given, which has to be one of that GPU's, or with its current one."""
     if stream is None:
         handle = torch._C._cuda_getCurrentRawStream(on)
-    elif stream.device.index == on:
-        handle = stream.cuda_stream
     else:
-        raise ValueError(f"{name}: the stream must be one of cuda:{on}")
+        handle, device = stream.cuda_stream, getattr(stream, "device", None)  # (other libraries' streams need not have one)
+        if device is not None and device.index != on:
+            raise ValueError(f"{name}: the stream must be one of cuda:{on}")
     call = getattr(load_library(), name)
     if torch._C._cuda_getDevice() == on:
         return call(*args, handle)
@@ -227,6 +227,8 @@ def _run_on(stream, device, call, touched):
     stream freed may still be in use there.  touched(): the other tensors that its work uses."""
     if stream is None:
         return call()
+    if hasattr(stream, "cuda_stream") and not isinstance(stream, torch.cuda.Stream):  # another library's
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device)
     with torch.cuda.stream(stream):
         out = call()
     _used_on(stream, *touched())

@@ -520,3 +520,16 @@ def test_states_without_elements():
     assert states[0].row_bytes == 32
     with pytest.raises(ValueError):
         rq.rvq_beam_states([(OnGpu(0, 2, 3, 0, 64), OnGpu(0, 2, 5, 0, 65))])
+
+
+def test_streams_of_other_libraries(gpus, streams, monkeypatch):
+    """An object with nothing but the handle is a stream of the tensors' device."""
+    class Handle:
+        cuda_stream = 77
+
+    call, tensors = quantiser(lambda *shape, dtype=F32: OnGpu(1, *shape, dtype=dtype))["rvq_encode"]
+    call(*tensors, stream=Handle())
+    assert gpus.pop() == ("rvq_encode", 1, 77)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device: f"external {handle} {device}")
+    rq._run_on(Handle(), "cuda:1", lambda: torch.empty(2), lambda: ())
+    assert list(streams.allocated.values()) == ["external 77 cuda:1"]

@@ -389,3 +389,35 @@ def ref_beam(logits, scores, finished, end_code, select, raw):
     value, at = value[:, :select], at[:, :select]
     there = value > -INF
     return torch.where(there, value.double(), -INF), torch.where(there, at // vocab, -1), torch.where(there, at % vocab, -1)
+
+
+def test_quantiser_on_other_streams():
+    """RVQ on torch's streams and on one that only has a handle, with frames that are converted on the way."""
+    import rvq_inputs as ri
+    load = ri.WORKLOAD_BY_NAME["tiny"]
+    w = ri.weights_to_torch(ri.make_weights(load), DEV)
+    rvq = rq.RVQ(w["w_in"], w["codebook"], w["w_out"], device=DEV)
+    x = torch.randn(250, load.D, dtype=torch.float64, device=DEV)
+    want = [t.clone() for t in rvq.reconstruct(x)]
+    side = torch.cuda.Stream()
+
+    class Handle:
+        cuda_stream = side.cuda_stream
+
+    for stream in (side, Handle()):
+        torch.cuda.synchronize()
+        busy()
+        with torch.cuda.stream(side):
+            busy(10)
+        held = x.clone()
+        side.wait_stream(torch.cuda.current_stream())
+        codes = rvq.encode(held, stream=stream)
+        y = rvq.decode(codes, stream=stream)
+        both = rvq.reconstruct(held, stream=stream)
+        del held
+        junk = torch.full_like(x, 9.0)
+        torch.cuda.current_stream().wait_stream(side)
+        for a, b in zip((*want, *want), (codes, y, *both)):
+            assert torch.equal(a, b)
+        del junk
+    torch.cuda.synchronize()
