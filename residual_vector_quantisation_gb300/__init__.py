@@ -173,45 +173,44 @@ def load_library(path: Optional[str] = None):
 # argument marshalling
 # ---------------------------------------------------------------------------
 
-def _ptr(t: Optional[torch.Tensor], on: Optional[int] = None):
-    """Address of a contiguous CUDA tensor (on GPU `on`, where that is given)."""
+def _ptr(t: Optional[torch.Tensor], on: Optional[int] = None) -> Optional[int]:
+    """Address of a contiguous CUDA tensor (on GPU `on`, where that is given; None: null)."""
     if t is None:
         return None
-    if not t.is_cuda:
-        raise ValueError("RVQ buffers must be CUDA tensors")
+    if t.get_device() != on if on is not None else not t.is_cuda:
+        raise ValueError("RVQ buffers must be CUDA tensors, those of one call on one device")
     if not t.is_contiguous():
         raise ValueError("RVQ buffers must be contiguous")
-    if on is not None and t.get_device() != on:
-        raise ValueError(f"RVQ buffers of one call must all be on cuda:{on}")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
-def _device(t: torch.Tensor, name: str) -> int:
-    """The GPU that a call's first tensor is on; the others have to be there too."""
-    on = t.get_device()
-    if on < 0:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    return on
+def _enqueue(name: str, on: int, stream, *args) -> None:
+    """Calls entry point `name` for tensors on GPU `on` (the first one's; the others have been compared with it),
+    whichever device is current: with the stream given, which has to be one of that GPU's, or with its current one."""
+    cuda = torch._C
+    if stream is None and on >= 0 and cuda._cuda_getDevice() == on:  # the usual call
+        status = getattr(load_library(), name)(*args, cuda._cuda_getCurrentRawStream(on))
+    else:
+        status = _status(name, on, stream, *args)
+    if status != RVQ_OK:
+        raise RVQError(name, status)
 
 
 def _status(name: str, on: int, stream, *args) -> int:
-    """What entry point `name` returns for tensors on GPU `on`, whichever device is current: called with the stream
-    given, which has to be one of that GPU's, or with its current one."""
+    """What entry point `name` returns."""
+    if on < 0:
+        raise ValueError(f"{name}: the tensors must be CUDA tensors")
     if stream is None:
         handle = torch._C._cuda_getCurrentRawStream(on)
     else:
-        handle, device = stream.cuda_stream, getattr(stream, "device", None)  # (other libraries' streams need not have one)
-        if device is not None and device.index != on:
+        handle = stream.cuda_stream
+        if getattr(stream, "device_index", on) != on:  # (other libraries' streams need not say)
             raise ValueError(f"{name}: the stream must be one of cuda:{on}")
     call = getattr(load_library(), name)
     if torch._C._cuda_getDevice() == on:
         return call(*args, handle)
     with torch.cuda.device(on):
         return call(*args, handle)
-
-
-def _enqueue(name: str, on: int, stream, *args) -> None:
-    _check(name, _status(name, on, stream, *args))
 
 
 def _used_on(stream, *tensors) -> None:
@@ -263,27 +262,27 @@ def rvq_encode_min_scratch_bytes(dims: rvq_dims, n_q: int) -> int:
 
 def rvq_prepare(dims: rvq_dims, w_in, codebook, w_out, b_in, b_out, tables: torch.Tensor, stream=None,
                 fc_w=None, fc_b=None, fc2_w=None, fc2_b=None) -> None:
-    on = _device(tables, "tables")
+    on = tables.get_device()
     w = rvq_weights(*(_ptr(t, on) for t in (w_in, b_in, codebook, w_out, b_out, fc_w, fc_b, fc2_w, fc2_b)))
     _enqueue("rvq_prepare", on, stream, dims, ctypes.byref(w), _ptr(tables, on), tables.numel() * tables.element_size())
 
 
 def rvq_encode(dims: rvq_dims, tables, x, n_q: int, codes, scratch, stream=None) -> None:
-    on = _device(tables, "tables")
+    on = tables.get_device()
     n = x.shape[0]
     _enqueue("rvq_encode", on, stream, dims, _ptr(tables, on), _ptr(x, on), n, int(n_q), _ptr(codes, on),
              _ptr(scratch, on), scratch.numel() * scratch.element_size())
 
 
 def rvq_decode(dims: rvq_dims, tables, codes, n_q: int, y, bad_codes=None, stream=None) -> None:
-    on = _device(tables, "tables")
+    on = tables.get_device()
     n = codes.shape[0]
     _enqueue("rvq_decode", on, stream, dims, _ptr(tables, on), _ptr(codes, on), n, int(n_q), _ptr(y, on),
              _ptr(bad_codes, on))
 
 
 def rvq_reconstruct(dims: rvq_dims, tables, x, n_q: int, codes, x_hat, scratch, stream=None) -> None:
-    on = _device(tables, "tables")
+    on = tables.get_device()
     n = x.shape[0]
     _enqueue("rvq_reconstruct", on, stream, dims, _ptr(tables, on), _ptr(x, on), n, int(n_q), _ptr(codes, on),
              _ptr(x_hat, on), _ptr(scratch, on), scratch.numel() * scratch.element_size())
@@ -291,7 +290,7 @@ def rvq_reconstruct(dims: rvq_dims, tables, x, n_q: int, codes, x_hat, scratch, 
 
 def rvq_encode_static(dims: rvq_dims, tables, x, n_q: int, codes, stream=None) -> None:
     """Encode with the library's own fixed scratch (no scratch argument; see rvq.h)."""
-    on = _device(tables, "tables")
+    on = tables.get_device()
     n = x.shape[0]
     _enqueue("rvq_encode_static", on, stream, dims, _ptr(tables, on), _ptr(x, on), n, int(n_q), _ptr(codes, on))
 
@@ -329,14 +328,14 @@ def rvq_read_status(scratch: Optional[torch.Tensor] = None, stream=None) -> int:
     """Synchronise `stream` and return the status (an rvq_status value, not
     raised) that the encode last enqueued with `scratch` left in its status
     word; scratch=None reads the library's own scratch (rvq_encode_static)."""
-    on = torch.cuda.current_device() if scratch is None else _device(scratch, "scratch")
+    on = torch.cuda.current_device() if scratch is None else scratch.get_device()
     return int(_status("rvq_read_status", on, stream, _ptr(scratch, on)))
 
 
 def rvq_read_error_count(bad_codes: torch.Tensor, stream=None) -> int:
     """Synchronise `stream` and return rvq_decode's bad-code counter."""
     out = ctypes.c_int64(0)
-    on = _device(bad_codes, "bad_codes")
+    on = bad_codes.get_device()
     _enqueue("rvq_read_error_count", on, stream, _ptr(bad_codes, on), ctypes.byref(out))
     return int(out.value)
 
@@ -412,7 +411,7 @@ def rvq_layer_norm_workspace_bytes(rows: int, width: int) -> int:
 
 def rvq_layer_norm(x, weight, bias, eps: float, y, mean=None, rstd=None, stream=None) -> None:
     """Layer norm of the rows of x [rows][width] into y (see rvq.h); mean and rstd [rows] are optional outputs."""
-    on = _device(x, "x")
+    on = x.get_device()
     shape, dtype = _shape2(x, "x"), x.dtype
     rows, width = shape
     p = weight if weight is not None else bias
@@ -426,7 +425,7 @@ def rvq_layer_norm(x, weight, bias, eps: float, y, mean=None, rstd=None, stream=
 
 def rvq_layer_norm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, workspace, stream=None) -> None:
     """Gradients of rvq_layer_norm; dx, dweight and dbias may each be None (not computed)."""
-    on = _device(x, "x")
+    on = x.get_device()
     shape, dtype = _shape2(x, "x"), x.dtype
     rows, width = shape
     p = weight if weight is not None else dweight if dweight is not None else dbias
@@ -443,7 +442,7 @@ def rvq_layer_norm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, works
 
 
 def _distill_args(logits, top_logits, top_codes, teacher_lse, weights, temperature):
-    on = _device(logits, "logits")
+    on = logits.get_device()
     rows, vocab = shape = _shape2(logits, "logits")
     entries = _shape2(top_logits, "top_logits")
     if entries[0] != rows:
@@ -485,7 +484,7 @@ def rvq_beam_select(dims: rvq_beam_dims, logits, scores, finished, end_code: int
     """One selection step (see rvq.h): logits [groups][beams][vocab] (or [groups * beams][vocab]), scores and finished
     [groups][beams]; outputs [groups][select].  finished, out_finished: bool or uint8 tensors, or None."""
     groups, beams, vocab = dims.groups, dims.beams, dims.vocab
-    on = _device(logits, "logits")
+    on = logits.get_device()
     if DTYPES.get(logits.dtype) != dims.dtype:
         raise ValueError("logits must have the dtype in dims")
     if logits.dim() == 3:
@@ -540,7 +539,10 @@ def rvq_beam_states(pairs, layered: bool = False):
         s.dst_group_stride, s.dst_beam_stride = b[-2:]
     out.shapes = [(src.shape[lead - 2:lead], dst.shape[lead - 2:lead]) for src, dst in pairs]
     out.tensors = pairs
-    out.devices = {t.get_device() for pair in pairs for t in pair}
+    on = {t.get_device() for pair in pairs for t in pair}
+    if len(on) > 1:
+        raise ValueError("states must all be on one device")
+    out.device = on.pop() if on else None
     return out
 
 
@@ -550,8 +552,8 @@ def rvq_beam_reorder(dims: rvq_beam_dims, parents, states, stream=None) -> None:
     for shapes in states.shapes:
         if shapes != want:
             raise ValueError(f"states must have {want[0]} and {want[1]} groups and beams")
-    on = _device(parents, "parents")
-    if not states.devices <= {on}:
+    on = parents.get_device()
+    if states.device != on and states.device is not None:
         raise ValueError(f"states must be on cuda:{on}, with their parents")
     _enqueue("rvq_beam_reorder", on, stream, dims, _at(parents, on, torch.int32, want[1], "parents"), states, len(states))
 

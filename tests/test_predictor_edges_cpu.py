@@ -69,7 +69,7 @@ class OnGpu:
 
 class Stream:
     def __init__(self, index, handle):
-        self.device, self.cuda_stream = torch.device("cuda", index), handle
+        self.device_index, self.cuda_stream = index, handle
 
 
 @pytest.fixture
