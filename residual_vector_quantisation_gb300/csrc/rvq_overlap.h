@@ -82,15 +82,41 @@ class ReachSearch {
   }
 };
 
-// Whether two rows of one set overlap.
+// Whether two rows of one set overlap.  (Usual sets, each axis longer than all
+// within it, need no search; nor, below, do sets with nothing between their
+// first and last bytes in common.)
 inline Overlap overlaps_itself(const RowSet &s) {
+  ReachSearch::Wide extent = s.row;
+  bool nested = true;
+  for (int i = 3; i-- > 0;) {
+    if (s.axis[i].count == 1) continue;
+    nested = nested && s.axis[i].stride >= extent;
+    extent += (ReachSearch::Wide)(s.axis[i].count - 1) * s.axis[i].stride;
+  }
+  if (nested) return Overlap::kNone;
   ReachSearch r;
   for (const auto &x : s.axis) r.add(-(x.count - 1), x.count - 1, x.stride);
   return r.find(0, s.row, s.row, true);
 }
 
+// The first byte of a set and the one after its last.
+struct Span {
+  ReachSearch::Wide first, end;
+};
+inline Span span(const RowSet &s) {
+  const ReachSearch::Wide at = reinterpret_cast<uintptr_t>(s.base);
+  Span r = {at, at + s.row};
+  for (const auto &x : s.axis) {
+    const ReachSearch::Wide reach = (ReachSearch::Wide)(x.count - 1) * x.stride;
+    (reach < 0 ? r.first : r.end) += reach;
+  }
+  return r;
+}
+
 // Whether a row of s and one of t overlap.
 inline Overlap overlap(const RowSet &s, const RowSet &t) {
+  const Span a = span(s), b = span(t);
+  if (a.end <= b.first || b.end <= a.first) return Overlap::kNone;
   ReachSearch r;
   for (int i = 0; i < 3; ++i) {
     const auto &x = s.axis[i], &y = t.axis[i];
