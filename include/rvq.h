@@ -410,7 +410,11 @@ typedef struct rvq_distill_dims {
  *     q_j = exp(t_j / T - teacher_lse), and the codes without an entry are one
  *     more outcome with q_r = 1 - sum_j q_j and p_r = their sum of p:
  *     loss = w * (sum_j q_j (log q_j - log p[i_j]) + q_r (log q_r - log p_r)).
- *     q_r below 2^-20 (the rounding of the sum) counts as zero.
+ *     q_r below 2^-20 (the rounding of the sum) counts as zero.  (q_r also
+ *     carries the rounding of teacher_lse, |teacher_lse| * 2^-24: past 16 that
+ *     alone may exceed 2^-20, and where p_r is zero the loss is then infinite.
+ *     Shift the teacher's logits by their largest, which changes no q, before
+ *     both are made where the list is all that has a share.)
  * weights ([rows], nullable: ones) gives w.  A row with w = 0 has loss 0 and
  * gradient 0 whatever its logits hold.
  * An entry with code -1 is empty.  Other codes outside [0, vocab), and a code
@@ -419,8 +423,10 @@ typedef struct rvq_distill_dims {
  * atomically, as in rvq_decode).  A row without entries has loss 0 and
  * gradient 0, and so has, without teacher_lse, one whose entries are all -inf.
  * Terms with q = 0 are zero even where p is zero; q > 0 where p = 0 gives an
- * infinite loss and a finite gradient.  A NaN or +inf in a row with w != 0
- * makes that row's results NaN, and no other's.
+ * infinite loss and a finite gradient.  A NaN, or a logit of +inf, in a row
+ * with w != 0 makes that row's results NaN, and no other's; so does a teacher's
+ * +inf without teacher_lse (with it, the loss and that entry's gradient are
+ * infinite).
  * Writes loss [rows]; if not NULL, lse [rows][2] for rvq_distill_backward (the
  * largest logit m and the sum of exp((logit - m) / T) over all codes, or, with
  * teacher_lse, over the codes without an entry; zeros where w = 0); if not

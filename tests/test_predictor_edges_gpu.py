@@ -421,3 +421,42 @@ def test_quantiser_on_other_streams():
             assert torch.equal(a, b)
         del junk
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("vocab", [200, 3000, 20000])
+def test_distill_infinite_teacher(vocab, tail):
+    g = gen(vocab + 1)
+    z = randn(g, 3, vocab)
+    t, codes = torch.topk(z + randn(g, 3, vocab), 6, dim=1)
+    lse = torch.logsumexp(t, 1) + 0.5 if tail else None
+    t[1, 2] = INF
+    codes = codes.to(torch.int32)
+    loss, d = torch.empty(3, device=DEV), torch.empty_like(z)
+    rq.rvq_distill(z, t, codes, lse, None, 1.0, loss, dlogits=d)
+    assert bool(torch.isfinite(loss[::2]).all()) and bool(torch.isfinite(d[::2]).all())
+    if tail:
+        assert loss[1].item() == INF and d[1, codes[1, 2].item()].item() == -INF
+        assert int(torch.isfinite(d[1]).sum()) == vocab - 1
+    else:
+        assert bool(torch.isnan(loss[1])) and bool(torch.isnan(d[1]).all())
+
+
+@pytest.mark.parametrize("vocab", [200, 3000, 20000])
+def test_distill_list_with_everything(vocab):
+    """A teacher and a mask that leave nothing off the list: with the teacher's logits shifted by their largest, as the
+    header says, the tail has no share and the loss is finite."""
+    g = gen(vocab + 2)
+    z = randn(g, 40, vocab)
+    t, codes = torch.topk(z + 60 + 8 * randn(g, 40, vocab), 40, dim=1)
+    keep = torch.zeros_like(z, dtype=torch.bool).scatter_(1, codes, True)
+    z[~keep] = -INF
+    t = t - t[:, :1]
+    lse = torch.logsumexp(t.double(), 1).float()
+    codes = codes.to(torch.int32)
+    loss, d = torch.empty(40, device=DEV), torch.empty_like(z)
+    rq.rvq_distill(z, t, codes, lse, None, 1.0, loss, dlogits=d)
+    val, tol, _ = ref.distill(z, t, codes, lse, None, 1.0)
+    assert bool(torch.isfinite(val["loss"]).all())
+    ref.check(loss, val["loss"], tol["loss"], "loss")
+    ref.check(d, val["dlogits"], tol["dlogits"], "dlogits")
