@@ -427,7 +427,7 @@ __device__ __forceinline__ void skip_row(const DistillArgs &a, int64_t row, cons
 // compiler would have it (78 registers, 6 blocks an SM), 100 at 7 and 95 at 8
 // blocks; for 384 000 rows of 1024 f32 (two passes) 892 us at 5, 819 at 6, 848
 // at 7, 910 at 8 blocks (90 and 814 us since then, with one logarithm fewer a
-// row).  The bytes alone would take 58 and 702 us.  Blocks of
+// row).  The bytes alone would take 59 and 704 us.  Blocks of
 // more than 512 threads, for rows above 16384, were slower than two reads (89
 // against 73 us for 2000 rows of 30 000 bf16).
 constexpr int kRowWarps = 4, kMaxWarps = 16;
@@ -523,8 +523,8 @@ __global__ void __launch_bounds__(WARP ? 32 * kRowWarps : 32 * kMaxWarps, WARP ?
 }
 
 // Longer rows: a row per block, read twice (the second time mostly from the
-// L2), U vectors of a thread at a time.  4096 rows of 65536 bf16 take 247 us
-// where the bytes alone would take 155: 304 rows are in flight, a third of the
+// L2), U vectors of a thread at a time.  4096 rows of 65536 bf16 take 246 us
+// where the bytes alone would take 156: 304 rows are in flight, a third of the
 // second reads misses the L2, and fewer rows in flight leave the SMs waiting at
 // the rows' ends (one block of 1024 threads an SM: 347 us).
 constexpr int kLongThreads = 512;
