@@ -522,6 +522,44 @@ typedef struct rvq_beam_state {
 RVQ_API rvq_status rvq_beam_reorder(rvq_beam_dims dims, const int32_t *parents, const rvq_beam_state *states,
                                     int32_t n_states, rvq_stream_t stream);
 
+/* What of each element stays in a dropout: element e (row * width + column of
+ * the call's rows) is dropped where its 16 bits of Philox4x32 with ten rounds
+ * (Salmon et al., 2011) are below round(p * 2^16): bits 16 * (e % 8) and up of
+ * the 128 that the counter (e / 8 in its lower 64 bits, offset + 2^32 * *step in
+ * its upper ones) gives under the key seed.  What stays is multiplied by
+ * 2^16 / (2^16 - round(p * 2^16)), which keeps the mean also where p is no
+ * multiple of 2^-16.  The mask depends on nothing else: not on dtype, strides or
+ * how the call is carried out, so the backward pass, or any other call, makes the
+ * same one again.
+ *   0 <= p <= 1 (1: everything is dropped).
+ *   seed: one of a run.  offset: one of each place in the model (below 2^32 they
+ *   never meet).  step: device memory (8-byte aligned; NULL: 0), read when the
+ *   call runs, so that a graph that is replayed gets a new mask where the graph
+ *   itself, or what runs between, counts it up. */
+typedef struct rvq_dropout_mask {
+  float p;
+  uint64_t seed;
+  uint64_t offset;
+  const int64_t *step;
+} rvq_dropout_mask;
+
+/* Rows of a dropout (rows and width 0 are valid; rows * width up to 2^48). */
+typedef struct rvq_dropout_dims {
+  int64_t rows;
+  int64_t width;
+  int32_t dtype;
+} rvq_dropout_dims;
+
+/* y = residual + (x where it stays, times the factor; 0 where it is dropped,
+ * whatever x holds there).  residual is nullable (0).  The factor's product and
+ * the sum are rounded to float32 each, y once more to its type.  The gradient of
+ * x is the same call on dy without a residual (that of the residual is dy).  y
+ * may be x or residual (same stride); other overlaps are refused
+ * (RVQ_ERR_INVALID_ARG). */
+RVQ_API rvq_status rvq_dropout(rvq_dropout_dims dims, const void *x, int64_t x_stride, const void *residual,
+                               int64_t residual_stride, const rvq_dropout_mask *mask, void *y, int64_t y_stride,
+                               rvq_stream_t stream);
+
 /* Static strings. */
 RVQ_API const char *rvq_status_string(rvq_status status);
 RVQ_API const char *rvq_version(void);

@@ -36,6 +36,7 @@ __all__ = [
     "rvq_distill_dims", "rvq_distill", "rvq_distill_backward", "rvq_beam_dims", "rvq_beam_workspace_bytes",
     "rvq_beam_select", "rvq_beam_state", "rvq_beam_states", "rvq_beam_reorder", "RVQ_BEAM_LOGITS", "RVQ_BEAM_RAW",
     "RVQ_BEAM_MAX_STATES", "DTYPES", "layer_norm", "distill_loss", "distill_loss_and_grad", "BeamSearch",
+    "rvq_dropout_mask", "rvq_dropout_dims", "rvq_dropout", "dropout",
 ]
 
 RVQ_OK = 0
@@ -54,6 +55,7 @@ EXPORTED_SYMBOLS = [
     "rvq_stream_plan", "rvq_read_status", "rvq_read_error_count", "rvq_pipeline_set_cancel",
     "rvq_layer_norm", "rvq_layer_norm_workspace_bytes", "rvq_layer_norm_backward", "rvq_distill",
     "rvq_distill_backward", "rvq_beam_workspace_bytes", "rvq_beam_select", "rvq_beam_reorder",
+    "rvq_dropout",
 ]
 
 # int (*rvq_cancel_fn)(void *user)
@@ -96,6 +98,25 @@ class rvq_norm_dims(ctypes.Structure):
 class rvq_distill_dims(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int64), ("vocab", ctypes.c_int32), ("top", ctypes.c_int32),
                 ("dtype", ctypes.c_int32), ("top_dtype", ctypes.c_int32), ("temperature", ctypes.c_float)]
+
+
+class rvq_dropout_mask(ctypes.Structure):
+    """What stays in a dropout (see rvq.h): p, seed, offset, and step: None, or a tensor of one int64 on the GPU, which
+    the mask keeps alive."""
+
+    _fields_ = [("p", ctypes.c_float), ("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64), ("step", ctypes.c_void_p)]
+
+    def __init__(self, p: float, seed: int, offset: int = 0, step: Optional[torch.Tensor] = None):
+        if not (0 <= seed < 1 << 64 and 0 <= offset < 1 << 64):
+            raise ValueError("seed and offset must be numbers of 64 bits, not negative")
+        if step is not None and not (step.is_cuda and step.dtype is torch.int64 and step.numel() == 1):
+            raise ValueError("step must be one int64 on the GPU")
+        super().__init__(p, seed, offset, None if step is None else step.data_ptr())
+        self.tensor = step
+
+
+class rvq_dropout_dims(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("width", ctypes.c_int64), ("dtype", ctypes.c_int32)]
 
 
 class rvq_beam_dims(ctypes.Structure):
@@ -156,6 +177,8 @@ def load_library(path: Optional[str] = None):
                                     ctypes.c_int),
         "rvq_distill": ([rvq_distill_dims, vp, i64, vp, vp, vp, vp, vp, vp, vp, i64, vp, vp], ctypes.c_int),
         "rvq_distill_backward": ([rvq_distill_dims, vp, vp, i64, vp, vp, vp, vp, vp, vp, i64, vp], ctypes.c_int),
+        "rvq_dropout": ([rvq_dropout_dims, vp, i64, vp, i64, ctypes.POINTER(rvq_dropout_mask), vp, i64, vp],
+                        ctypes.c_int),
         "rvq_beam_workspace_bytes": ([rvq_beam_dims], sz),
         "rvq_beam_select": ([rvq_beam_dims, vp, i64, vp, vp, i32, vp, vp, vp, vp, vp, sz, vp], ctypes.c_int),
         "rvq_beam_reorder": ([rvq_beam_dims, vp, ctypes.POINTER(rvq_beam_state), i32, vp], ctypes.c_int),
@@ -368,7 +391,7 @@ def rvq_stream_plan(dims: rvq_dims, n_q: int, n_frames: int) -> dict:
 
 
 # ---------------------------------------------------------------------------
-# operators of a code predictor (layer norm, distillation loss, beam step)
+# operators of a code predictor (norms, dropout, log probabilities, distillation loss, beam step)
 # ---------------------------------------------------------------------------
 
 def _at(t: Optional[torch.Tensor], on: int, dtype, shape, name: str):
@@ -439,6 +462,28 @@ def rvq_layer_norm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, works
              dyp, dys, xp, xs, _at(weight, on, pd, (width,), "weight"), _at(mean, on, torch.float32, (rows,), "mean"),
              _at(rstd, on, torch.float32, (rows,), "rstd"), dxp, dxs, _at(dweight, on, pd, (width,), "dweight"),
              _at(dbias, on, pd, (width,), "dbias"), *_workspace(workspace, on))
+
+
+def _rows_or_none(t: Optional[torch.Tensor], on: int, dtype, shape, name: str):
+    return (None, 0) if t is None else _rows_at(t, on, dtype, shape, name)
+
+
+def _mask_on(mask: Optional[rvq_dropout_mask], on: int):
+    """A pointer to the mask, whose step has to be on GPU `on` (None: null)."""
+    if mask is None:
+        return None
+    if mask.tensor is not None and mask.tensor.get_device() != on:
+        raise ValueError(f"the mask's step must be on cuda:{on}")
+    return ctypes.byref(mask)
+
+
+def rvq_dropout(x, mask: rvq_dropout_mask, y, residual=None, stream=None) -> None:
+    """Dropout of x [rows][width] into y, plus residual (see rvq.h); on the gradient of y, its backward pass."""
+    on = x.get_device()
+    shape, dtype = _shape2(x, "x"), x.dtype
+    _enqueue("rvq_dropout", on, stream, rvq_dropout_dims(*shape, DTYPES[dtype]), *_rows_at(x, on, dtype, shape, "x"),
+             *_rows_or_none(residual, on, dtype, shape, "residual"), _mask_on(mask, on),
+             *_rows_at(y, on, dtype, shape, "y"))
 
 
 def _distill_args(logits, top_logits, top_codes, teacher_lse, weights, temperature):
@@ -694,4 +739,4 @@ class RVQPipeline:
             pass
 
 
-from .predictor import BeamSearch, distill_loss, distill_loss_and_grad, layer_norm  # noqa: E402
+from .predictor import BeamSearch, distill_loss, distill_loss_and_grad, dropout, layer_norm  # noqa: E402

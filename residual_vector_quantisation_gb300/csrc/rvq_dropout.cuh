@@ -1,0 +1,68 @@
+// The dropout mask (rvq_dropout_mask): a function of an element's index, the
+// seed and the call, computed where it is needed and never stored.
+//
+// Eight elements share one call of Philox4x32 with ten rounds (Salmon, Moraes,
+// Dror, Shaw: Parallel random numbers: as easy as 1, 2, 3; 2011): counter
+// (e / 8, offset + 2^32 * step), key seed; 16 of its 128 bits each.  An element
+// is dropped where its 16 bits are below round(p * 2^16), so that the factor
+// 2^16 / (2^16 - that) is exact to the probability that is used.  16 bits and not
+// 32: ten rounds are 20 wide products, and at 8 elements a call that is 2.5 an
+// element.
+#pragma once
+
+#include "rvq_rows.cuh"
+
+namespace rvq {
+
+struct DropoutMask {
+  uint64_t seed, offset;
+  const int64_t *step;  // null: 0
+  uint32_t drop;        // of 2^16
+  float factor;         // of what stays (0 where nothing does)
+};
+
+// What a call's mask becomes; false: not valid.
+inline bool dropout_mask(const rvq_dropout_mask &m, DropoutMask &out) {
+  if (!(m.p >= 0.f && m.p <= 1.f) || !aligned_to(m.step, 8)) return false;
+  const uint32_t drop = (uint32_t)((double)m.p * 65536.0 + 0.5);
+  out = {m.seed, m.offset, m.step, drop, drop < 65536 ? (float)(65536.0 / (65536 - drop)) : 0.f};
+  return true;
+}
+
+// The mask of one launch, its call's counter read.
+struct Keep {
+  uint32_t k0, k1, u0, u1, drop;
+  float factor;
+  __device__ __forceinline__ explicit Keep(const DropoutMask &m)
+      : k0((uint32_t)m.seed), k1((uint32_t)(m.seed >> 32)), drop(m.drop), factor(m.factor) {
+    const uint64_t upper = m.offset + (m.step ? (uint64_t)*m.step << 32 : 0);
+    u0 = (uint32_t)upper, u1 = (uint32_t)(upper >> 32);
+  }
+  // Bit i: whether element 8 * group + i stays.
+  __device__ __forceinline__ uint32_t group(uint64_t g) const {
+    uint32_t a = (uint32_t)g, b = (uint32_t)(g >> 32), c = u0, d = u1, x = k0, y = k1;
+#pragma unroll
+    for (int i = 0; i < 10; ++i) {
+      const uint64_t p = (uint64_t)a * 0xD2511F53u, q = (uint64_t)c * 0xCD9E8D57u;
+      a = (uint32_t)(q >> 32) ^ b ^ x, b = (uint32_t)q;
+      c = (uint32_t)(p >> 32) ^ d ^ y, d = (uint32_t)p;
+      x += 0x9E3779B9u, y += 0xBB67AE85u;
+    }
+    const uint32_t w[4] = {a, b, c, d};
+    uint32_t bits = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      bits |= (uint32_t)((w[i] & 0xffffu) >= drop) << (2 * i) | (uint32_t)((w[i] >> 16) >= drop) << (2 * i + 1);
+    return bits;
+  }
+  // Bit i (i < N <= 8): whether element e + i stays (the bits above mean nothing).
+  template <int N>
+  __device__ __forceinline__ uint32_t from(uint64_t e) const {
+    const int at = (int)(e & 7);
+    uint32_t bits = group(e >> 3) >> at;
+    if (at + N > 8) bits |= group((e >> 3) + 1) << (8 - at);
+    return bits;
+  }
+};
+
+}  // namespace rvq

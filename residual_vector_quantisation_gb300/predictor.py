@@ -1,5 +1,6 @@
-"""Operators of a code predictor over torch tensors: differentiable layer norm
-and distillation loss, and a beam search over a quantiser's codes.
+"""Operators of a code predictor over torch tensors: differentiable norms,
+dropout, log probabilities and distillation loss, and a beam search over a
+quantiser's codes.
 
 They sit on the C ABI of include/rvq.h (the rvq_* functions of the package) and
 own what those leave to the caller: outputs, statistics and workspaces.
@@ -60,6 +61,47 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
         if p is not None and not p.is_contiguous():
             raise ValueError("weight and bias must be contiguous")
     return _LayerNorm.apply(x, weight, bias, eps)
+
+
+def _beside(x: torch.Tensor, residual: Optional[torch.Tensor]):
+    """x and residual as rows."""
+    if residual is not None and (residual.shape != x.shape or residual.dtype != x.dtype):
+        raise ValueError("residual must have x's shape and dtype")
+    return _as_rows(x), None if residual is None else _as_rows(residual)
+
+
+class _Dropout(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, residual, mask, step):
+        rows, add = _beside(x, residual)
+        y = torch.empty(rows.shape, dtype=x.dtype, device=x.device)
+        _rq.rvq_dropout(rows, mask, y, add)
+        ctx.save_for_backward(step)  # counted up before the backward pass, it would give another mask
+        ctx.mask = mask
+        return y.view(x.shape)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        ctx.saved_tensors  # raises where the step has been counted up
+        dx = None
+        if ctx.needs_input_grad[0]:
+            rows = _as_rows(dy)
+            dx = torch.empty(rows.shape, dtype=rows.dtype, device=rows.device)
+            _rq.rvq_dropout(rows, ctx.mask, dx)
+            dx = dx.view(dy.shape)
+        return dx, dy if ctx.needs_input_grad[1] else None, None, None
+
+
+def dropout(x: torch.Tensor, mask: _rq.rvq_dropout_mask, residual: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """x where the mask has it stay, times the factor that keeps its mean, and 0 elsewhere; plus residual.
+    Differentiable in x and residual (x's shape and dtype).  The mask is made anew in the backward pass and never
+    stored: mask = rvq_dropout_mask(p, seed, offset, step) says which one, element by element of x in its order
+    (whatever its strides).  A step on the GPU has to be counted up after the backward pass.  Runs on the current
+    stream."""
+    if x.numel() == 0:
+        return x.clone() if residual is None else x + residual
+    return _Dropout.apply(x, residual, mask, None if mask is None else mask.tensor)
 
 
 def _teacher(logits, top_logits, top_codes, teacher_lse, weights):
