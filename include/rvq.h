@@ -560,6 +560,59 @@ RVQ_API rvq_status rvq_dropout(rvq_dropout_dims dims, const void *x, int64_t x_s
                                int64_t residual_stride, const rvq_dropout_mask *mask, void *y, int64_t y_stride,
                                rvq_stream_t stream);
 
+/* An output in 8 bits (e4m3) beside, or in place of, rvq_rms_norm's y: values
+ * [rows] rows of width bytes, `stride` bytes apart; scales [rows][n], contiguous,
+ * one for each `block` neighbouring columns (32, 64 or 128; n = ceil(width /
+ * block)) or, block 0, one a row.  A value stands for itself times its scale:
+ *   scale = max(largest magnitude of the block's y / 448, 2^-126),
+ * of scale_type RVQ_SCALE_F32, or, RVQ_SCALE_E8M0, rounded up to a power of two
+ * and held as its biased exponent (a byte); value = y / scale, rounded to nearest
+ * (y before its own rounding; the division is a product with the inverse).  A
+ * NaN in a block makes its scale and all its values NaN. */
+#define RVQ_SCALE_F32 0
+#define RVQ_SCALE_E8M0 1
+typedef struct rvq_rms_8bit {
+  void *values;
+  int64_t stride;
+  void *scales;
+  int32_t block;
+  int32_t scale_type;
+} rvq_rms_8bit;
+
+/* Root-mean-square norm (dims as for rvq_layer_norm):
+ *   h = residual + drop(x), rounded to dtype;  rstd = 1 / sqrt(mean(h^2) + eps);
+ *   y = h * rstd * weight.
+ * residual, mask (nothing is dropped) and weight (one) are nullable, and so are
+ * the outputs: total (h, where there is a residual or a mask: else h is x and
+ * total has to be NULL), y, rstd ([rows], kept for the backward pass) and q (the
+ * output in 8 bits); one of total, y and q is needed.  The mask is that of the
+ * call's rows of `width`.  total and y may each be x or residual (same stride);
+ * what is written may lie over nothing else (RVQ_ERR_INVALID_ARG).  (mean(h^2) is
+ * a float32: of a row past 1.8e19 it is infinite and y is zero.) */
+RVQ_API rvq_status rvq_rms_norm(rvq_norm_dims dims, const void *x, int64_t x_stride, const void *residual,
+                                int64_t residual_stride, const rvq_dropout_mask *mask, const void *weight, void *total,
+                                int64_t total_stride, void *y, int64_t y_stride, float *rstd, const rvq_rms_8bit *q,
+                                rvq_stream_t stream);
+
+/* Workspace bytes of rvq_rms_norm_backward (0 for unsupported arguments). */
+RVQ_API size_t rvq_rms_norm_workspace_bytes(int64_t rows, int32_t width);
+
+/* Gradients of rvq_rms_norm, from total (h; x where there was neither residual
+ * nor mask), its mask and its rstd: with u = h * rstd and g = dy * weight,
+ *   dh = rstd * (g - u * mean(g * u)) + dtotal,  dresidual = dh,  dx = drop(dh),
+ *   dweight = sum over rows of dy * u.
+ * dtotal (nullable: 0) is the gradient that reaches h from elsewhere.  dresidual,
+ * dx and dweight are each nullable (not computed); dx needs the mask (without one
+ * it is dresidual).  dresidual and dx may each be dy, dtotal or total (same
+ * stride); what is written may lie over nothing else.  With zero rows dweight is
+ * set to zero.  The workspace (16-byte aligned) is needed for dweight; its
+ * contents mean nothing before and after the call. */
+RVQ_API rvq_status rvq_rms_norm_backward(rvq_norm_dims dims, const void *dy, int64_t dy_stride, const void *dtotal,
+                                         int64_t dtotal_stride, const void *total, int64_t total_stride,
+                                         const rvq_dropout_mask *mask, const void *weight, const float *rstd,
+                                         void *dresidual, int64_t dresidual_stride, void *dx, int64_t dx_stride,
+                                         void *dweight, void *workspace, size_t workspace_bytes, rvq_stream_t stream);
+
 /* Static strings. */
 RVQ_API const char *rvq_status_string(rvq_status status);
 RVQ_API const char *rvq_version(void);

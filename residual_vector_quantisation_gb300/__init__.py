@@ -36,7 +36,9 @@ __all__ = [
     "rvq_distill_dims", "rvq_distill", "rvq_distill_backward", "rvq_beam_dims", "rvq_beam_workspace_bytes",
     "rvq_beam_select", "rvq_beam_state", "rvq_beam_states", "rvq_beam_reorder", "RVQ_BEAM_LOGITS", "RVQ_BEAM_RAW",
     "RVQ_BEAM_MAX_STATES", "DTYPES", "layer_norm", "distill_loss", "distill_loss_and_grad", "BeamSearch",
-    "rvq_dropout_mask", "rvq_dropout_dims", "rvq_dropout", "dropout",
+    "rvq_dropout_mask", "rvq_dropout_dims", "rvq_dropout", "dropout", "rvq_rms_8bit", "rvq_rms_norm",
+    "rvq_rms_norm_workspace_bytes", "rvq_rms_norm_backward", "RVQ_SCALE_F32", "RVQ_SCALE_E8M0", "rms_norm",
+    "rms_norm_8bit",
 ]
 
 RVQ_OK = 0
@@ -55,7 +57,7 @@ EXPORTED_SYMBOLS = [
     "rvq_stream_plan", "rvq_read_status", "rvq_read_error_count", "rvq_pipeline_set_cancel",
     "rvq_layer_norm", "rvq_layer_norm_workspace_bytes", "rvq_layer_norm_backward", "rvq_distill",
     "rvq_distill_backward", "rvq_beam_workspace_bytes", "rvq_beam_select", "rvq_beam_reorder",
-    "rvq_dropout",
+    "rvq_dropout", "rvq_rms_norm", "rvq_rms_norm_workspace_bytes", "rvq_rms_norm_backward",
 ]
 
 # int (*rvq_cancel_fn)(void *user)
@@ -77,6 +79,9 @@ DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}  # RVQ_DTYPE_*
 RVQ_BEAM_LOGITS = 0
 RVQ_BEAM_RAW = 1
 RVQ_BEAM_MAX_STATES = 32
+RVQ_SCALE_F32 = 0
+RVQ_SCALE_E8M0 = 1
+SCALES = {torch.float32: RVQ_SCALE_F32, torch.float8_e8m0fnu: RVQ_SCALE_E8M0}
 
 
 class rvq_dims(ctypes.Structure):
@@ -117,6 +122,11 @@ class rvq_dropout_mask(ctypes.Structure):
 
 class rvq_dropout_dims(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int64), ("width", ctypes.c_int64), ("dtype", ctypes.c_int32)]
+
+
+class rvq_rms_8bit(ctypes.Structure):
+    _fields_ = [("values", ctypes.c_void_p), ("stride", ctypes.c_int64), ("scales", ctypes.c_void_p),
+                ("block", ctypes.c_int32), ("scale_type", ctypes.c_int32)]
 
 
 class rvq_beam_dims(ctypes.Structure):
@@ -179,6 +189,11 @@ def load_library(path: Optional[str] = None):
         "rvq_distill_backward": ([rvq_distill_dims, vp, vp, i64, vp, vp, vp, vp, vp, vp, i64, vp], ctypes.c_int),
         "rvq_dropout": ([rvq_dropout_dims, vp, i64, vp, i64, ctypes.POINTER(rvq_dropout_mask), vp, i64, vp],
                         ctypes.c_int),
+        "rvq_rms_norm": ([rvq_norm_dims, vp, i64, vp, i64, ctypes.POINTER(rvq_dropout_mask), vp, vp, i64, vp, i64, vp,
+                          ctypes.POINTER(rvq_rms_8bit), vp], ctypes.c_int),
+        "rvq_rms_norm_workspace_bytes": ([i64, i32], sz),
+        "rvq_rms_norm_backward": ([rvq_norm_dims, vp, i64, vp, i64, vp, i64, ctypes.POINTER(rvq_dropout_mask), vp, vp,
+                                   vp, i64, vp, i64, vp, vp, sz, vp], ctypes.c_int),
         "rvq_beam_workspace_bytes": ([rvq_beam_dims], sz),
         "rvq_beam_select": ([rvq_beam_dims, vp, i64, vp, vp, i32, vp, vp, vp, vp, vp, sz, vp], ctypes.c_int),
         "rvq_beam_reorder": ([rvq_beam_dims, vp, ctypes.POINTER(rvq_beam_state), i32, vp], ctypes.c_int),
@@ -486,6 +501,54 @@ def rvq_dropout(x, mask: rvq_dropout_mask, y, residual=None, stream=None) -> Non
              *_rows_at(y, on, dtype, shape, "y"))
 
 
+def rvq_rms_norm_workspace_bytes(rows: int, width: int) -> int:
+    return load_library().rvq_rms_norm_workspace_bytes(int(rows), int(width))
+
+
+def rvq_rms_norm(x, weight, eps: float, y, rstd=None, residual=None, mask: Optional[rvq_dropout_mask] = None,
+                 total=None, q=None, scales=None, block: int = 0, stream=None) -> None:
+    """Root-mean-square norm of the rows of residual + drop(x) [rows][width] into y (see rvq.h).  Optional outputs:
+    rstd [rows], total (the sum), q (float8_e4m3fn) with scales [rows][ceil(width / block)] (block 0: [rows][1];
+    float32, or float8_e8m0fnu for powers of two); y may be None."""
+    on = x.get_device()
+    shape, dtype = _shape2(x, "x"), x.dtype
+    rows, width = shape
+    pd = torch.float32 if weight is None else weight.dtype
+    eight = None
+    if (q is None) != (scales is None):
+        raise ValueError("q and scales go together")
+    if q is not None:
+        if scales.dtype not in SCALES:
+            raise ValueError("scales must be float32 or float8_e8m0fnu")
+        qp, qs = _rows_at(q, on, torch.float8_e4m3fn, shape, "q")
+        count = 1 if block <= 0 else -(-width // block)
+        eight = rvq_rms_8bit(qp, qs, _at(scales, on, scales.dtype, (rows, count), "scales"), block, SCALES[scales.dtype])
+    _enqueue("rvq_rms_norm", on, stream, rvq_norm_dims(rows, width, DTYPES[dtype], DTYPES.get(pd, -1), eps),
+             *_rows_at(x, on, dtype, shape, "x"), *_rows_or_none(residual, on, dtype, shape, "residual"),
+             _mask_on(mask, on), _at(weight, on, pd, (width,), "weight"),
+             *_rows_or_none(total, on, dtype, shape, "total"), *_rows_or_none(y, on, dtype, shape, "y"),
+             _at(rstd, on, torch.float32, (rows,), "rstd"), None if eight is None else ctypes.byref(eight))
+
+
+def rvq_rms_norm_backward(dy, total, weight, rstd, dresidual, dweight, workspace, dtotal=None,
+                          mask: Optional[rvq_dropout_mask] = None, dx=None, stream=None) -> None:
+    """Gradients of rvq_rms_norm from its total (x, where it had neither residual nor mask), mask and rstd; dresidual,
+    dweight and dx may each be None (not computed)."""
+    on = total.get_device()
+    shape, dtype = _shape2(total, "total"), total.dtype
+    rows, width = shape
+    p = weight if weight is not None else dweight
+    pd = torch.float32 if p is None else p.dtype
+    if rstd is None:
+        raise ValueError("rvq_rms_norm_backward needs the forward pass's rstd")
+    _enqueue("rvq_rms_norm_backward", on, stream, rvq_norm_dims(rows, width, DTYPES[dtype], DTYPES.get(pd, -1), 0.0),
+             *_rows_at(dy, on, dtype, shape, "dy"), *_rows_or_none(dtotal, on, dtype, shape, "dtotal"),
+             *_rows_at(total, on, dtype, shape, "total"), _mask_on(mask, on), _at(weight, on, pd, (width,), "weight"),
+             _at(rstd, on, torch.float32, (rows,), "rstd"), *_rows_or_none(dresidual, on, dtype, shape, "dresidual"),
+             *_rows_or_none(dx, on, dtype, shape, "dx"), _at(dweight, on, pd, (width,), "dweight"),
+             *_workspace(workspace, on))
+
+
 def _distill_args(logits, top_logits, top_codes, teacher_lse, weights, temperature):
     on = logits.get_device()
     rows, vocab = shape = _shape2(logits, "logits")
@@ -739,4 +802,5 @@ class RVQPipeline:
             pass
 
 
-from .predictor import BeamSearch, distill_loss, distill_loss_and_grad, dropout, layer_norm  # noqa: E402
+from .predictor import (BeamSearch, distill_loss, distill_loss_and_grad, dropout, layer_norm, rms_norm,  # noqa: E402
+                        rms_norm_8bit)

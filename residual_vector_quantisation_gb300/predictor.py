@@ -104,6 +104,75 @@ def dropout(x: torch.Tensor, mask: _rq.rvq_dropout_mask, residual: Optional[torc
     return _Dropout.apply(x, residual, mask, None if mask is None else mask.tensor)
 
 
+class _RmsNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, residual, weight, eps, mask, step):
+        rows, add = _beside(x, residual)
+        y = torch.empty(rows.shape, dtype=x.dtype, device=x.device)
+        total = None if add is None and mask is None else torch.empty_like(y)
+        rstd = torch.empty(rows.shape[0], dtype=torch.float32, device=x.device)
+        _rq.rvq_rms_norm(rows, weight, eps, y, rstd, add, mask, total)
+        ctx.save_for_backward(rows if total is None else total, weight, rstd, step)
+        ctx.set_materialize_grads(False)
+        ctx.shape, ctx.mask = x.shape, mask
+        return y.view(x.shape) if total is None else (y.view(x.shape), total.view(x.shape))
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dtotal=None):
+        total, weight, rstd, _ = ctx.saved_tensors
+        need, mask = ctx.needs_input_grad, ctx.mask
+        if dy is None and dtotal is None:
+            return (None,) * 6
+        like = dict(dtype=total.dtype, device=total.device)
+        dy = torch.zeros(total.shape, **like) if dy is None else _as_rows(dy.to(total.dtype))
+        dtotal = None if dtotal is None else _as_rows(dtotal.to(total.dtype))
+        dresidual = torch.empty(total.shape, **like) if need[1] or (need[0] and mask is None) else None
+        dx = torch.empty(total.shape, **like) if need[0] and mask is not None else None
+        dweight = workspace = None
+        if weight is not None and need[2]:
+            dweight = torch.empty_like(weight)
+            nbytes = _rq.rvq_rms_norm_workspace_bytes(*total.shape)
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=total.device)
+        _rq.rvq_rms_norm_backward(dy, total, weight, rstd, dresidual, dweight, workspace, dtotal, mask, dx)
+        if mask is None:
+            dx = dresidual
+        return (dx.view(ctx.shape) if need[0] else None, dresidual.view(ctx.shape) if need[1] else None, dweight,
+                None, None, None)
+
+
+def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+             residual: Optional[torch.Tensor] = None, mask: Optional[_rq.rvq_dropout_mask] = None):
+    """Root-mean-square norm over the last axis of x (float32, bfloat16 or float16), or of total = residual + drop(x):
+    y, or (y, total) where a residual or a mask is given, total being the residual of the next sublayer.
+    Differentiable in x, weight (float32, or x's dtype) and residual (x's shape and dtype), from both results.  mask: as
+    in dropout.  Runs on the current stream."""
+    if weight is not None and not weight.is_contiguous():
+        raise ValueError("weight must be contiguous")
+    return _RmsNorm.apply(x, residual, weight, eps, mask, None if mask is None else mask.tensor)
+
+
+def rms_norm_8bit(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                  residual: Optional[torch.Tensor] = None, block: int = 0, powers: bool = False):
+    """The same norm with its result in 8 bits: (q, scales), or (q, scales, total) with a residual.  q: float8_e4m3fn,
+    x's shape; scales [...][n]: one for each `block` columns (32, 64 or 128), or (0) one a row; float32, or, with powers,
+    powers of two (float8_e8m0fnu).  q * scales is the norm's result.  For inference: it has no gradient."""
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, weight, residual)):
+        raise ValueError("rms_norm_8bit has no gradient: call it under torch.no_grad(), or on tensors that need none")
+    if block not in (0, 32, 64, 128):
+        raise ValueError("block must be 0, 32, 64 or 128")
+    if weight is not None and not weight.is_contiguous():
+        raise ValueError("weight must be contiguous")
+    rows, add = _beside(x, residual)
+    count = 1 if block == 0 else -(-x.shape[-1] // block)
+    q = torch.empty(rows.shape, dtype=torch.float8_e4m3fn, device=x.device)
+    scales = torch.empty((rows.shape[0], count), dtype=torch.float8_e8m0fnu if powers else torch.float32, device=x.device)
+    total = None if add is None else torch.empty(rows.shape, dtype=x.dtype, device=x.device)
+    _rq.rvq_rms_norm(rows, weight, eps, None, residual=add, total=total, q=q, scales=scales, block=block)
+    out = q.view(x.shape), scales.view(x.shape[:-1] + (count,))
+    return out if total is None else out + (total.view(x.shape),)
+
+
 def _teacher(logits, top_logits, top_codes, teacher_lse, weights):
     """The loss's arguments as rows."""
     vocab, top = logits.shape[-1], top_logits.shape[-1]

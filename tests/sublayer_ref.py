@@ -49,3 +49,89 @@ def dropout(x, mask, residual=None):
         v = v + residual.double()
         tol = tol + U * v.abs()
     return v, tol
+
+
+# ---------------------------------------------------------------------------
+# root-mean-square norm
+# ---------------------------------------------------------------------------
+
+def total_of(x, mask=None, residual=None):
+    """What is normalised: the sum in 32 bits, rounded to the type (the definition of the operator's `total`)."""
+    h = x.float()
+    if mask is not None:
+        keep, factor = stays(x.numel(), *mask)
+        keep = torch.from_numpy(keep).view(x.shape).to(x.device)
+        h = torch.where(keep, h * torch.tensor(factor, dtype=torch.float32, device=x.device), 0.0)
+    if residual is not None:
+        h = h + residual.float()
+    return h.to(x.dtype)
+
+
+def rms(h, weight, eps, dy=None, dtotal=None, mask=None):
+    """({name: value}, {name: inner tolerance}) of y and, with dy, dresidual, dx (with a mask) and dweight, from h.
+
+    Sums over a row are taken in pieces, a thread's at most 40 terms one after the other and the rest in trees, so that
+    no more than STEPS roundings lie on a path; the rows' sum of dweight likewise (a block's rows one after the other,
+    the blocks in a tree): its terms' roundings are counted with their number where that is more."""
+    h = h.double()
+    rows, width = h.shape
+    w = torch.ones(width, dtype=torch.float64, device=h.device) if weight is None else weight.double()
+    r = 1 / torch.sqrt((h * h).mean(1, keepdim=True) + eps)
+    u = h * r
+    val = {"y": u * w}
+    tol = {"y": STEPS * U * (u * w).abs()}
+    if dy is not None:
+        dy = dy.double()
+        g = dy * w
+        m = (g * u).mean(1, keepdim=True)
+        size = (g * u).abs().mean(1, keepdim=True)
+        dh = r * (g - u * m)
+        inner = STEPS * U * r * (g.abs() + u.abs() * (size + m.abs()))
+        if dtotal is not None:
+            dh = dh + dtotal.double()
+            inner = inner + U * (dh.abs() + dtotal.double().abs())
+        val["dresidual"], tol["dresidual"] = dh, inner
+        if mask is not None:
+            keep, factor = stays(h.numel(), *mask)
+            keep = torch.from_numpy(keep).view(h.shape).to(h.device)
+            val["dx"] = torch.where(keep, dh * factor, 0.0)
+            tol["dx"] = torch.where(keep, inner * factor + 2 * U * val["dx"].abs(), 0.0)
+        val["dweight"] = (dy * u).sum(0)
+        tol["dweight"] = (STEPS + rows / 152) * U * (dy * u).abs().sum(0)
+    return val, tol
+
+
+def e4m3_grid():
+    """The values of e4m3 that are not negative, in order."""
+    v = [m * 2.0 ** -9 for m in range(8)]
+    v += [(1 + m / 8) * 2.0 ** (e - 7) for e in range(1, 16) for m in range(8)]
+    return torch.tensor(v[:-1], dtype=torch.float64)       # the last code is NaN
+
+
+def check_8bit(q, scales, y, tol, block, powers):
+    """q * scales is y (64 bits, off by at most tol) to half a step of e4m3 at its place; the scales are the blocks'
+    largest magnitudes / 448, at least 2^-126, and, with powers, the next power of two."""
+    y, tol = y.cpu(), tol.cpu()
+    rows, width = y.shape
+    size = block or width
+    count = -(-width // size)
+    s, got = scales.float().double().cpu(), q.float().double().cpu()
+    assert s.shape == (rows, count) and bool(torch.isfinite(got).all())
+    grid = e4m3_grid()
+    step = torch.cat([grid[1:] - grid[:-1], grid[-1:] - grid[-2:-1]])
+    for i in range(count):
+        a, b = i * size, min(width, (i + 1) * size)
+        most, off = y[:, a:b].abs().amax(1), tol[:, a:b].amax(1)
+        low, high = (torch.clamp(v / 448, min=2.0 ** -126) for v in (most - off, most + off))
+        if powers:
+            low, high = (2.0 ** torch.ceil(torch.log2(v)) for v in (low, high))
+            assert bool(((s[:, i] == low) | (s[:, i] == high)).all())
+        else:   # the division is rounded once
+            assert bool((s[:, i] >= low * (1 - 2 * U)).all()) and bool((s[:, i] <= high * (1 + 2 * U)).all())
+        # a value is at most half a step from y / scale (its quotient is rounded twice); the step at its place is the
+        # larger of those on its two sides
+        t = got[:, a:b].abs()
+        at = torch.searchsorted(grid, t.contiguous())
+        assert bool((grid[at] == t).all())
+        off = (y[:, a:b] / s[:, i:i + 1] - got[:, a:b]).abs()
+        assert bool((off <= step[at] / 2 + 4 * U * t + tol[:, a:b] / s[:, i:i + 1]).all())

@@ -87,3 +87,65 @@ def test_dropout_refusals(lib):
     for kw in (dict(y=AT + 2), dict(y=AT, ys=65), dict(y=AT - 128), dict(x=3 * AT, r=AT, y=AT + 2), dict(r=2 * AT, rs=65),
                dict(m=mask(step=2 * AT + 8))):
         assert run(**kw) == INVALID, kw
+
+
+RMS = (4, 64, 1, 0, 1e-6)
+
+
+def rms_call(lib, dims=RMS, x=AT, xs=64, r=None, rs=64, m=None, w=2 * AT, t=None, ts=64, y=3 * AT, ys=64, rstd=None, q=None):
+    return lib.rvq_rms_norm(rq.rvq_norm_dims(*dims), ptr(x), xs, ptr(r), rs, None if m is None else ctypes.byref(m), ptr(w),
+                            ptr(t), ts, ptr(y), ys, ptr(rstd), None if q is None else ctypes.byref(q), None)
+
+
+def eight(values=5 * AT, stride=64, scales=6 * AT, block=32, kind=0):
+    return rq.rvq_rms_8bit(values, stride, scales, block, kind)
+
+
+def test_rms_norm_refusals(lib):
+    for dims in ((-1, 64, 1, 0, 1e-5), (4, 0, 1, 0, 1e-5), (4, 64, 3, 0, 1e-5), (4, 64, -1, 0, 1e-5), (4, 64, 1, 2, 1e-5),
+                 (4, 64, 0, 1, 1e-5), (4, 64, 1, 0, -1.0), (4, 64, 1, 0, float("nan"))):
+        assert rms_call(lib, dims) == INVALID, dims
+    assert rms_call(lib, (4, 16385, 1, 0, 1e-5), xs=20000, ys=20000) == UNSUPPORTED
+    for kw in (dict(x=None), dict(y=None), dict(xs=63), dict(ys=63), dict(x=AT + 1), dict(y=AT + 1), dict(w=AT + 2),
+               dict(rstd=AT + 2), dict(r=4 * AT, rs=63), dict(r=4 * AT + 1), dict(r=4 * AT, t=7 * AT, ts=63),
+               dict(r=4 * AT, t=7 * AT + 1), dict(t=7 * AT),                       # nothing is added: the sum is x
+               dict(m=mask(2.0)), dict(q=eight(values=None)), dict(q=eight(scales=None)), dict(q=eight(scales=AT + 2)),
+               dict(q=eight(stride=63)), dict(q=eight(block=16)), dict(q=eight(block=-1)), dict(q=eight(kind=2))):
+        assert rms_call(lib, **kw) == INVALID, kw
+    assert rms_call(lib, (0, 64, 1, 0, 1e-5), x=None, y=None) == 0
+
+
+def test_rms_norm_refuses_overlaps(lib):
+    """Rows of 128 bytes; refused on the host."""
+    far = dict(r=4 * AT, t=7 * AT)
+    for kw in (dict(y=AT + 2), dict(y=AT, ys=65), dict(y=AT - 128), dict(r=4 * AT, y=4 * AT + 2), dict(far, t=AT + 2),
+               dict(far, t=3 * AT), dict(far, t=4 * AT, ts=72), dict(y=2 * AT), dict(y=2 * AT + 128), dict(rstd=AT),
+               dict(rstd=3 * AT + 8), dict(far, rstd=7 * AT), dict(q=eight(values=AT)), dict(q=eight(values=3 * AT + 500)),
+               dict(q=eight(scales=AT + 8)), dict(q=eight(scales=5 * AT + 8)), dict(q=eight(scales=2 * AT)),
+               dict(rstd=6 * AT, q=eight()), dict(far, m=mask(step=7 * AT + 8)), dict(m=mask(step=3 * AT))):
+        assert rms_call(lib, **kw) == INVALID, kw
+
+
+def test_rms_norm_backward_refusals(lib):
+    need = lib.rvq_rms_norm_workspace_bytes(4, 64)
+    assert need >= 4 * 64 * 4
+    assert lib.rvq_rms_norm_workspace_bytes(-1, 64) == 0 and lib.rvq_rms_norm_workspace_bytes(4, 16385) == 0
+    assert lib.rvq_rms_norm_workspace_bytes(4, 0) == 0 and lib.rvq_rms_norm_workspace_bytes(0, 64) > 0
+    assert lib.rvq_rms_norm_workspace_bytes(10 ** 9, 16384) < 1 << 25
+
+    def back(dims=RMS, dy=AT, dys=64, dt=None, dts=64, t=2 * AT, ts=64, m=None, w=3 * AT, rstd=4 * AT, dr=5 * AT, drs=64,
+             dx=None, dxs=64, dw=6 * AT, ws=7 * AT, nb=need):
+        return lib.rvq_rms_norm_backward(rq.rvq_norm_dims(*dims), ptr(dy), dys, ptr(dt), dts, ptr(t), ts,
+                                         None if m is None else ctypes.byref(m), ptr(w), ptr(rstd), ptr(dr), drs, ptr(dx),
+                                         dxs, ptr(dw), ptr(ws), nb, None)
+
+    for kw in (dict(dy=None), dict(t=None), dict(rstd=None), dict(dys=63), dict(ts=63), dict(dt=8 * AT, dts=63), dict(drs=63),
+               dict(dy=AT + 1), dict(t=AT + 1), dict(dt=AT + 1), dict(dr=AT + 1), dict(w=AT + 2), dict(dw=AT + 2),
+               dict(rstd=AT + 2), dict(ws=None), dict(ws=7 * AT + 8), dict(nb=need - 1), dict(dx=8 * AT),
+               dict(dx=8 * AT, m=mask(), dxs=63), dict(dx=8 * AT + 1, m=mask()), dict(m=mask(-1.0)),
+               # overlaps
+               dict(dr=AT + 2), dict(dr=2 * AT, drs=65), dict(dt=8 * AT, dr=8 * AT + 128), dict(dr=3 * AT), dict(dr=4 * AT),
+               dict(dx=5 * AT, m=mask()), dict(dx=AT + 2, m=mask()), dict(dw=AT), dict(dw=5 * AT), dict(ws=AT), dict(ws=6 * AT),
+               dict(dr=7 * AT + need - 128), dict(dx=8 * AT, m=mask(step=8 * AT))):
+        assert back(**kw) == INVALID, kw
+    assert back(dr=None, dw=None, ws=None, nb=0) == 0                  # nothing asked for

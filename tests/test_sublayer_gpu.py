@@ -185,3 +185,302 @@ def test_dropout_graph_counts_its_steps():
         assert torch.equal(y.double(), val) and torch.equal(dx.double(), 2 * val)
         seen.append(y.clone())
     assert not torch.equal(seen[0], seen[1]) and not torch.equal(seen[1], seen[2])
+
+
+# ---------------------------------------------------------------------------
+# root-mean-square norm
+# ---------------------------------------------------------------------------
+
+MASK = (0.2, 17, 4, 2)
+
+
+def mask_of(m):
+    return None if m is None else rq.rvq_dropout_mask(m[0], m[1], m[2], step_of(m[3]))
+
+
+def run_rms(x, w, eps, dy, r=None, m=None, dt=None, place=lambda t: t.clone()):
+    """Both passes, every tensor where `place` puts it; outputs hold NaN before."""
+    rows, width = x.shape
+    mask = mask_of(m)
+    out = {"y": place(torch.full_like(x, NAN))}
+    if r is not None or mask is not None:
+        out["total"] = place(torch.full_like(x, NAN))
+    rstd = torch.full((rows,), NAN, device=DEV)
+    xv, rv = place(x), None if r is None else place(r)
+    rq.rvq_rms_norm(xv, w, eps, out["y"], rstd, rv, mask, out.get("total"))
+    total = out.get("total", xv)
+    out["dresidual"] = place(torch.full_like(x, NAN))
+    if mask is not None:
+        out["dx"] = place(torch.full_like(x, NAN))
+    out["dweight"] = None if w is None else torch.full_like(w, NAN)
+    need = rq.rvq_rms_norm_workspace_bytes(rows, width)
+    buffer = torch.full((need + (1 << 16),), 0xFF, dtype=torch.uint8, device=DEV)
+    rq.rvq_rms_norm_backward(place(dy), total, w, rstd, out["dresidual"], out["dweight"], buffer[:need],
+                             None if dt is None else place(dt), mask, out.get("dx"))
+    assert bool((buffer[need:] == 0xFF).all())
+    return out
+
+
+def check_rms(got, x, w, eps, dy, r=None, m=None, dt=None):
+    total = ref.total_of(x, m, r)
+    if "total" in got:
+        assert torch.equal(got["total"], total)
+    val, tol = ref.rms(total, w, eps, dy, dt, m)
+    for k in val:
+        if got[k] is not None:
+            ref.check(got[k], val[k], tol[k], k)
+
+
+def make_rms(rows, width, dtype, pdtype):
+    g = gen(rows * 31 + width)
+    x, r, dy, dt = (randn(g, rows, width).to(dtype) for _ in range(4))
+    return x, r, dy, dt, (1 + 0.2 * randn(g, width)).to(pdtype)
+
+
+@pytest.mark.parametrize("dtype,pdtype", [(F32, F32), (BF16, F32), (BF16, BF16), (F16, F32), (F16, F16)])
+@pytest.mark.parametrize("rows,width", [(1, 1), (1, 1024), (3, 7), (5, 33), (130, 256), (700, 768), (9, 1000), (33, 1024),
+                                        (6, 1025), (17, 1032), (4, 2048), (3, 4097), (200, 1500), (2, 8200), (5, 12288),
+                                        (3, 13400), (2, 16384), (2, 16383)])
+def test_rms_sizes(rows, width, dtype, pdtype):
+    x, r, dy, dt, w = make_rms(rows, width, dtype, pdtype)
+    check_rms(run_rms(x, w, 1e-6, dy), x, w, 1e-6, dy)
+    check_rms(run_rms(x, w, 1e-6, dy, r, None, dt), x, w, 1e-6, dy, r, None, dt)
+    check_rms(run_rms(x, w, 1e-6, dy, r, MASK, dt), x, w, 1e-6, dy, r, MASK, dt)
+    check_rms(run_rms(x, w, 1e-6, dy, None, MASK), x, w, 1e-6, dy, None, MASK)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("pad,shift", [(8, 0), (3, 0), (0, 1), (5, 7)])
+@pytest.mark.parametrize("width", [1, 9, 40, 250, 500, 1024, 1500, 9000])
+def test_rms_strides_and_alignment(width, pad, shift, dtype):
+    rows = 37 if width < 5000 else 9
+    x, r, dy, dt, w = make_rms(rows, width, dtype, F32)
+    placed = []
+
+    def place(t):
+        placed.append(rows_in(t, pad, shift))
+        return placed[-1]
+
+    check_rms(run_rms(x, w, 1e-6, dy, r, MASK, dt, place), x, w, 1e-6, dy, r, MASK, dt)
+    check_rms(run_rms(x, w, 1e-6, dy, r, None, dt, place), x, w, 1e-6, dy, r, None, dt)
+    assert all(untouched(t) for t in placed)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("width", [5, 100, 768, 1025, 5000])
+def test_rms_tensors_that_lie_differently(width, dtype):
+    x, r, dy, dt, w = make_rms(21, width, dtype, F32)
+    placed = []
+
+    def place(t):
+        placed.append(rows_in(t, len(placed) % 5, 3 * len(placed) % 8))
+        return placed[-1]
+
+    check_rms(run_rms(x, w, 1e-6, dy, r, MASK, dt, place), x, w, 1e-6, dy, r, MASK, dt)
+    assert all(untouched(t) for t in placed)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("width", [1, 8, 48, 96, 130, 248, 256, 257, 352, 512, 519])
+def test_rms_narrow_rows_share_a_warp(width, dtype):
+    """Row counts that leave a warp's last rows, and a block's, without work."""
+    for rows in (1, 7, 153, 1219, 5003):
+        x, r, dy, dt, w = make_rms(rows, width, dtype, F32)
+        check_rms(run_rms(x, w, 1e-6, dy, r, MASK, dt), x, w, 1e-6, dy, r, MASK, dt)
+        check_rms(run_rms(x, w, 1e-6, dy), x, w, 1e-6, dy)
+
+
+@pytest.mark.parametrize("width", [96, 1024, 3000])
+def test_rms_without_weight_in_place_and_parts(width):
+    x, r, dy, dt, w = make_rms(41, width, F32, F32)
+    check_rms(run_rms(x, None, 1e-6, dy, r, MASK, dt), x, None, 1e-6, dy, r, MASK, dt)
+    want = run_rms(x, w, 1e-6, dy, r, MASK, dt)
+    mask = mask_of(MASK)
+    # the sum over the residual and the result over x, and the other way round
+    for swap in (False, True):
+        xx, rr = x.clone(), r.clone()
+        y, total = (rr, xx) if swap else (xx, rr)
+        rstd = torch.empty(41, device=DEV)
+        rq.rvq_rms_norm(xx, w, 1e-6, y, rstd, rr, mask, total)
+        assert torch.equal(y, want["y"]) and torch.equal(total, want["total"])
+    # gradients over what they are made from, and each of them alone
+    for over in range(3):
+        t = [dy.clone(), want["total"].clone(), dt.clone()]
+        dx = t[(over + 1) % 3]
+        rq.rvq_rms_norm_backward(t[0], t[1], w, rstd, t[over], None, None, t[2], mask, dx)
+        assert torch.equal(t[over], want["dresidual"]) and torch.equal(dx, want["dx"])
+    ws = torch.empty(rq.rvq_rms_norm_workspace_bytes(41, width), dtype=torch.uint8, device=DEV)
+    for k in ("dresidual", "dx", "dweight"):
+        out = {n: None for n in ("dresidual", "dx", "dweight")}
+        out[k] = torch.empty_like(want[k])
+        rq.rvq_rms_norm_backward(dy, want["total"], w, rstd, out["dresidual"], out["dweight"], ws, dt, mask, out["dx"])
+        assert torch.equal(out[k], want[k]), k
+
+
+def test_rms_odd_values_and_no_rows():
+    x, _, dy, _, w = make_rms(7, 512, F32, F32)
+    x[1] = 0.0                      # the norm of zeros: eps alone
+    x[2] = 1e-30
+    x[3] *= 1e15
+    x[4, 17] = NAN
+    x[5, 3] = INF
+    x[6] = 3e19                     # its square is past float32: infinite, and the result zero
+    got = run_rms(x, w, 1e-6, dy)
+    val, tol = ref.rms(x[:4], w, 1e-6, dy[:4])
+    ref.check(got["y"][:4], val["y"], tol["y"] + 1e-38, "y")
+    ref.check(got["dresidual"][:4], val["dresidual"], tol["dresidual"], "dresidual")
+    assert bool(torch.isnan(got["y"][4]).all()) and bool(torch.isnan(got["dresidual"][4:6]).all())
+    assert bool(torch.isnan(got["y"][5, 3])) and bool((got["y"][5, :3] == 0).all()) and bool((got["y"][6] == 0).all())
+    empty = torch.empty((0, 64), device=DEV)
+    w = torch.ones(64, device=DEV)
+    assert bool((run_rms(empty, w, 1e-6, empty)["dweight"] == 0).all())
+
+
+def test_rms_many_rows_and_repeats():
+    x, r, dy, dt, w = make_rms(20011, 192, BF16, F32)
+    one = run_rms(x, w, 1e-6, dy, r, MASK, dt)
+    check_rms(one, x, w, 1e-6, dy, r, MASK, dt)
+    two = run_rms(x, w, 1e-6, dy, r, MASK, dt)
+    for k in one:
+        assert torch.equal(one[k], two[k]), k
+
+
+def run_8bit(x, w, r, block, powers, pad=0, shift=0, m=None):
+    rows, width = x.shape
+    count = -(-width // block) if block else 1
+    buffer = torch.full((rows * (width + pad) + shift + 16,), 0x5A, dtype=torch.uint8, device=DEV)
+    q = buffer.as_strided((rows, width), (width + pad, 1), shift).view(torch.float8_e4m3fn)
+    scales = torch.full((rows, count), NAN, device=DEV).to(torch.float8_e8m0fnu if powers else F32)
+    total = None if r is None else torch.empty_like(x)
+    xv = rows_in(x, pad, shift)
+    rq.rvq_rms_norm(xv, w, 1e-6, None, None, None if r is None else rows_in(r, pad, shift), mask_of(m),
+                    None if total is None else rows_in(total, pad, shift), q, scales, block)
+    held = buffer.clone()
+    held.as_strided((rows, width), (width + pad, 1), shift).fill_(0x5A)
+    assert bool((held == 0x5A).all())
+    return q, scales
+
+
+@pytest.mark.parametrize("powers", [False, True])
+@pytest.mark.parametrize("block", [0, 32, 64, 128])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_rms_8bit(dtype, block, powers):
+    for rows, width, pad, shift in ((1, 1, 0, 0), (3, 31, 0, 0), (5, 64, 0, 0), (700, 200, 0, 0), (9, 768, 16, 0),
+                                    (33, 1024, 0, 0), (5, 1025, 6, 0), (6, 1100, 0, 0), (7, 1100, 3, 5), (4, 520, 2, 1),
+                                    (3, 5000, 0, 0), (2, 5003, 1, 3), (2, 16384, 0, 0), (2, 16383, 0, 0), (1200, 40, 1, 1)):
+        g = gen(rows + width)
+        x, r = (randn(g, rows, width).to(dtype) for _ in range(2))
+        x *= torch.exp(randn(g, rows, width)).to(dtype)
+        w = 1 + 0.2 * randn(g, width)
+        for res in (None, r):
+            val, tol = ref.rms(ref.total_of(x, None, res), w, 1e-6)
+            q, s = run_8bit(x, w, res, block, powers, pad, shift)
+            ref.check_8bit(q, s, val["y"], tol["y"], block, powers)
+
+
+def test_rms_8bit_beside_y_with_a_mask_and_odd_values():
+    g = gen(5)
+    x, r = randn(g, 6, 256).to(BF16), randn(g, 6, 256).to(BF16)
+    w = 1 + 0.2 * randn(g, 256)
+    val, tol = ref.rms(ref.total_of(x, MASK, r), w, 1e-6)
+    q, s = run_8bit(x, w, r, 64, True, m=MASK)
+    ref.check_8bit(q, s, val["y"], tol["y"], 64, True)
+    y, q2, s2 = torch.empty_like(x), torch.empty_like(q), torch.empty_like(s)
+    rq.rvq_rms_norm(x, w, 1e-6, y, None, r, mask_of(MASK), None, q2, s2, 64)
+    assert torch.equal(q.view(torch.uint8), q2.view(torch.uint8)) and torch.equal(s.view(torch.uint8), s2.view(torch.uint8))
+    ref.check(y, val["y"], tol["y"], "y")
+    # a block of zeros, a NaN in one row, and a weight that makes one block's values overflow
+    x = randn(g, 4, 256)
+    x[1] = 0.0
+    x[2, 7] = NAN
+    w = torch.ones(256, device=DEV)
+    w[64:128] = INF
+    for powers in (False, True):
+        q, s = run_8bit(x, w, None, 64, powers)
+        q, s = q.float(), s.float()
+        assert bool((s[1, [0, 2, 3]] == 2.0 ** -126).all()) and bool((q[1, 128:] == 0).all())
+        assert bool(torch.isnan(s[2]).all()) and bool(torch.isnan(q[2]).all())
+        assert bool(torch.isnan(s[0, 1]) if powers else torch.isinf(s[0, 1])) and bool(torch.isnan(q[0, 64:128]).all())
+        assert bool(torch.isfinite(q[0, :64]).all()) and bool(torch.isfinite(q[0, 128:]).all())
+
+
+def test_rms_8bit_scales_at_their_borders():
+    """Largest magnitudes of 448 * 2^k and its neighbours: the next power of two, no value past the type's largest."""
+    eps = 1e-6                                 # run_8bit's
+    for k in (-9, -1, 0, 3):
+        for ulps in (-1, 0, 1):
+            x = torch.zeros((1, 64), device=DEV)
+            w = torch.zeros(64, device=DEV)
+            x[0, 0] = 1.0                      # rstd is about 8
+            rstd = torch.empty(1, device=DEV)
+            y = torch.empty_like(x)
+            rq.rvq_rms_norm(x, torch.ones(64, device=DEV), eps, y, rstd)
+            target = torch.tensor(448.0 * 2.0 ** k)
+            for _ in range(abs(ulps)):
+                target = torch.nextafter(target, torch.tensor(INF if ulps > 0 else 0.0))
+            # a weight whose product with y is the target, where there is one
+            w0 = (target.double() / y[0, 0].double().cpu()).float()
+            for d in range(-2, 3):
+                c = w0
+                for _ in range(abs(d)):
+                    c = torch.nextafter(c, torch.tensor(INF if d > 0 else 0.0))
+                w[0] = c
+                q, s = run_8bit(x, w, None, 32, True)
+                most = (y[0, 0] * w[0]).double().item()
+                want = 2.0 ** math.ceil(math.log2(most / 448))
+                assert s[0, 0].float().item() == want and abs(q[0, 0].float().item()) <= 448.0
+
+
+def test_rms_autograd():
+    g = gen(9)
+    x, r, up, ut = (randn(g, 2, 9, 64) for _ in range(4))
+    w = 1 + 0.2 * randn(g, 64)
+    flat = [t.view(18, 64) for t in (x, r, up, ut)]
+    for res, m in ((False, None), (True, None), (False, MASK), (True, MASK)):
+        xs, rs, ws = (t.clone().requires_grad_() for t in (x, r, w))
+        out = rq.rms_norm(xs, ws, 1e-6, rs if res else None, mask_of(m))
+        both = isinstance(out, tuple)
+        assert both == (res or m is not None)
+        torch.autograd.backward(out, (up, ut) if both else (up,))
+        val, tol = ref.rms(ref.total_of(flat[0], m, flat[1] if res else None), w, 1e-6, flat[2], flat[3] if both else None, m)
+        ref.check(xs.grad.view(18, 64), val["dx" if m else "dresidual"], tol["dx" if m else "dresidual"], "dx")
+        ref.check(ws.grad, val["dweight"], tol["dweight"], "dweight")
+        if res:
+            ref.check(rs.grad.view(18, 64), val["dresidual"], tol["dresidual"], "dresidual")
+    # the sum alone is used, or the result alone
+    xs, rs = x.clone().requires_grad_(), r.clone().requires_grad_()
+    rq.rms_norm(xs, w, 1e-6, rs)[1].backward(ut)
+    assert torch.equal(xs.grad, ut) and torch.equal(rs.grad, ut)
+    xs.grad = None
+    rq.rms_norm(xs, w, 1e-6, r)[0].backward(up)
+    val, tol = ref.rms(ref.total_of(flat[0], None, flat[1]), w, 1e-6, flat[2])
+    ref.check(xs.grad.view(18, 64), val["dresidual"], tol["dresidual"], "dx")
+    with pytest.raises(ValueError):
+        rq.rms_norm_8bit(xs, w)
+    with torch.no_grad():
+        q, s, total = rq.rms_norm_8bit(xs, w, 1e-6, r, 32, True)
+    assert q.shape == x.shape and s.shape == (2, 9, 2) and torch.equal(total, x + r)
+    val, tol = ref.rms(total.view(18, 64), w, 1e-6)
+    ref.check_8bit(q.view(18, 64), s.view(18, 2), val["y"], tol["y"], 32, True)
+
+
+def test_rms_gradient_against_differences():
+    """d sum(c * y + d * total) along a direction, by differences of the 64-bit statement."""
+    g = gen(10)
+    x, r, up, ut, dx, dr = (randn(g, 5, 40).double() for _ in range(6))
+    w, dw = 1 + 0.2 * randn(g, 40).double(), randn(g, 40).double()
+    keep, factor = ref.stays(200, *MASK)
+    keep = torch.from_numpy(keep).view(5, 40).to(DEV)
+
+    def value(t):
+        h = torch.where(keep, (x + t * dx) * factor, 0.0) + r + t * dr
+        return (h / torch.sqrt((h * h).mean(1, keepdim=True) + 1e-6) * (w + t * dw) * up + h * ut).sum().item()
+
+    step = 1e-5
+    want = (value(step) - value(-step)) / (2 * step)
+    xs, rs, ws = (t.float().requires_grad_() for t in (x, r, w))
+    torch.autograd.backward(rq.rms_norm(xs, ws, 1e-6, rs, mask_of(MASK)), (up.float(), ut.float()))
+    terms = [(xs.grad.double() * dx), (rs.grad.double() * dr), (ws.grad.double() * dw)]
+    got, size = sum(t.sum().item() for t in terms), sum(t.abs().sum().item() for t in terms)
+    # the inputs' rounding and the gradient's (64 roundings of 2^-24 each), and the differences' own error of about step^2
+    assert abs(got - want) <= size * (128 * ref.U + 1e-8), (got, want)
