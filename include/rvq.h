@@ -613,6 +613,52 @@ RVQ_API rvq_status rvq_rms_norm_backward(rvq_norm_dims dims, const void *dy, int
                                          void *dresidual, int64_t dresidual_stride, void *dx, int64_t dx_stride,
                                          void *dweight, void *workspace, size_t workspace_bytes, rvq_stream_t stream);
 
+/* Log probabilities of `rows` rows of `vocab` logits (1 <= vocab <= 2^20) at
+ * temperature T (as in rvq_distill_dims), with the `top` best alternatives of
+ * each (0 <= top <= 64).  dtype: of logits and dlogits. */
+typedef struct rvq_log_probs_dims {
+  int64_t rows;
+  int32_t vocab;
+  int32_t top;
+  int32_t dtype;
+  float temperature;
+} rvq_log_probs_dims;
+
+/* Per row, with p = softmax(logits / T), the outputs that are not NULL:
+ *   log_probs [rows]: log p[codes[row]].  A code of -1 is none (padding): 0.
+ *     Other codes outside [0, vocab) are taken as none too, and counted into
+ *     *bad_codes if it is not NULL (device int64, added to atomically).  codes and
+ *     log_probs go together;
+ *   entropy [rows]: -sum p log p (codes without a share add nothing);
+ *   lse [rows]: log sum exp(logits / T);
+ *   stats [rows][2]: the largest logit m and the sum of exp((logit - m) / T), for
+ *     rvq_log_probs_backward;
+ *   top_log_probs, top_codes [rows][top]: the largest logits' log p and codes, best
+ *     first, of equal ones the lower code.  NaN and -inf are never among them;
+ *     places for which nothing is left hold -inf and -1.  (As a teacher of
+ *     rvq_distill: top_logits = T * top_log_probs with a teacher_lse of zeros.)
+ * A row of nothing but -inf has no distribution: its lse and its code's log p are
+ * -inf, its entropy is 0.  A logit of +inf or NaN makes the row's numbers NaN (its
+ * top_codes are those of its other values, +inf among them).  A row of nothing but
+ * the type's lowest value is a uniform distribution.  What is written may not meet
+ * anything else (RVQ_ERR_INVALID_ARG). */
+RVQ_API rvq_status rvq_log_probs(rvq_log_probs_dims dims, const void *logits, int64_t logits_stride,
+                                 const int32_t *codes, float *log_probs, float *entropy, float *lse, float *stats,
+                                 float *top_log_probs, int32_t *top_codes, int64_t *bad_codes, rvq_stream_t stream);
+
+/* dlogits from the gradients of log_probs, entropy and lse ([rows] each, nullable:
+ * zero), with rvq_log_probs' stats and, where grad_entropy is given, its entropy:
+ *   dlogits[j] = (g_p ([j = code] - p_j) + g_l p_j - g_h p_j (log p_j + entropy)) / T.
+ * (top_log_probs have no gradient here.)  A row to which no gradient comes, all of
+ * them 0, has gradient 0 whatever its logits hold, and so has a row of nothing but
+ * -inf.  dlogits may be logits itself (same stride); rows that overlap in another
+ * way are refused. */
+RVQ_API rvq_status rvq_log_probs_backward(rvq_log_probs_dims dims, const float *grad_log_probs,
+                                          const float *grad_entropy, const float *grad_lse, const void *logits,
+                                          int64_t logits_stride, const int32_t *codes, const float *stats,
+                                          const float *entropy, void *dlogits, int64_t dlogits_stride,
+                                          rvq_stream_t stream);
+
 /* Static strings. */
 RVQ_API const char *rvq_status_string(rvq_status status);
 RVQ_API const char *rvq_version(void);

@@ -38,7 +38,7 @@ __all__ = [
     "RVQ_BEAM_MAX_STATES", "DTYPES", "layer_norm", "distill_loss", "distill_loss_and_grad", "BeamSearch",
     "rvq_dropout_mask", "rvq_dropout_dims", "rvq_dropout", "dropout", "rvq_rms_8bit", "rvq_rms_norm",
     "rvq_rms_norm_workspace_bytes", "rvq_rms_norm_backward", "RVQ_SCALE_F32", "RVQ_SCALE_E8M0", "rms_norm",
-    "rms_norm_8bit",
+    "rms_norm_8bit", "rvq_log_probs_dims", "rvq_log_probs", "rvq_log_probs_backward", "log_probs", "LogProbs",
 ]
 
 RVQ_OK = 0
@@ -58,6 +58,7 @@ EXPORTED_SYMBOLS = [
     "rvq_layer_norm", "rvq_layer_norm_workspace_bytes", "rvq_layer_norm_backward", "rvq_distill",
     "rvq_distill_backward", "rvq_beam_workspace_bytes", "rvq_beam_select", "rvq_beam_reorder",
     "rvq_dropout", "rvq_rms_norm", "rvq_rms_norm_workspace_bytes", "rvq_rms_norm_backward",
+    "rvq_log_probs", "rvq_log_probs_backward",
 ]
 
 # int (*rvq_cancel_fn)(void *user)
@@ -129,6 +130,11 @@ class rvq_rms_8bit(ctypes.Structure):
                 ("block", ctypes.c_int32), ("scale_type", ctypes.c_int32)]
 
 
+class rvq_log_probs_dims(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("vocab", ctypes.c_int32), ("top", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("temperature", ctypes.c_float)]
+
+
 class rvq_beam_dims(ctypes.Structure):
     _fields_ = [("groups", ctypes.c_int64), ("beams", ctypes.c_int32), ("vocab", ctypes.c_int32),
                 ("select", ctypes.c_int32), ("mode", ctypes.c_int32), ("dtype", ctypes.c_int32)]
@@ -194,6 +200,8 @@ def load_library(path: Optional[str] = None):
         "rvq_rms_norm_workspace_bytes": ([i64, i32], sz),
         "rvq_rms_norm_backward": ([rvq_norm_dims, vp, i64, vp, i64, vp, i64, ctypes.POINTER(rvq_dropout_mask), vp, vp,
                                    vp, i64, vp, i64, vp, vp, sz, vp], ctypes.c_int),
+        "rvq_log_probs": ([rvq_log_probs_dims, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp], ctypes.c_int),
+        "rvq_log_probs_backward": ([rvq_log_probs_dims, vp, vp, vp, vp, i64, vp, vp, vp, vp, i64, vp], ctypes.c_int),
         "rvq_beam_workspace_bytes": ([rvq_beam_dims], sz),
         "rvq_beam_select": ([rvq_beam_dims, vp, i64, vp, vp, i32, vp, vp, vp, vp, vp, sz, vp], ctypes.c_int),
         "rvq_beam_reorder": ([rvq_beam_dims, vp, ctypes.POINTER(rvq_beam_state), i32, vp], ctypes.c_int),
@@ -549,6 +557,36 @@ def rvq_rms_norm_backward(dy, total, weight, rstd, dresidual, dweight, workspace
              *_workspace(workspace, on))
 
 
+def rvq_log_probs(logits, codes, temperature: float, log_probs=None, entropy=None, lse=None, stats=None,
+                  top_log_probs=None, top_codes=None, bad_codes=None, stream=None) -> None:
+    """Log probabilities [rows] of codes [rows] (int32, -1: none) under logits [rows][vocab] (see rvq.h), and what else
+    has a place to go: entropy and lse [rows], stats [rows][2], top_log_probs and top_codes [rows][top]."""
+    on = logits.get_device()
+    rows, vocab = shape = _shape2(logits, "logits")
+    top = 0 if top_codes is None else top_codes.shape[-1]
+    one, best, f32 = (rows,), (rows, top), torch.float32
+    _enqueue("rvq_log_probs", on, stream, rvq_log_probs_dims(rows, vocab, top, DTYPES[logits.dtype], temperature),
+             *_rows_at(logits, on, logits.dtype, shape, "logits"), _at(codes, on, torch.int32, one, "codes"),
+             _at(log_probs, on, f32, one, "log_probs"), _at(entropy, on, f32, one, "entropy"),
+             _at(lse, on, f32, one, "lse"), _at(stats, on, f32, (rows, 2), "stats"),
+             _at(top_log_probs, on, f32, best, "top_log_probs"), _at(top_codes, on, torch.int32, best, "top_codes"),
+             _at(bad_codes, on, torch.int64, (1,), "bad_codes"))
+
+
+def rvq_log_probs_backward(grad_log_probs, grad_entropy, grad_lse, logits, codes, temperature: float, stats, entropy,
+                           dlogits, stream=None) -> None:
+    """dlogits from the gradients [rows] of rvq_log_probs' log_probs, entropy and lse (None: zero), with its stats and
+    entropy."""
+    on = logits.get_device()
+    rows, vocab = shape = _shape2(logits, "logits")
+    one, f32 = (rows,), torch.float32
+    _enqueue("rvq_log_probs_backward", on, stream, rvq_log_probs_dims(rows, vocab, 0, DTYPES[logits.dtype], temperature),
+             _at(grad_log_probs, on, f32, one, "grad_log_probs"), _at(grad_entropy, on, f32, one, "grad_entropy"),
+             _at(grad_lse, on, f32, one, "grad_lse"), *_rows_at(logits, on, logits.dtype, shape, "logits"),
+             _at(codes, on, torch.int32, one, "codes"), _at(stats, on, f32, (rows, 2), "stats"),
+             _at(entropy, on, f32, one, "entropy"), *_rows_at(dlogits, on, logits.dtype, shape, "dlogits"))
+
+
 def _distill_args(logits, top_logits, top_codes, teacher_lse, weights, temperature):
     on = logits.get_device()
     rows, vocab = shape = _shape2(logits, "logits")
@@ -802,5 +840,5 @@ class RVQPipeline:
             pass
 
 
-from .predictor import (BeamSearch, distill_loss, distill_loss_and_grad, dropout, layer_norm, rms_norm,  # noqa: E402
-                        rms_norm_8bit)
+from .predictor import (BeamSearch, LogProbs, distill_loss, distill_loss_and_grad, dropout, layer_norm,  # noqa: E402
+                        log_probs, rms_norm, rms_norm_8bit)

@@ -8,7 +8,7 @@ own what those leave to the caller: outputs, statistics and workspaces.
 
 from __future__ import annotations
 
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 from torch.autograd.function import once_differentiable
@@ -173,6 +173,68 @@ def rms_norm_8bit(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: f
     return out if total is None else out + (total.view(x.shape),)
 
 
+class LogProbs(NamedTuple):
+    """What log_probs gives; None where it was not asked for."""
+    log_probs: Optional[torch.Tensor]
+    entropy: Optional[torch.Tensor]
+    lse: torch.Tensor
+    top_log_probs: Optional[torch.Tensor]
+    top_codes: Optional[torch.Tensor]
+
+
+class _LogProbs(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, codes, entropy, top, temperature):
+        rows = _as_rows(logits)
+        n, lead = rows.shape[0], logits.shape[:-1]
+        if codes is not None:
+            if codes.shape != lead:
+                raise ValueError("codes must have the logits' leading axes")
+            codes = _int32(codes).reshape(-1).contiguous()
+
+        def one(*shape, dtype=torch.float32):
+            return torch.empty((n,) + shape, dtype=dtype, device=rows.device)
+
+        log_p, h = None if codes is None else one(), one() if entropy else None
+        lse, stats = one(), one(2)
+        best = (one(top), one(top, dtype=torch.int32)) if top else (None, None)
+        _rq.rvq_log_probs(rows, codes, temperature, log_p, h, lse, stats, *best)
+        ctx.save_for_backward(rows, codes, stats, h)
+        ctx.set_materialize_grads(False)
+        ctx.shape, ctx.temperature = logits.shape, temperature
+        out = tuple(None if t is None else t.view(lead + t.shape[1:]) for t in (log_p, h, lse, *best))
+        ctx.mark_non_differentiable(*(t for t in out[3:] if t is not None))
+        return out
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad_log_probs, grad_entropy, grad_lse, *_):
+        rows, codes, stats, entropy = ctx.saved_tensors
+        grads = [None if g is None else g.to(torch.float32).reshape(-1).contiguous()
+                 for g in (grad_log_probs, grad_entropy, grad_lse)]
+        dlogits = torch.empty(rows.shape, dtype=rows.dtype, device=rows.device)
+        _rq.rvq_log_probs_backward(*grads, rows, codes, ctx.temperature, stats, entropy, dlogits)
+        return dlogits.view(ctx.shape), None, None, None, None
+
+
+def log_probs(logits: torch.Tensor, codes: Optional[torch.Tensor] = None, entropy: bool = False, top: int = 0,
+              temperature: float = 1.0) -> LogProbs:
+    """Log probabilities of codes [...] (integers; -1: none, 0 then) under softmax(logits [...][vocab] / temperature),
+    the distributions' entropy where asked for, their log sum exp, and the `top` best codes (at most 64) with their log
+    probabilities.  Differentiable in logits through log_probs, entropy and lse; top_log_probs are constants.
+
+    The lists are a teacher's for distill_loss: at the same temperature T,
+    distill_loss(student, T * top_log_probs, top_codes, torch.zeros_like(lse), temperature=T).  Runs on the current
+    stream."""
+    return LogProbs(*_LogProbs.apply(logits, codes, bool(entropy), int(top), float(temperature)))
+
+
+def _int32(codes: torch.Tensor) -> torch.Tensor:
+    if codes.dtype != torch.int32:  # a code past 32 bits stays out of range
+        codes = codes.to(torch.int64).clamp(-2, 2 ** 31 - 1).to(torch.int32)
+    return codes
+
+
 def _teacher(logits, top_logits, top_codes, teacher_lse, weights):
     """The loss's arguments as rows."""
     vocab, top = logits.shape[-1], top_logits.shape[-1]
@@ -186,8 +248,7 @@ def _teacher(logits, top_logits, top_codes, teacher_lse, weights):
                 raise ValueError(f"{name} must have the logits' leading axes")
             t = t.to(torch.float32).reshape(-1).contiguous()
         flat.append(t)
-    if top_codes.dtype != torch.int32:  # a code past 32 bits stays out of range
-        top_codes = top_codes.to(torch.int64).clamp(-2, 2 ** 31 - 1).to(torch.int32)
+    top_codes = _int32(top_codes)
     return rows, (top_logits.reshape(-1, top).contiguous(), top_codes.reshape(-1, top).contiguous(), *flat)
 
 

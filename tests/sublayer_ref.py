@@ -135,3 +135,63 @@ def check_8bit(q, scales, y, tol, block, powers):
         assert bool((grid[at] == t).all())
         off = (y[:, a:b] / s[:, i:i + 1] - got[:, a:b]).abs()
         assert bool((off <= step[at] / 2 + 4 * U * t + tol[:, a:b] / s[:, i:i + 1]).all())
+
+
+# ---------------------------------------------------------------------------
+# log probabilities
+# ---------------------------------------------------------------------------
+
+def log_probs(logits, codes, temperature, top=0, grads=(None, None, None)):
+    """({name: value}, {name: inner tolerance}) of log_probs, entropy, lse, top_log_probs, top_codes and, with the
+    gradients of the first three, dlogits; on the CPU.
+
+    z / T is a difference from the largest logit, rounded before and after its product with 1 / T (a float32 itself):
+    4 roundings of |z - m| / T in all, which are a relative error of each exponential, with 2 units of the exponential
+    itself; the sums' paths and what else is done are STEPS roundings of what is added."""
+    z, inv = logits.double().cpu(), 1.0 / temperature
+    rows, vocab = z.shape
+    m = z.amax(1, keepdim=True)
+    m = torch.where(torch.isinf(m), 0.0, m)
+    d = (z - m) * inv
+    lse0 = torch.logsumexp(d, 1, keepdim=True)
+    alive = torch.isfinite(lse0)
+    lp = torch.where(alive, d - lse0, -torch.inf)
+    p = lp.exp()
+    near = torch.where(p > 0, d.abs(), 0.0)
+    rel = STEPS * U + 4 * U * (p * near).sum(1, keepdim=True)       # of a sum of exponentials
+    off = 4 * U * near + rel + 4 * U * lse0.abs().nan_to_num(0.0, 0.0, 0.0)
+    entropy = -torch.where(p > 0, p * lp, 0.0).sum(1, keepdim=True)
+    # H = ln S - sum p d: its terms' sizes, each with the relative errors above
+    size = (p * near).sum(1, keepdim=True)
+    h_off = 2 * (STEPS * U + rel) * (1 + size) + 4 * U * (p * near * near).sum(1, keepdim=True)
+    c = codes.cpu().long()
+    there = (c >= 0) & (c < vocab)
+    at = torch.where(there, c, 0)[:, None]
+    val = {"log_probs": torch.where(there, lp.gather(1, at)[:, 0], 0.0), "entropy": entropy[:, 0],
+           "lse": torch.where(alive, m * inv + lse0, -torch.inf)[:, 0]}
+    at_off = 4 * U * (z.gather(1, at) - m).abs().nan_to_num(0.0, 0.0, 0.0) * inv + off.amin(1, keepdim=True)
+    tol = {"log_probs": at_off[:, 0], "entropy": h_off[:, 0],
+           "lse": (rel + 4 * U * ((m * inv).abs() + lse0.abs().nan_to_num(0.0, 0.0, 0.0)))[:, 0]}
+    if top:
+        order = torch.sort(z, 1, descending=True, stable=True)
+        best, place = order.values[:, :top], order.indices[:, :top]
+        real = best > -torch.inf
+        fill = top - best.shape[1]
+        val["top_codes"] = torch.nn.functional.pad(torch.where(real, place, -1), (0, max(0, fill)), value=-1)
+        val["top_log_probs"] = torch.nn.functional.pad(torch.where(real, lp.gather(1, place), -torch.inf),
+                                                       (0, max(0, fill)), value=-torch.inf)
+        reach = torch.where(real, (best - m).abs() * inv, 0.0)
+        tol["top_log_probs"] = torch.nn.functional.pad(4 * U * reach + off.amin(1, keepdim=True), (0, max(0, fill)))
+    if any(g is not None for g in grads):
+        gp, gh, gl = (torch.zeros(rows, 1, dtype=torch.float64) if g is None else g.double().cpu()[:, None] for g in grads)
+        gp = torch.where(there[:, None], gp, 0.0)
+        dead = ~alive | ((gp == 0) & (gh == 0) & (gl == 0))
+        lp0 = torch.where(p > 0, lp, 0.0)
+        one = torch.zeros_like(z).scatter_(1, at, 1.0)
+        grad = gp * (one - p) + gl * p - gh * p * (lp0 + entropy)
+        val["dlogits"] = torch.where(dead, 0.0, grad * inv)
+        e_rel = 4 * U * near + rel
+        size = p * (gp.abs() + gl.abs() + gh.abs() * (lp0.abs() + entropy))
+        inner = size * (e_rel + STEPS * U) + gh.abs() * p * (off + h_off) + 4 * U * one * gp.abs()
+        tol["dlogits"] = torch.where(dead, 0.0, inner * inv)
+    return val, tol

@@ -149,3 +149,109 @@ def test_rms_norm_backward_refusals(lib):
                dict(dr=7 * AT + need - 128), dict(dx=8 * AT, m=mask(step=8 * AT))):
         assert back(**kw) == INVALID, kw
     assert back(dr=None, dw=None, ws=None, nb=0) == 0                  # nothing asked for
+
+
+def test_log_probs_refusals(lib):
+    ok = (4, 100, 0, 2, 1.0)
+
+    def run(dims=ok, z=AT, zs=100, c=2 * AT, lp=3 * AT, h=None, lse=None, st=None, tl=None, tc=None, bad=None):
+        return lib.rvq_log_probs(rq.rvq_log_probs_dims(*dims), ptr(z), zs, ptr(c), ptr(lp), ptr(h), ptr(lse), ptr(st), ptr(tl),
+                                 ptr(tc), ptr(bad), None)
+
+    for dims in ((-1, 100, 0, 2, 1.0), (4, 0, 0, 2, 1.0), (4, 100, -1, 2, 1.0), (4, 100, 0, 5, 1.0), (4, 100, 0, 2, 0.0),
+                 (4, 100, 0, 2, -1.0), (4, 100, 0, 2, float("nan")), (4, 100, 0, 2, float("inf")), (4, 100, 0, 2, 1e-39)):
+        assert run(dims) == INVALID, dims
+    assert run((4, (1 << 20) + 1, 0, 2, 1.0), zs=1 << 21) == UNSUPPORTED
+    assert run((4, 100, 65, 2, 1.0), tl=5 * AT, tc=6 * AT) == UNSUPPORTED
+    top = dict(dims=(4, 100, 3, 2, 1.0), tl=5 * AT, tc=6 * AT)
+    for kw in (dict(z=None), dict(z=AT + 1), dict(zs=99), dict(c=None), dict(lp=None), dict(c=None, lp=None), dict(c=AT + 2),
+               dict(lp=3 * AT + 2), dict(h=AT + 2), dict(lse=AT + 2), dict(st=AT + 2), dict(bad=7 * AT + 4), dict(tl=5 * AT),
+               dict(tc=5 * AT), dict(top, tl=None), dict(top, tc=None), dict(top, tl=5 * AT + 2), dict(top, tc=5 * AT + 2),
+               # overlaps
+               dict(lp=AT), dict(lp=AT + 796), dict(lp=2 * AT + 12), dict(h=3 * AT + 4), dict(lse=3 * AT - 12),
+               dict(st=3 * AT - 28), dict(top, tc=5 * AT + 44), dict(top, tl=3 * AT - 44), dict(bad=3 * AT + 8), dict(bad=AT)):
+        assert run(**kw) == INVALID, kw
+    assert run((0, 100, 0, 2, 1.0), z=None, c=None, lp=None) == 0
+
+
+def test_log_probs_backward_refusals(lib):
+    def run(dims=(4, 100, 0, 2, 1.0), g=2 * AT, gh=None, gl=None, z=AT, zs=100, c=3 * AT, st=4 * AT, h=None, d=5 * AT, ds=100):
+        return lib.rvq_log_probs_backward(rq.rvq_log_probs_dims(*dims), ptr(g), ptr(gh), ptr(gl), ptr(z), zs, ptr(c), ptr(st),
+                                          ptr(h), ptr(d), ds, None)
+
+    for kw in (dict(z=None), dict(st=None), dict(d=None), dict(c=None), dict(gh=6 * AT), dict(zs=99), dict(ds=99),
+               dict(d=5 * AT + 1), dict(g=AT + 2), dict(gh=AT + 2, h=7 * AT), dict(gl=AT + 2), dict(st=AT + 2),
+               dict(d=AT + 2), dict(d=AT, ds=101), dict(d=AT - 200), dict(d=2 * AT), dict(d=3 * AT), dict(d=4 * AT - 790),
+               dict(gl=6 * AT, d=6 * AT), dict(gh=6 * AT, h=7 * AT, d=7 * AT)):
+        assert run(**kw) == INVALID, kw
+    assert run((0, 100, 0, 2, 1.0), z=None, st=None, d=None, c=None, g=None) == 0
+
+
+# ---------------------------------------------------------------------------
+# the device of a call
+# ---------------------------------------------------------------------------
+
+from test_predictor_edges_cpu import F32, I32, U8, OnGpu, Stream, gpus, kernels  # noqa: E402, F401
+
+
+def operators(t):
+    rows, one, w = (lambda: t(4, 8)), (lambda: t(4)), (lambda: t(8))
+    step = lambda: t(1, dtype=torch.int64)  # noqa: E731
+
+    def masked(call):
+        """The mask's step is one of the tensors (a mask takes those that are on a GPU)."""
+        def run(*tensors, **kw):
+            m = rq.rvq_dropout_mask(0.1, 1)
+            m.tensor = tensors[-1]
+            return call(*tensors[:-1], m, **kw)
+        return run
+
+    return {
+        "rvq_dropout": (masked(lambda x, y, r, m, **kw: rq.rvq_dropout(x, m, y, r, **kw)), [rows(), rows(), rows(), step()]),
+        "rvq_rms_norm": (masked(lambda x, w, y, s, r, t, q, sc, m, **kw: rq.rvq_rms_norm(
+            x, w, 1e-6, y, s, r, m, t, q, sc, 32, **kw)),
+            [rows(), w(), rows(), one(), rows(), rows(), t(4, 8, dtype=torch.float8_e4m3fn), t(4, 1), step()]),
+        "rvq_rms_norm_backward": (masked(lambda dy, t, w, s, dr, dw, ws, dt, dx, m, **kw: rq.rvq_rms_norm_backward(
+            dy, t, w, s, dr, dw, ws, dt, m, dx, **kw)),
+            [rows(), rows(), w(), one(), rows(), w(), t(64, dtype=U8), rows(), rows(), step()]),
+        "rvq_log_probs": (lambda z, c, *out, **kw: rq.rvq_log_probs(z, c, 1.0, *out, **kw),
+                          [rows(), t(4, dtype=I32), one(), one(), one(), t(4, 2), t(4, 3), t(4, 3, dtype=I32), step()]),
+        "rvq_log_probs_backward": (lambda a, b, c, z, codes, s, h, d, **kw: rq.rvq_log_probs_backward(
+            a, b, c, z, codes, 1.0, s, h, d, **kw),
+            [one(), one(), one(), rows(), t(4, dtype=I32), t(4, 2), one(), rows()]),
+    }
+
+
+NAMES = sorted(operators(lambda *shape, dtype=F32: None))
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_calls_run_on_their_tensors_device(name, gpus):  # noqa: F811
+    for index in (0, 1):
+        call, tensors = operators(lambda *shape, dtype=F32: OnGpu(index, *shape, dtype=dtype))[name]
+        call(*tensors)
+        assert gpus.pop() == (name, index, 100 + index)
+        call(*tensors, stream=Stream(index, 7))
+        assert gpus.pop() == (name, index, 7)
+        with pytest.raises(ValueError):
+            call(*tensors, stream=Stream(1 - index, 7))
+    assert not gpus
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_calls_refuse_tensors_of_two_devices(name, gpus):  # noqa: F811
+    call, tensors = operators(lambda *shape, dtype=F32: OnGpu(0, *shape, dtype=dtype))[name]
+    for i, t in enumerate(tensors):
+        for other in (OnGpu(1, *t.shape, dtype=t.dtype), t.t):
+            with pytest.raises(ValueError):
+                call(*tensors[:i], other, *tensors[i + 1:])
+    assert not gpus
+
+
+@pytest.mark.parametrize("name", ["rvq_rms_backward.cu"])
+def test_overlapping_kernels_take_no_read_only_pointers(name):
+    """As for the other kernels that start while the one before them runs."""
+    waiting = [(kernel, parameters, body) for kernel, parameters, body in kernels(name) if "griddep_wait" in body]
+    assert waiting
+    for kernel, parameters, body in waiting:
+        assert "__restrict__" not in parameters and "__ldg(" not in body, kernel
