@@ -406,16 +406,17 @@ cudaError_t launch_cluster(void (*kernel)(P...), int64_t rows, int cs, int block
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// Blocks of a row: as many as the SMs have room for, each with `least` vectors a thread at least.
-inline int cluster_size(int64_t rows, int full, int threads, int least) {
-  int cs = 1;
-  while (cs < kMaxCluster && rows * cs * 2 <= 152 && full >= cs * 2 * threads * least) cs *= 2;
-  return cs;
-}
-inline int block_threads(int full, int each) {  // at most 512, `each` vectors a thread
-  int threads = 64;
-  while (threads < 32 * kMaxWarps && threads * each < full) threads *= 2;
-  return threads;
+// How a row of `full` vectors lies: over a cluster of blocks where there are
+// fewer rows than SMs, each with two warps of `each` vectors a lane at least; over
+// at most 512 threads of a block.
+struct RowPlan {
+  int blocks, threads;
+};
+inline RowPlan row_plan(int64_t rows, int full, int each) {
+  int cs = 1, threads = 64;
+  while (cs < kMaxCluster && rows * cs * 2 <= 152 && full >= cs * 2 * 64 * each) cs *= 2;
+  while (threads < 32 * kMaxWarps && cs * threads * each < full) threads *= 2;
+  return {cs, threads};
 }
 
 template <class T, int NV>
@@ -447,17 +448,17 @@ cudaError_t launch_forward(const LogProbsArgs &a, cudaStream_t st) {
   }
   if (a.dm.top) {
     constexpr int kEach = 8;
-    const int threads = block_threads(full, kEach), cs = cluster_size(a.dm.rows, full, threads, kEach);
-    const size_t smem = sizeof(ListRoom) + threads / 32 * sizeof(WarpRoom);
+    const RowPlan p = row_plan(a.dm.rows, full, kEach);
+    const size_t smem = sizeof(ListRoom) + p.threads / 32 * sizeof(WarpRoom);
     const auto kernel = k_log_probs_row_top<T, kEach>;
     static std::atomic<bool> allowed[64];
     const cudaError_t e = allow_smem(kernel, allowed);
     if (e != cudaSuccess) return e;
-    return launch_cluster(kernel, a.dm.rows, cs, threads, smem, st, a, cs);
+    return launch_cluster(kernel, a.dm.rows, p.blocks, p.threads, smem, st, a, p.blocks);
   }
-  const int threads = block_threads(full, 4), cs = cluster_size(a.dm.rows, full, threads, 4);
-  return a.entropy ? launch_cluster(k_log_probs_row<T, true>, a.dm.rows, cs, threads, 0, st, a, cs)
-                   : launch_cluster(k_log_probs_row<T, false>, a.dm.rows, cs, threads, 0, st, a, cs);
+  const RowPlan p = row_plan(a.dm.rows, full, 4);
+  return launch_cluster(a.entropy ? k_log_probs_row<T, true> : k_log_probs_row<T, false>, a.dm.rows, p.blocks, p.threads, 0,
+                        st, a, p.blocks);
 }
 
 template <class T>

@@ -76,27 +76,34 @@ __device__ __forceinline__ void warp_pieces(const CutRow<T> &in, int first, int 
     }
     const int edge_at = p == 0 ? in.edge(lane) : -1;
     const float edge = edge_at >= 0 ? to_float(in.z[edge_at]) + add : -CUDART_INF_F;
-    // each vector's largest, and the largest of each half of the lane's elements (z + add: add is 0 where the sum
+    // each vector's largest, and the largest of each quarter of the lane's elements (z + add: add is 0 where the sum
     // is wanted).  Once the sum is taken the vectors are done with: the few that hold an entry worth ordering are
     // read again, by their lanes at the same time.
-    float most[NV], half[2] = {-CUDART_INF_F, -CUDART_INF_F};
+    float most[NV], part[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       most[j] = largest_of<T>(z[j]) + add;
-      half[j >= NV / 2] = fmaxf(half[j >= NV / 2], most[j]);
+      part[j * 4 / NV] = fmaxf(part[j * 4 / NV], most[j]);
     }
-    half[0] = fmaxf(half[0], edge);
-    const float high = fmaxf(half[0], half[1]);
+    part[0] = fmaxf(part[0], edge);
+    const float half[2] = {fmaxf(part[0], part[1]), fmaxf(part[2], part[3])}, high = fmaxf(half[0], half[1]);
     sum(z, edge, high);
     const uint64_t last = held ? r.best[n - 1] : 0;  // an entry counts if it is above this
     const uint32_t last_value = (uint32_t)(last >> 32);
     if (!__any_sync(0xffffffffu, order_of(high) > 0 && order_of(high) >= last_value)) continue;
+    // n entries reach the bar: the n-th of the lanes' largest, or, for more, half as far down among the largest of
+    // their halves, or a quarter among those of their quarters.  (The 32nd of 32 is a low one: it let through more
+    // than there is room for, and 6 rows of 65536 f16 with 32 kept took 338 us.)
     uint32_t bar;
-    if (n <= 32) {
+    if (n <= 16) {
       bar = warp_nth(order_of(high), n);
-    } else {
+    } else if (n <= 32) {
       const int at = (n + 1) / 2;
       bar = min(warp_nth(order_of(half[0]), at), warp_nth(order_of(half[1]), at));
+    } else {
+      bar = 0xffffffffu;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) bar = min(bar, warp_nth(order_of(part[i]), (n + 3) / 4));
     }
     bar = max(bar, last_value);
     const float line = bar ? value_of(bar) : -3.402823466e38f;

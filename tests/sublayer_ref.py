@@ -173,7 +173,7 @@ def log_probs(logits, codes, temperature, top=0, grads=(None, None, None)):
     tol = {"log_probs": at_off[:, 0], "entropy": h_off[:, 0],
            "lse": (rel + 4 * U * ((m * inv).abs() + lse0.abs().nan_to_num(0.0, 0.0, 0.0)))[:, 0]}
     if top:
-        order = torch.sort(z, 1, descending=True, stable=True)
+        order = torch.sort(z, stable=True, dim=1, descending=True)
         best, place = order.values[:, :top], order.indices[:, :top]
         real = best > -torch.inf
         fill = top - best.shape[1]
