@@ -23,7 +23,7 @@ constexpr int kThreads = 256;
 template <class T>
 __global__ void __launch_bounds__(kThreads) k_dropout(const DropoutArgs a) {
   constexpr int N = 16 / (int)sizeof(T), V = 8 / N;
-  const Keep keep(a.mask);
+  const Dropped drop(a.mask);
   const int64_t each = a.width / 8, groups = a.rows * each;
   for (int64_t g = blockIdx.x * (int64_t)kThreads + threadIdx.x; g < groups; g += (int64_t)gridDim.x * kThreads) {
     const int64_t row = a.rows == 1 ? 0 : g / each, col = (g - row * each) * 8;
@@ -36,7 +36,7 @@ __global__ void __launch_bounds__(kThreads) k_dropout(const DropoutArgs a) {
       add[v] = a.residual ? reinterpret_cast<const uint4 *>(static_cast<const T *>(a.residual) + row * a.rs + col)[v]
                           : make_uint4(0, 0, 0, 0);
     }
-    const uint32_t bits = keep.group((uint64_t)g);
+    const uint32_t bits = drop.group((uint64_t)g);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       float f[N], r[N];
@@ -44,7 +44,7 @@ __global__ void __launch_bounds__(kThreads) k_dropout(const DropoutArgs a) {
       unpack16<T>(add[v], r);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        f[i] = bits >> (v * N + i) & 1 ? __fmul_rn(f[i], keep.factor) : 0.f;
+        f[i] = Dropped::at(bits, v * N + i) ? 0.f : __fmul_rn(f[i], drop.factor);
         if (a.residual) f[i] = __fadd_rn(f[i], r[i]);
       }
       reinterpret_cast<uint4 *>(y)[v] = pack16<T>(f);
@@ -55,18 +55,18 @@ __global__ void __launch_bounds__(kThreads) k_dropout(const DropoutArgs a) {
 // Anything else: a warp takes 256 elements, 8 groups' masks in its lanes' bits.
 template <class T>
 __global__ void __launch_bounds__(kThreads) k_dropout_elements(const DropoutArgs a) {
-  const Keep keep(a.mask);
+  const Dropped drop(a.mask);
   const int lane = threadIdx.x & 31;
   const int64_t all = a.rows * a.width, warps = (int64_t)gridDim.x * (kThreads / 32);
   for (int64_t e0 = (blockIdx.x * (int64_t)(kThreads / 32) + (threadIdx.x >> 5)) * 256; e0 < all; e0 += warps * 256) {
-    const uint32_t bits = keep.group((uint64_t)(e0 / 8 + lane));
+    const uint32_t bits = drop.group((uint64_t)(e0 / 8 + lane));
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int64_t e = e0 + i * 32 + lane;
-      const bool stays = __shfl_sync(0xffffffffu, bits, i * 4 + lane / 8) >> (lane & 7) & 1;
+      const bool gone = Dropped::at(__shfl_sync(0xffffffffu, bits, i * 4 + lane / 8), lane & 7);
       if (e >= all) continue;
       const int64_t row = e / a.width, col = e - row * a.width;
-      float f = stays ? __fmul_rn(to_float(static_cast<const T *>(a.x)[row * a.xs + col]), keep.factor) : 0.f;
+      float f = gone ? 0.f : __fmul_rn(to_float(static_cast<const T *>(a.x)[row * a.xs + col]), drop.factor);
       if (a.residual) f = __fadd_rn(f, to_float(static_cast<const T *>(a.residual)[row * a.rs + col]));
       static_cast<T *>(a.y)[row * a.ys + col] = from_float<T>(f);
     }

@@ -29,16 +29,25 @@ inline bool dropout_mask(const rvq_dropout_mask &m, DropoutMask &out) {
   return true;
 }
 
-// The mask of one launch, its call's counter read.
-struct Keep {
-  uint32_t k0, k1, u0, u1, drop;
+// The mask of one launch, its call's counter read.  What is dropped of 8 elements
+// comes as one bit each, the even ones' in the lower half of a word and the odd
+// ones' in the upper: a pair is compared at once, by 16-bit maxima.
+struct Dropped {
+  uint32_t k0, k1, u0, u1, limit, all;
   float factor;
-  __device__ __forceinline__ explicit Keep(const DropoutMask &m)
-      : k0((uint32_t)m.seed), k1((uint32_t)(m.seed >> 32)), drop(m.drop), factor(m.factor) {
+  __device__ __forceinline__ explicit Dropped(const DropoutMask &m)
+      : k0((uint32_t)m.seed), k1((uint32_t)(m.seed >> 32)), limit((m.drop & 0xffffu) * 0x10001u),
+        all(m.drop > 0xffffu ? 0x000f000fu : 0u), factor(m.factor) {
     const uint64_t upper = m.offset + (m.step ? (uint64_t)*m.step << 32 : 0);
     u0 = (uint32_t)upper, u1 = (uint32_t)(upper >> 32);
   }
-  // Bit i: whether element 8 * group + i stays.
+  static __device__ __forceinline__ uint32_t below(uint32_t w, uint32_t limit) {  // of each half: 1 where w < limit
+    uint32_t m, d;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(m) : "r"(w), "r"(limit));
+    asm("min.u16x2 %0, %1, %2;" : "=r"(d) : "r"(m ^ w), "r"(0x00010001u));
+    return d;
+  }
+  // Of group g: bit i: element 2 i, bit 16 + i: element 2 i + 1 (i < 4).
   __device__ __forceinline__ uint32_t group(uint64_t g) const {
     uint32_t a = (uint32_t)g, b = (uint32_t)(g >> 32), c = u0, d = u1, x = k0, y = k1;
 #pragma unroll
@@ -48,20 +57,19 @@ struct Keep {
       c = (uint32_t)(p >> 32) ^ d ^ y, d = (uint32_t)p;
       x += 0x9E3779B9u, y += 0xBB67AE85u;
     }
-    const uint32_t w[4] = {a, b, c, d};
-    uint32_t bits = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      bits |= (uint32_t)((w[i] & 0xffffu) >= drop) << (2 * i) | (uint32_t)((w[i] >> 16) >= drop) << (2 * i + 1);
-    return bits;
+    return below(a, limit) + below(b, limit) * 2 + below(c, limit) * 4 + below(d, limit) * 8 | all;
   }
-  // Bit i (i < N <= 8): whether element e + i stays (the bits above mean nothing).
+  // Whether element i of the 8 that `bits` is of is dropped.
+  static __device__ __forceinline__ bool at(uint32_t bits, int i) { return bits >> (i / 2 + (i & 1) * 16) & 1; }
+  __device__ __forceinline__ bool element(uint64_t e) const { return at(group(e >> 3), (int)(e & 7)); }
+  // In the same form, elements e to e + N - 1 (N 4 or 8).
   template <int N>
   __device__ __forceinline__ uint32_t from(uint64_t e) const {
-    const int at = (int)(e & 7);
-    uint32_t bits = group(e >> 3) >> at;
-    if (at + N > 8) bits |= group((e >> 3) + 1) << (8 - at);
-    return bits;
+    const int i = (int)(e & 7);
+    uint32_t w = group(e >> 3);
+    if (i + N > 8) w |= group((e >> 3) + 1) << 4;
+    if (i & 1) w = w >> 16 | (w & 0xffffu) >> 1 << 16;  // the odd ones become the even ones
+    return w >> (i / 2) & (N == 8 ? 0x000f000fu : 0x00030003u);
   }
 };
 

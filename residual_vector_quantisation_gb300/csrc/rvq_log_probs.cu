@@ -356,21 +356,29 @@ __global__ void __launch_bounds__(32 * kBackWarps) k_log_probs_backward(const Lo
   const bool zero = (g == 0.f && gh == 0.f && gl == 0.f) || s == 0.f;
   const float scale = __fdividef(a.inv_t, s), at_code = zero ? 0.f : g * a.inv_t;
   const float k0 = (gl - g - (ENT ? gh * (entropy - logf(s)) : 0.f)) * scale, k1 = -gh * kLn2 * scale;
-  auto grad = [&](float z) {
-    float y = (z - m) * a.c;
-    if constexpr (ENT) y = max_nan(y, kLowest);
-    const float e = exp2_fast(y);
-    return zero ? 0.f : ENT ? e * fmaf(k1, y, k0) : e * k0;
+  const F2 minus = f2(-m, -m), c2 = f2(a.c, a.c), k0s = f2(k0, k0), k1s = f2(k1, k1);
+  auto grad = [&](F2 z) {
+    const F2 p = (z + minus) * c2;
+    float2 y = floats(p);
+    if constexpr (ENT) y.x = max_nan(y.x, kLowest), y.y = max_nan(y.y, kLowest);
+    const F2 e = f2(exp2_fast(y.x), exp2_fast(y.y));
+    return ENT ? e * fma2(k1s, f2(y.x, y.y), k0s) : e * k0s;
   };
   const bool same = ((reinterpret_cast<uintptr_t>(r.z) ^ reinterpret_cast<uintptr_t>(d)) & 15) == 0;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int v = v0 + j * 32;
     if (v >= r.full) continue;
-    float f[N];
-    unpack16<T>(raw[j], f);
+    float f[N] = {};
+    if (!zero) {
+      F2 z[N / 2];
+      unpack_pairs<T>(raw[j], z);
 #pragma unroll
-    for (int i = 0; i < N; ++i) f[i] = grad(f[i]);
+      for (int i = 0; i < N / 2; ++i) {
+        const float2 g2 = floats(grad(z[i]));
+        f[2 * i] = g2.x, f[2 * i + 1] = g2.y;
+      }
+    }
     const int first = r.head + v * N;
     if (code >= first && code < first + N)
 #pragma unroll
@@ -383,7 +391,8 @@ __global__ void __launch_bounds__(32 * kBackWarps) k_log_probs_backward(const Lo
       for (int i = 0; i < N; ++i) d[first + i] = from_float<T>(f[i]);
     }
   }
-  if (edge_at >= 0) d[edge_at] = from_float<T>(grad(edge) + (edge_at == code ? at_code : 0.f));
+  if (edge_at >= 0)
+    d[edge_at] = from_float<T>((zero ? 0.f : floats(grad(f2(edge, edge))).x) + (edge_at == code ? at_code : 0.f));
 }
 
 // ---------------------------------------------------------------------------

@@ -14,8 +14,8 @@ namespace rvq {
 namespace {
 
 // A scale from the bits of a block's largest magnitude (NaN is above infinity),
-// and its inverse: max / 448, at least 2^-126, so that a block of zeros has a
-// scale and every scale an inverse; or the next power of two, read off the bits:
+// and its inverse: max / 448 (a product), at least 2^-126, so that a block of zeros
+// has a scale and every scale an inverse; or the next power of two, read off the bits:
 // 448 is 1.75 * 2^8.
 struct Scale {
   float value, inverse;
@@ -27,15 +27,21 @@ __device__ __forceinline__ Scale scale_of(uint32_t most, bool power) {
     int e = (int)(most >> 23) - 8 + ((most & 0x7fffffu) > 0x600000u);
     e = most >= 0x7f800000u ? 255 : e < 1 ? 1 : e;  // infinity has no scale of this kind
     s.exponent = (uint8_t)e;
-    s.value = e == 255 ? CUDART_NAN_F : __uint_as_float((uint32_t)e << 23);
+    s.value = 0.f;
     s.inverse = e == 255 ? CUDART_NAN_F : __uint_as_float((uint32_t)(254 - e) << 23);  // 1 <= e <= 247
   } else {
-    s.value = __fdiv_rn(__uint_as_float(most), 448.f);
+    s.value = __uint_as_float(most) * (1.f / 448.f);
     if (s.value < 1.17549435e-38f) s.value = 1.17549435e-38f;
-    s.inverse = __frcp_rn(s.value);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.inverse) : "f"(s.value));  // (to a unit in the last place)
     s.exponent = 0;
   }
   return s;
+}
+// The larger of m and the magnitudes of a and b, NaN where one is NaN.
+__device__ __forceinline__ float most3(float m, float a, float b) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(a), "f"(b));
+  return r;
 }
 __device__ __forceinline__ void put_scale(const RmsArgs &a, int64_t row, int at, const Scale &s) {
   const int64_t i = row * a.scale_count + at;
@@ -84,7 +90,7 @@ __device__ __forceinline__ void group_barrier(int group, int tpr) {
 // keeps its columns' weights in registers.  All tensors of T start equally far
 // from a 16-byte boundary in each row.
 template <class T, int C, int LANES, int STAGES, bool DROP>
-__global__ void __launch_bounds__(kRmsThreads) k_rms_ring(const RmsArgs a, const int tpr_) {
+__global__ void __launch_bounds__(rms_threads<T>()) k_rms_ring(const RmsArgs a, const int tpr_) {
   constexpr int N = 16 / (int)sizeof(T), NV = C / N;
   extern __shared__ uint4 ring[];
   __shared__ float box[2 * kRmsThreads / 32][1][16];
@@ -121,7 +127,7 @@ __global__ void __launch_bounds__(kRmsThreads) k_rms_ring(const RmsArgs a, const
     return p && c.edge >= 0 && row < rows ? to_float(p[row * stride + c.edge]) : 0.f;
   };
   float e_next = edge_of(x, a.xs, first), re_next = edge_of(res, a.rs, first);
-  const Keep keep(a.mask);
+  const Dropped dropped(a.mask);
   int turn = 0, stage = 0;
   // the groups of a warp stay together: what a row past the end computes is stored nowhere
   constexpr int kPerWarp = LANES ? 32 / (LANES ? LANES : 32) : 1;
@@ -134,14 +140,19 @@ __global__ void __launch_bounds__(kRmsThreads) k_rms_ring(const RmsArgs a, const
     e_next = edge_of(x, a.xs, row + step), re_next = edge_of(res, a.rs, row + step);
     copies_wait<STAGES - 1>();
     const uint4 *xv = slot + stage * arrays * NV * blockDim.x, *rv = xv + NV * blockDim.x;
+    uint32_t gone = 0;  // of all the thread's vectors
+    if constexpr (DROP) {
+#pragma unroll 2
+      for (int j = 0; j < NV; ++j) gone |= dropped.from<N>((uint64_t)(row * width + c.column(j))) << (j * N / 2);
+    }
     float f[NV][N], s[1] = {0.f};
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       unpack16<T>(xv[j * blockDim.x], f[j]);
       if constexpr (DROP) {
-        const uint32_t bits = keep.from<N>((uint64_t)(row * width + c.column(j)));
 #pragma unroll
-        for (int i = 0; i < N; ++i) f[j][i] = bits >> i & 1 ? __fmul_rn(f[j][i], keep.factor) : 0.f;
+        for (int i = 0; i < N; ++i)
+          f[j][i] = Dropped::at(gone >> (j * N / 2), i) ? 0.f : __fmul_rn(f[j][i], dropped.factor);
       }
       if (two) {
         float r[N];
@@ -161,7 +172,7 @@ __global__ void __launch_bounds__(kRmsThreads) k_rms_ring(const RmsArgs a, const
       if (c.has(j)) s[0] += q;
     }
     if (c.edge >= 0) {
-      if constexpr (DROP) e = keep.from<1>((uint64_t)(row * width + c.edge)) & 1 ? __fmul_rn(e, keep.factor) : 0.f;
+      if constexpr (DROP) e = dropped.element((uint64_t)(row * width + c.edge)) ? 0.f : __fmul_rn(e, dropped.factor);
       if (two) e = __fadd_rn(e, re);
       if (two || DROP) {
         const T sum = from_float<T>(e);
@@ -215,17 +226,23 @@ __global__ void __launch_bounds__(kRmsThreads) k_rms_ring(const RmsArgs a, const
     auto put_edge = [&](float inverse) {
       if (c.edge >= 0 && there) q[c.edge] = (uint8_t)two_e4m3(e * inverse, 0.f);
     };
+    auto most_all = [&](int j) {
+      float m = 0.f;
+#pragma unroll
+      for (int i = 0; i < N; i += 2) m = most3(m, f[j][i], f[j][i + 1]);
+      return c.has(j) ? __float_as_uint(m) : 0u;
+    };
     auto most_of = [&](int j, int from, int to) {
       uint32_t m = 0;
 #pragma unroll
       for (int i = 0; i < N; ++i)
-        if (c.has(j) && i >= from && i < to) m = max(m, __float_as_uint(f[j][i]) & 0x7fffffffu);
+        if (i >= from && i < to) m = max(m, __float_as_uint(f[j][i]) & 0x7fffffffu);
       return m;
     };
     if (a.block == 0) {
       uint32_t m = c.edge >= 0 ? __float_as_uint(e) & 0x7fffffffu : 0u;
 #pragma unroll
-      for (int j = 0; j < NV; ++j) m = max(m, most_of(j, 0, N));
+      for (int j = 0; j < NV; ++j) m = max(m, most_all(j));
       const Scale sc = scale_of(group_max<LANES>(m, high, group, tpr), power);
       if (c.t == 0 && there) put_scale(a, row, 0, sc);
 #pragma unroll
@@ -236,7 +253,7 @@ __global__ void __launch_bounds__(kRmsThreads) k_rms_ring(const RmsArgs a, const
       const int lanes = a.block / N;
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        uint32_t m = most_of(j, 0, N);
+        uint32_t m = most_all(j);
         for (int o = lanes / 2; o; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
         const Scale sc = scale_of(m, power);
         const int v = c.t + j * tpr;
@@ -305,7 +322,7 @@ __global__ void __launch_bounds__(WARP ? 32 * kAnyWarps : kAnyThreads)
   uint32_t *table = reinterpret_cast<uint32_t *>(sums + (WARP ? kAnyWarps : 1) * width) + team * a.scale_count;
   const T *x = static_cast<const T *>(a.x) + row * a.xs;
   const T *res = a.residual ? static_cast<const T *>(a.residual) + row * a.rs : nullptr;
-  const Keep keep(a.mask);
+  const Dropped dropped(a.mask);
   float s = 0.f;
   for (int c0 = warp * 256; c0 < width; c0 += warps * 256) {
     float f[8], r[8];
@@ -318,13 +335,13 @@ __global__ void __launch_bounds__(WARP ? 32 * kAnyWarps : kAnyThreads)
     if (drop) {
       const uint64_t e0 = (uint64_t)(row * width + c0);
       const int at = (int)(e0 & 7);
-      const uint32_t bits = keep.group((e0 >> 3) + lane), last = keep.group((e0 >> 3) + 32);
+      const uint32_t bits = dropped.group((e0 >> 3) + lane), last = dropped.group((e0 >> 3) + 32);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int e = at + i * 32 + lane;
         uint32_t b = __shfl_sync(0xffffffffu, bits, (e >> 3) & 31);
         if (e >= 256) b = last;
-        f[i] = b >> (e & 7) & 1 ? __fmul_rn(f[i], keep.factor) : 0.f;
+        f[i] = Dropped::at(b, e & 7) ? 0.f : __fmul_rn(f[i], dropped.factor);
       }
     }
 #pragma unroll
@@ -411,7 +428,7 @@ size_t rms_thread_bytes(const RmsArgs &a, int columns) {
 template <class T, int C, int LANES, bool DROP>
 cudaError_t launch_ring(const RmsArgs &a, const RmsShape &s, cudaStream_t st) {
   const size_t thread = rms_thread_bytes<T>(a, C);
-  const RmsGrid grid = rms_grid(a.dm.rows, s, thread);
+  const RmsGrid grid = rms_grid<T>(a.dm.rows, s, thread);
   const auto kernel = k_rms_ring<T, C, LANES, rms_stages<T>(), DROP>;
   static std::atomic<bool> allowed[64];
   const cudaError_t e = allow_smem(kernel, allowed);
@@ -452,7 +469,7 @@ cudaError_t launch_rms_typed(const RmsArgs &a, bool drop, cudaStream_t st) {
   const RmsShape s = rms_shape(a.dm.width, e, rows_aligned16(a.x, a.xs, rows, e) && a.dm.width % N == 0, a.q ? a.block / N : 8);
   auto alike = [&](const void *p, int64_t stride) { return rows_alike(p, stride, a.x, a.xs, rows, e); };
   if (!alike(a.residual, a.rs) || !alike(a.total, a.ts) || !alike(a.y, a.ys) ||
-      rms_thread_bytes<T>(a, s.columns) * s.threads > kMostSmem)
+      s.threads > rms_threads<T>() || rms_thread_bytes<T>(a, s.columns) * s.threads > kMostSmem)
     return launch_any<T>(a, drop, st);
   return drop ? launch_ring_shape<T, true>(a, s, st) : launch_ring_shape<T, false>(a, s, st);
 }

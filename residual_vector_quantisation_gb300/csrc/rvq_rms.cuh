@@ -38,7 +38,11 @@ __device__ __forceinline__ float weight_at(const RmsArgs &a, int c) {
                                            : to_float(static_cast<const T *>(a.weight)[c]);
 }
 
-constexpr int kRmsThreads = 512;  // of a block of the ring kernels, one on an SM (128 registers a thread)
+// Threads of a block of the ring kernels, one on an SM: 128 registers each, or 168 in 32 bits, whose slots leave no room
+// for more threads.
+constexpr int kRmsThreads = 512;
+template <class T>
+constexpr int rms_threads() { return sizeof(T) == 4 ? 384 : kRmsThreads; }
 
 // How a row lies in a ring kernel: over `threads`, `lanes` of a warp or (lanes 0)
 // whole warps, at most `columns` a thread.
@@ -70,8 +74,9 @@ struct RmsGrid {
   int groups;
   int64_t blocks;
 };
-inline RmsGrid rms_grid(int64_t rows, const RmsShape &s, size_t thread_bytes) {
-  int most = kRmsThreads / s.threads;
+template <class T>
+RmsGrid rms_grid(int64_t rows, const RmsShape &s, size_t thread_bytes) {
+  int most = rms_threads<T>() / s.threads;
   const int fit = (int)(kMostSmem / (thread_bytes * s.threads));
   most = most < fit ? most : fit;
   const int per_warp = s.lanes ? 32 / s.lanes : 1;

@@ -9,7 +9,7 @@ namespace {
 // Rows through a ring in shared memory, as in the forward pass: dresidual and dx
 // per row, and each block's sums of dy u over its rows into part[block][width].
 template <class T, int C, int LANES, int STAGES, bool DROP>
-__global__ void __launch_bounds__(kRmsThreads) k_rms_backward_ring(const RmsArgs a, const int tpr_) {
+__global__ void __launch_bounds__(rms_threads<T>()) k_rms_backward_ring(const RmsArgs a, const int tpr_) {
   constexpr int N = 16 / (int)sizeof(T), NV = C / N, H = N / 2;
   extern __shared__ uint4 ring[];
   __shared__ float box[2 * kRmsThreads / 32][1][16];
@@ -58,7 +58,7 @@ __global__ void __launch_bounds__(kRmsThreads) k_rms_backward_ring(const RmsArgs
     return p && c.edge >= 0 && row < rows ? to_float(p[row * stride + c.edge]) : 0.f;
   };
   float he_next = edge_of(hp, a.ts, first), de_next = edge_of(dp, a.dys, first), te_next = edge_of(tp, a.dts, first);
-  const Keep keep(a.mask);
+  const Dropped dropped(a.mask);
   int turn = 0, stage = 0;
   // the groups of a warp stay together
   constexpr int kPerWarp = LANES ? 32 / (LANES ? LANES : 32) : 1;
@@ -69,6 +69,14 @@ __global__ void __launch_bounds__(kRmsThreads) k_rms_backward_ring(const RmsArgs
     const float he = he_next, de = de_next, te = te_next;
     he_next = edge_of(hp, a.ts, row + step), de_next = edge_of(dp, a.dys, row + step), te_next = edge_of(tp, a.dts, row + step);
     copies_wait<STAGES - 1>();
+    // what is dropped of all the thread's vectors, in one word, one group after the other: worked out where it is used,
+    // it spilled 124 bytes a thread
+    uint32_t gone = 0;
+    if constexpr (DROP) {
+      if (a.dx)
+#pragma unroll 1
+        for (int j = 0; j < NV; ++j) gone |= dropped.from<N>((uint64_t)(row * width + c.column(j))) << (j * H);
+    }
     const float r = stat[stage * blockDim.x];
     const F2 r2 = f2(r, r);
     const uint4 *hv = slot + stage * arrays * NV * blockDim.x, *dv = hv + NV * blockDim.x, *tv = dv + NV * blockDim.x;
@@ -111,13 +119,12 @@ __global__ void __launch_bounds__(kRmsThreads) k_rms_backward_ring(const RmsArgs
         if (a.y && store) *reinterpret_cast<uint4 *>(static_cast<T *>(a.y) + row * a.ys + c.column(j)) = pack_pairs<T>(h);
         if constexpr (DROP) {
           if (a.dx && store) {
-            const uint32_t bits = keep.from<N>((uint64_t)(row * width + c.column(j)));
             float f[N];
 #pragma unroll
             for (int i = 0; i < H; ++i) {
               const float2 p = floats(h[i]);
-              f[2 * i] = bits >> (2 * i) & 1 ? p.x * keep.factor : 0.f;
-              f[2 * i + 1] = bits >> (2 * i + 1) & 1 ? p.y * keep.factor : 0.f;
+              f[2 * i] = gone >> (j * H + i) & 1 ? 0.f : p.x * dropped.factor;
+              f[2 * i + 1] = gone >> (16 + j * H + i) & 1 ? 0.f : p.y * dropped.factor;
             }
             *reinterpret_cast<uint4 *>(static_cast<T *>(a.dx) + row * a.dxs + c.column(j)) = pack16<T>(f);
           }
@@ -128,7 +135,7 @@ __global__ void __launch_bounds__(kRmsThreads) k_rms_backward_ring(const RmsArgs
         if (a.y) static_cast<T *>(a.y)[row * a.ys + c.edge] = from_float<T>(dh);
         if (DROP && a.dx)
           static_cast<T *>(a.dx)[row * a.dxs + c.edge] =
-              from_float<T>(keep.from<1>((uint64_t)(row * width + c.edge)) & 1 ? dh * keep.factor : 0.f);
+              from_float<T>(dropped.element((uint64_t)(row * width + c.edge)) ? 0.f : dh * dropped.factor);
       }
     }
     stage = (stage + 1) % STAGES;
@@ -170,7 +177,7 @@ __global__ void __launch_bounds__(WARP ? 32 * kAnyWarps : kAnyThreads) k_rms_bac
   const int team = WARP ? threadIdx.x >> 5 : 0;
   constexpr int kTeams = WARP ? kAnyWarps : 1;
   float *dw = sums + team * width;
-  const Keep keep(a.mask);
+  const Dropped dropped(a.mask);
   const float inv = 1.f / (float)width;
   for (int c = WARP ? lane : threadIdx.x; c < width; c += WARP ? 32 : blockDim.x) dw[c] = 0.f;
   if constexpr (WARP)
@@ -227,13 +234,13 @@ __global__ void __launch_bounds__(WARP ? 32 * kAnyWarps : kAnyThreads) k_rms_bac
       if (!drop || a.dx == nullptr) continue;
       const uint64_t e0 = (uint64_t)(row * width + c0);
       const int at = (int)(e0 & 7);
-      const uint32_t bits = keep.group((e0 >> 3) + lane), last = keep.group((e0 >> 3) + 32);
+      const uint32_t bits = dropped.group((e0 >> 3) + lane), last = dropped.group((e0 >> 3) + 32);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int c = c0 + i * 32 + lane, e = at + i * 32 + lane;
         uint32_t b = __shfl_sync(0xffffffffu, bits, (e >> 3) & 31);
         if (e >= 256) b = last;
-        if (c < width) static_cast<T *>(a.dx)[row * a.dxs + c] = from_float<T>(b >> (e & 7) & 1 ? f[i] * keep.factor : 0.f);
+        if (c < width) static_cast<T *>(a.dx)[row * a.dxs + c] = from_float<T>(Dropped::at(b, e & 7) ? 0.f : f[i] * dropped.factor);
       }
     }
   }
@@ -282,7 +289,7 @@ size_t rms_thread_bytes(const RmsArgs &a, int columns) {
 template <class T, int C, int LANES, bool DROP>
 cudaError_t launch_ring(RmsArgs &a, const RmsShape &s, cudaStream_t st) {
   const size_t thread = rms_thread_bytes<T>(a, C);
-  const RmsGrid grid = rms_grid(a.dm.rows, s, thread);
+  const RmsGrid grid = rms_grid<T>(a.dm.rows, s, thread);
   const auto kernel = k_rms_backward_ring<T, C, LANES, rms_stages<T>(), DROP>;
   static std::atomic<bool> allowed[64];
   const cudaError_t e = allow_smem(kernel, allowed);
@@ -321,7 +328,7 @@ cudaError_t launch_rms_typed(RmsArgs &a, bool drop, cudaStream_t st) {
   const RmsShape s = rms_shape(a.dm.width, e, rows_aligned16(a.total, a.ts, rows, e) && a.dm.width % N == 0, 8);
   auto alike = [&](const void *p, int64_t stride) { return rows_alike(p, stride, a.total, a.ts, rows, e); };
   if (!alike(a.dy, a.dys) || !alike(a.dtotal, a.dts) || !alike(a.y, a.ys) || !alike(a.dx, a.dxs) ||
-      rms_thread_bytes<T>(a, s.columns) * s.threads > kMostSmem)
+      s.threads > rms_threads<T>() || rms_thread_bytes<T>(a, s.columns) * s.threads > kMostSmem)
     return launch_any<T>(a, drop, st);
   return drop ? launch_ring_shape<T, true>(a, s, st) : launch_ring_shape<T, false>(a, s, st);
 }
