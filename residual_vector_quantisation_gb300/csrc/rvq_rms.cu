@@ -89,8 +89,8 @@ __device__ __forceinline__ void group_barrier(int group, int tpr) {
 // copies its vectors of the rows to come into its own slots of shared memory, and
 // keeps its columns' weights in registers.  All tensors of T start equally far
 // from a 16-byte boundary in each row.
-template <class T, int C, int LANES, int STAGES, bool DROP>
-__global__ void __launch_bounds__(rms_threads<T>()) k_rms_ring(const RmsArgs a, const int tpr_) {
+template <class T, int C, int LANES, bool DROP>
+__global__ void __launch_bounds__(rms_threads<T>(), 1) k_rms_ring(const RmsArgs a, const int tpr_) {
   constexpr int N = 16 / (int)sizeof(T), NV = C / N;
   extern __shared__ uint4 ring[];
   __shared__ float box[2 * kRmsThreads / 32][1][16];
@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(rms_threads<T>()) k_rms_ring(const RmsArgs a, 
 #pragma unroll
     for (int i = 0; i < N; ++i) g[j][i] = c.has(j) ? weight_at<T>(a, c.column(j) + i) : 0.f;
   uint4 *slot = ring + threadIdx.x;  // [stage][x, residual][j][thread]
-  for (int i = 0; i < STAGES * arrays * NV; ++i) slot[i * blockDim.x] = make_uint4(0, 0, 0, 0);
+  for (int i = 0; i < kStages * arrays * NV; ++i) slot[i * blockDim.x] = make_uint4(0, 0, 0, 0);
   auto fetch = [&](int64_t row, int stage) {
     if (row < rows) {
       uint4 *at = slot + stage * arrays * NV * blockDim.x;
@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(rms_threads<T>()) k_rms_ring(const RmsArgs a, 
     copies_end();
   };
 #pragma unroll
-  for (int k = 0; k < STAGES - 1; ++k) fetch(first + k * step, k);
+  for (int k = 0; k < kStages - 1; ++k) fetch(first + k * step, k);
   auto edge_of = [&](const T *p, int64_t stride, int64_t row) {
     return p && c.edge >= 0 && row < rows ? to_float(p[row * stride + c.edge]) : 0.f;
   };
@@ -134,11 +134,11 @@ __global__ void __launch_bounds__(rms_threads<T>()) k_rms_ring(const RmsArgs a, 
   const int64_t ahead = (int64_t)(group % kPerWarp) * gridDim.x;
   for (int64_t row = first; row - ahead < rows; row += step) {
     const bool there = row < rows;
-    fetch(row + (STAGES - 1) * step, (stage + STAGES - 1) % STAGES);
+    fetch(row + (kStages - 1) * step, (stage + kStages - 1) % kStages);
     float e = e_next;
     const float re = re_next;
     e_next = edge_of(x, a.xs, row + step), re_next = edge_of(res, a.rs, row + step);
-    copies_wait<STAGES - 1>();
+    copies_wait<kStages - 1>();
     const uint4 *xv = slot + stage * arrays * NV * blockDim.x, *rv = xv + NV * blockDim.x;
     uint32_t gone = 0;  // of all the thread's vectors
     if constexpr (DROP) {
@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(rms_threads<T>()) k_rms_ring(const RmsArgs a, 
     }
     e = e * r * ge;
     if (a.y && c.edge >= 0 && there) static_cast<T *>(a.y)[row * a.ys + c.edge] = from_float<T>(e);
-    stage = (stage + 1) % STAGES;
+    stage = (stage + 1) % kStages;
     if (a.q == nullptr) continue;
 
     uint8_t *q = a.q + row * a.qs;
@@ -419,17 +419,15 @@ __global__ void __launch_bounds__(WARP ? 32 * kAnyWarps : kAnyThreads)
 // ---------------------------------------------------------------------------
 
 template <class T>
-constexpr int rms_stages() { return sizeof(T) == 4 ? 2 : 3; }
-template <class T>
 size_t rms_thread_bytes(const RmsArgs &a, int columns) {
-  return (size_t)rms_stages<T>() * (a.residual ? 2 : 1) * columns * sizeof(T);
+  return (size_t)kStages * (a.residual ? 2 : 1) * columns * sizeof(T);
 }
 
 template <class T, int C, int LANES, bool DROP>
 cudaError_t launch_ring(const RmsArgs &a, const RmsShape &s, cudaStream_t st) {
   const size_t thread = rms_thread_bytes<T>(a, C);
   const RmsGrid grid = rms_grid<T>(a.dm.rows, s, thread);
-  const auto kernel = k_rms_ring<T, C, LANES, rms_stages<T>(), DROP>;
+  const auto kernel = k_rms_ring<T, C, LANES, DROP>;
   static std::atomic<bool> allowed[64];
   const cudaError_t e = allow_smem(kernel, allowed);
   if (e != cudaSuccess) return e;

@@ -44,6 +44,10 @@ constexpr int kRmsThreads = 512;
 template <class T>
 constexpr int rms_threads() { return sizeof(T) == 4 ? 384 : kRmsThreads; }
 
+// Rows that a thread has slots for: the one it works on and the next.  (Three leave room for fewer warps: 192 000 x 1024
+// bf16 with dropout, both passes, 691 us against 558.)
+constexpr int kStages = 2;
+
 // How a row lies in a ring kernel: over `threads`, `lanes` of a warp or (lanes 0)
 // whole warps, at most `columns` a thread.
 struct RmsShape {

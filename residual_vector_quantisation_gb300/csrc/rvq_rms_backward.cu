@@ -8,8 +8,8 @@ namespace {
 
 // Rows through a ring in shared memory, as in the forward pass: dresidual and dx
 // per row, and each block's sums of dy u over its rows into part[block][width].
-template <class T, int C, int LANES, int STAGES, bool DROP>
-__global__ void __launch_bounds__(rms_threads<T>()) k_rms_backward_ring(const RmsArgs a, const int tpr_) {
+template <class T, int C, int LANES, bool DROP>
+__global__ void __launch_bounds__(rms_threads<T>(), 1) k_rms_backward_ring(const RmsArgs a, const int tpr_) {
   constexpr int N = 16 / (int)sizeof(T), NV = C / N, H = N / 2;
   extern __shared__ uint4 ring[];
   __shared__ float box[2 * kRmsThreads / 32][1][16];
@@ -31,8 +31,8 @@ __global__ void __launch_bounds__(rms_threads<T>()) k_rms_backward_ring(const Rm
       dw[j][i] = zero;
     }
   uint4 *slot = ring + threadIdx.x;  // [stage][h, dy, dtotal][j][thread], then [stage][thread] of rstd
-  float *stat = reinterpret_cast<float *>(ring + STAGES * arrays * NV * blockDim.x) + threadIdx.x;
-  for (int i = 0; i < STAGES * arrays * NV; ++i) slot[i * blockDim.x] = make_uint4(0, 0, 0, 0);
+  float *stat = reinterpret_cast<float *>(ring + kStages * arrays * NV * blockDim.x) + threadIdx.x;
+  for (int i = 0; i < kStages * arrays * NV; ++i) slot[i * blockDim.x] = make_uint4(0, 0, 0, 0);
   auto fetch = [&](int64_t row, int stage) {
     uint4 *at = slot + stage * arrays * NV * blockDim.x;
     if (row < rows) {
@@ -53,7 +53,7 @@ __global__ void __launch_bounds__(rms_threads<T>()) k_rms_backward_ring(const Rm
     copies_end();
   };
 #pragma unroll
-  for (int k = 0; k < STAGES - 1; ++k) fetch(first + k * step, k);
+  for (int k = 0; k < kStages - 1; ++k) fetch(first + k * step, k);
   auto edge_of = [&](const T *p, int64_t stride, int64_t row) {
     return p && c.edge >= 0 && row < rows ? to_float(p[row * stride + c.edge]) : 0.f;
   };
@@ -65,10 +65,10 @@ __global__ void __launch_bounds__(rms_threads<T>()) k_rms_backward_ring(const Rm
   const int64_t ahead = (int64_t)(group % kPerWarp) * gridDim.x;
   for (int64_t row = first; row - ahead < rows; row += step) {
     const bool there = row < rows;
-    fetch(row + (STAGES - 1) * step, (stage + STAGES - 1) % STAGES);
+    fetch(row + (kStages - 1) * step, (stage + kStages - 1) % kStages);
     const float he = he_next, de = de_next, te = te_next;
     he_next = edge_of(hp, a.ts, row + step), de_next = edge_of(dp, a.dys, row + step), te_next = edge_of(tp, a.dts, row + step);
-    copies_wait<STAGES - 1>();
+    copies_wait<kStages - 1>();
     // what is dropped of all the thread's vectors, in one word, one group after the other: worked out where it is used,
     // it spilled 124 bytes a thread
     uint32_t gone = 0;
@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(rms_threads<T>()) k_rms_backward_ring(const Rm
               from_float<T>(dropped.element((uint64_t)(row * width + c.edge)) ? 0.f : dh * dropped.factor);
       }
     }
-    stage = (stage + 1) % STAGES;
+    stage = (stage + 1) % kStages;
   }
   if (a.part == nullptr || blockIdx.x >= rows) return;  // (a block without rows has no part in the workspace)
   copies_wait<0>();
@@ -278,19 +278,17 @@ __global__ void __launch_bounds__(32 * kSumRows) k_rms_weight(const float *part,
 // Blocks of the backward pass at most: the workspace holds a part of each.
 inline int rms_parts(int64_t rows) { return (int)(rows < 2 * kSms ? rows : 2 * kSms); }
 
-template <class T>
-constexpr int rms_stages() { return sizeof(T) == 4 ? 2 : 3; }
 // Shared memory of a thread: its slots and a place for rstd.
 template <class T>
 size_t rms_thread_bytes(const RmsArgs &a, int columns) {
-  return (size_t)rms_stages<T>() * ((a.dtotal ? 3 : 2) * columns * sizeof(T) + 4);
+  return (size_t)kStages * ((a.dtotal ? 3 : 2) * columns * sizeof(T) + 4);
 }
 
 template <class T, int C, int LANES, bool DROP>
 cudaError_t launch_ring(RmsArgs &a, const RmsShape &s, cudaStream_t st) {
   const size_t thread = rms_thread_bytes<T>(a, C);
   const RmsGrid grid = rms_grid<T>(a.dm.rows, s, thread);
-  const auto kernel = k_rms_backward_ring<T, C, LANES, rms_stages<T>(), DROP>;
+  const auto kernel = k_rms_backward_ring<T, C, LANES, DROP>;
   static std::atomic<bool> allowed[64];
   const cudaError_t e = allow_smem(kernel, allowed);
   if (e != cudaSuccess) return e;

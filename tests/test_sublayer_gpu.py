@@ -484,3 +484,66 @@ def test_rms_gradient_against_differences():
     got, size = sum(t.sum().item() for t in terms), sum(t.abs().sum().item() for t in terms)
     # the inputs' rounding and the gradient's (64 roundings of 2^-24 each), and the differences' own error of about step^2
     assert abs(got - want) <= size * (128 * ref.U + 1e-8), (got, want)
+
+
+# ---------------------------------------------------------------------------
+# together
+# ---------------------------------------------------------------------------
+
+def test_a_predictor_is_trained_scored_and_distilled():
+    """Two sublayers (drop, add, norm), a head, log probabilities with entropy, one step of a policy's loss, the lists of
+    a teacher, a distillation step and a beam step on the scores; the gradients against the same in 64 bits."""
+    g = gen(21)
+    rows, width, vocab = 60, 64, 90
+    x0, f0, f1 = (randn(g, rows, width) for _ in range(3))
+    w = [(1 + 0.2 * randn(g, width)) for _ in range(2)]
+    head = randn(g, vocab, width) / 8
+    codes = torch.randint(-1, vocab, (rows,), generator=g, device=DEV)
+    gain = randn(g, rows)
+    step = step_of(5)
+    masks = [rq.rvq_dropout_mask(0.1, 33, place, step) for place in range(2)]
+    keeps = [tuple(torch.as_tensor(v, device=DEV) for v in ref.stays(rows * width, 0.1, 33, place, 5)) for place in range(2)]
+
+    def model(x, f, g2, wa, wb, ours):
+        if ours:
+            y, total = rq.rms_norm(f, wa, 1e-6, x, masks[0])
+            y, total = rq.rms_norm(g2 + y, wb, 1e-6, total, masks[1])
+        else:
+            total = torch.where(keeps[0][0].view(rows, width), f * keeps[0][1], 0.0) + x
+            y = total / torch.sqrt((total * total).mean(1, keepdim=True) + 1e-6) * wa
+            total = torch.where(keeps[1][0].view(rows, width), (g2 + y) * keeps[1][1], 0.0) + total
+            y = total / torch.sqrt((total * total).mean(1, keepdim=True) + 1e-6) * wb
+        return y
+
+    def loss_of(leaves, ours):
+        logits = model(*leaves[:5], ours) @ leaves[5].t()
+        if ours:
+            out = rq.log_probs(logits, codes, entropy=True)
+            return -(gain * out.log_probs).sum() - 0.1 * out.entropy.sum() + 0.01 * (out.lse ** 2).sum(), logits
+        lp = torch.log_softmax(logits, 1)
+        at = torch.where(codes >= 0, lp.gather(1, codes.clamp(min=0)[:, None])[:, 0], 0.0)
+        entropy = -(lp.exp() * lp).sum(1)
+        return -(gain * at).sum() - 0.1 * entropy.sum() + 0.01 * (torch.logsumexp(logits, 1) ** 2).sum(), logits
+
+    plain = [t.double().requires_grad_() for t in (x0, f0, f1, *w, head)]
+    leaves = [t.clone().requires_grad_() for t in (x0, f0, f1, *w, head)]
+    loss, logits = loss_of(leaves, True)
+    loss.backward()
+    loss_of(plain, False)[0].backward()
+    for a, b in zip(leaves, plain):
+        # a product of 64, one of 90, four norms and two sums over 64: each STEPS roundings of what it adds, which the
+        # largest gradients bound
+        assert (a.grad.double() - b.grad).abs().max() <= 16 * ref.STEPS * ref.U * b.grad.abs().max() * width ** 0.5
+    step.add_(1)
+
+    # the trained model as the teacher of a student, by its lists; and its answers' scores in a beam step
+    logits = logits.detach()
+    top = rq.log_probs(logits, top=8, temperature=2.0)
+    student = randn(g, rows, vocab).requires_grad_()
+    rq.distill_loss(student, 2.0 * top.top_log_probs, top.top_codes, torch.zeros_like(top.lse), temperature=2.0).sum().backward()
+    assert bool(torch.isfinite(student.grad).all()) and bool((student.grad != 0).any())
+    best = rq.log_probs(logits, top=4)
+    search = rq.BeamSearch(rows, 1, vocab, 4)
+    scores, _, chosen, _ = search.select(logits.view(rows, 1, vocab), torch.zeros((rows, 1), device=DEV))
+    assert torch.equal(chosen, best.top_codes)
+    ref.check(scores, best.top_log_probs.double().cpu(), 64 * ref.U * best.top_log_probs.abs().double().cpu() + 64 * ref.U, "scores")
