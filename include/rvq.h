@@ -564,11 +564,13 @@ RVQ_API rvq_status rvq_dropout(rvq_dropout_dims dims, const void *x, int64_t x_s
  * [rows] rows of width bytes, `stride` bytes apart; scales [rows][n], contiguous,
  * one for each `block` neighbouring columns (32, 64 or 128; n = ceil(width /
  * block)) or, block 0, one a row.  A value stands for itself times its scale:
- *   scale = max(largest magnitude of the block's y / 448, 2^-126),
- * of scale_type RVQ_SCALE_F32, or, RVQ_SCALE_E8M0, rounded up to a power of two
+ *   scale = max(largest magnitude of the block's y / 448, 2^-126)
+ * (a product with 1 / 448, off by a unit in the last place at most), of scale_type RVQ_SCALE_F32, or, RVQ_SCALE_E8M0, rounded up to a power of two
  * and held as its biased exponent (a byte); value = y / scale, rounded to nearest
  * (y before its own rounding; the division is a product with the inverse).  A
- * NaN in a block makes its scale and all its values NaN. */
+ * NaN in a block makes its scale and all its values NaN.  An infinity makes its
+ * own value NaN: in float32 the scale is infinite and the block's other values are
+ * 0, as a power of two it is NaN and so are they. */
 #define RVQ_SCALE_F32 0
 #define RVQ_SCALE_E8M0 1
 typedef struct rvq_rms_8bit {

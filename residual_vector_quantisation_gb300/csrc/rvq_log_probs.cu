@@ -123,6 +123,9 @@ __device__ __forceinline__ CutRow<T> row_of(const LogProbsArgs &a, int64_t row) 
 
 constexpr int kRowWarps = 4;  // of a block
 
+// Bound by instructions: 439 a row of 1025 codes, 180 of them for the elements (a
+// power, its sum and its product with the exponent), the rest for two sums, the
+// edges and the results.  60 000 x 1025 bf16: 31 us (bytes alone: 18).
 template <class T, int NV, bool ENT>
 __global__ void __launch_bounds__(32 * kRowWarps) k_log_probs(const LogProbsArgs a) {
   const int lane = threadIdx.x & 31;
@@ -146,6 +149,9 @@ __global__ void __launch_bounds__(32 * kRowWarps) k_log_probs(const LogProbsArgs
   if (lane == 0) put_row(a, row, r.z, t);
 }
 
+// With the best alternatives: 1200 instructions a row of 1024 codes and 16 kept,
+// two thirds of them for finding the bar, reading again what reaches it and
+// ordering it.  60 000 x 1024 f32: 92 us (bytes alone: 36).
 template <class T>
 __global__ void __launch_bounds__(32 * kRowWarps) k_log_probs_top(const LogProbsArgs a) {
   constexpr int NV = 32 * (int)sizeof(T) / 16;
@@ -202,6 +208,9 @@ __device__ __forceinline__ Tally row_tally(Tally v, float c, Tally *box, Tally *
   return rank == 0 ? warp_join(lane < cs ? parts[lane] : no_tally(), c) : v;
 }
 
+// Each thread raises its own largest value as it goes; U vectors of it are under
+// way while U are added.  Bound by bandwidth: with the gradient's kernel 241 us for
+// 4096 x 65536 bf16 (98 % of a copy's rate).
 template <class T, bool ENT>
 __global__ void __launch_bounds__(32 * kMaxWarps) k_log_probs_row(const LogProbsArgs a, const int cs) {
   constexpr int U = 4;
@@ -274,6 +283,9 @@ __device__ __forceinline__ int join_lists(const uint64_t *list, int stride, int 
   return min(c, n);
 }
 
+// With the best alternatives: each warp orders its pieces, the block the warps'
+// lists, the cluster's first block the blocks'.  6 rows of 65536 f16 with 32 kept
+// take 18 us over 8 blocks a row: latency of one piece's ordering and two joins.
 template <class T, int NV>
 __global__ void __launch_bounds__(32 * kMaxWarps) k_log_probs_row_top(const LogProbsArgs a, const int cs) {
   extern __shared__ uint64_t smem[];
@@ -329,7 +341,8 @@ __global__ void __launch_bounds__(32 * kMaxWarps) k_log_probs_row_top(const LogP
 
 constexpr int kBackWarps = 8;
 
-// A warp per piece of a row (`pieces` of NV vectors a lane each).
+// A warp per piece of a row (`pieces` of NV vectors a lane each).  60 000 x 1025
+// bf16 with the entropy's gradient: 42 us (bytes alone: 36), 491 instructions a row.
 template <class T, int NV, bool ENT>
 __global__ void __launch_bounds__(32 * kBackWarps) k_log_probs_backward(const LogProbsArgs a, const int pieces) {
   constexpr int N = 16 / (int)sizeof(T);

@@ -8,6 +8,8 @@ namespace {
 
 // Rows through a ring in shared memory, as in the forward pass: dresidual and dx
 // per row, and each block's sums of dy u over its rows into part[block][width].
+// 60 000 x 1024 bf16 with the sum's gradient: 81 us (bytes alone: 72), with
+// dropout, one tensor more, 108 (90).
 template <class T, int C, int LANES, bool DROP>
 __global__ void __launch_bounds__(rms_threads<T>(), 1) k_rms_backward_ring(const RmsArgs a, const int tpr_) {
   constexpr int N = 16 / (int)sizeof(T), NV = C / N, H = N / 2;

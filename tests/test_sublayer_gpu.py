@@ -486,6 +486,52 @@ def test_rms_gradient_against_differences():
     assert abs(got - want) <= size * (128 * ref.U + 1e-8), (got, want)
 
 
+def test_rms_two_streams_at_once_and_a_graph():
+    x, r, dy, dt, w = make_rms(3000, 520, BF16, F32)
+    want = run_rms(x, w, 1e-6, dy, r, MASK, dt)
+    q_want = run_8bit(x, w, r, 32, True)
+    torch.cuda.synchronize()
+    got = []
+    for s in [torch.cuda.Stream() for _ in range(2)]:
+        with torch.cuda.stream(s):
+            got.append((run_rms(x, w, 1e-6, dy, r, MASK, dt), run_8bit(x, w, r, 32, True)))
+    torch.cuda.synchronize()
+    for a, q in got:
+        for k in want:
+            assert torch.equal(a[k], want[k]), k
+        for u, v in zip(q, q_want):
+            assert torch.equal(u.view(torch.uint8), v.view(torch.uint8))
+    # a training step through autograd, captured: a new mask at each replay, the gradients those of its own
+    step, grads = step_of(0), []
+    leaves = [t.float().clone().requires_grad_() for t in (x[:40], r[:40], w)]
+    mask = rq.rvq_dropout_mask(0.2, 3, 1, step)
+
+    def train():
+        y, total = rq.rms_norm(leaves[0], leaves[2], 1e-6, leaves[1], mask)
+        out = torch.autograd.grad((y.square().sum() + total.sum()), leaves)
+        step.add_(1)
+        return [y, total, *out]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        train()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = train()
+    for k in (1, 2):
+        graph.replay()
+        torch.cuda.synchronize()
+        total = ref.total_of(leaves[0].detach(), (0.2, 3, 1, k), leaves[1].detach())
+        assert torch.equal(captured[1], total)
+        grads.append([t.clone() for t in captured])
+        step.fill_(k)
+        for a, b in zip(train(), grads[-1]):
+            assert torch.equal(a, b)
+    assert not torch.equal(grads[0][1], grads[1][1])
+
+
 # ---------------------------------------------------------------------------
 # together
 # ---------------------------------------------------------------------------
