@@ -151,9 +151,10 @@ __global__ void __launch_bounds__(32 * kRowWarps) k_log_probs(const LogProbsArgs
 
 // With the best alternatives: 1200 instructions a row of 1024 codes and 16 kept,
 // two thirds of them for finding the bar, reading again what reaches it and
-// ordering it.  60 000 x 1024 f32: 92 us (bytes alone: 36).
+// ordering it.  384 000 x 1024 f32: 510 us (bytes alone: 239), with registers held
+// down for 8 blocks an SM; 546 as the compiler would have it (72 registers).
 template <class T>
-__global__ void __launch_bounds__(32 * kRowWarps) k_log_probs_top(const LogProbsArgs a) {
+__global__ void __launch_bounds__(32 * kRowWarps, 8) k_log_probs_top(const LogProbsArgs a) {
   constexpr int NV = 32 * (int)sizeof(T) / 16;
   __shared__ WarpRoom room[kRowWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = a.dm.top;
