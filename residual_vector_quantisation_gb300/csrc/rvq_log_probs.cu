@@ -7,7 +7,7 @@
 // one scales both), and from them
 //   log p[c] = (z_c - m) / T - ln s,   H = ln s - ln 2 * a / s,   lse = m / T + ln s.
 // Both terms of H are positive: nothing cancels.  The gradient needs no sum:
-//   dz_j = 2^y_j (k0 + k1 y_j) + [j = c] g / T.
+//   dz_j = (2^y_j (k0 + k1 y_j) + [j = c] g) / T.
 #include "rvq_internal.cuh"
 #include "rvq_overlap.h"
 #include "rvq_top.cuh"
@@ -368,15 +368,15 @@ __global__ void __launch_bounds__(32 * kBackWarps) k_log_probs_backward(const Lo
   if (code < 0 || code >= a.dm.vocab) code = -1, g = 0.f;
   // no gradient reaches the row, or nothing in it has a probability
   const bool zero = (g == 0.f && gh == 0.f && gl == 0.f) || s == 0.f;
-  const float scale = __fdividef(a.inv_t, s), at_code = zero ? 0.f : g * a.inv_t;
+  const float scale = __fdividef(1.f, s), at_code = zero ? 0.f : g * a.inv_t;
   const float k0 = (gl - g - (ENT ? gh * (entropy - logf(s)) : 0.f)) * scale, k1 = -gh * kLn2 * scale;
-  const F2 minus = f2(-m, -m), c2 = f2(a.c, a.c), k0s = f2(k0, k0), k1s = f2(k1, k1);
+  const F2 minus = f2(-m, -m), c2 = f2(a.c, a.c), k0s = f2(k0, k0), k1s = f2(k1, k1), inv_t = f2(a.inv_t, a.inv_t);
   auto grad = [&](F2 z) {
     const F2 p = (z + minus) * c2;
     float2 y = floats(p);
     if constexpr (ENT) y.x = max_nan(y.x, kLowest), y.y = max_nan(y.y, kLowest);
     const F2 e = f2(exp2_fast(y.x), exp2_fast(y.y));
-    return ENT ? e * fma2(k1s, f2(y.x, y.y), k0s) : e * k0s;
+    return (ENT ? e * fma2(k1s, f2(y.x, y.y), k0s) : e * k0s) * inv_t;  // (1 / T last: a power of 0 stays 0)
   };
   const bool same = ((reinterpret_cast<uintptr_t>(r.z) ^ reinterpret_cast<uintptr_t>(d)) & 15) == 0;
 #pragma unroll

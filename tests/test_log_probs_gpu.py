@@ -176,6 +176,20 @@ def test_nan_inf_and_rows_without_gradient(vocab):
         assert torch.equal(got[k][[0, 3, 5]], clean[k][[0, 3, 5]]), k
 
 
+@pytest.mark.parametrize("vocab", [100, 3000, 20000])
+def test_lowest_temperature(vocab):
+    """All is on the largest logit: no entropy, and gradients of 0 where that is the code and elsewhere, however large a
+    finite one the inverse of the temperature makes of those that are not."""
+    z, codes, _ = make(5, vocab, F32)
+    codes[:] = z.argmax(1).to(torch.int32)
+    grads = [torch.full((5,), 1000.0, device=DEV), torch.full((5,), 2.0, device=DEV), None]
+    got = run(z, codes, 4.3e-39, 2, [torch.full((5,), 0.5, device=DEV), grads[1], None])
+    assert bool((got["log_probs"] == 0).all()) and bool((got["entropy"] == 0).all()) and bool((got["dlogits"] == 0).all())
+    got = run(z, codes, 4.3e-39, 2, grads)          # 1000 / T is past float32
+    others = got["dlogits"].scatter(1, codes.long()[:, None], 0.0)
+    assert bool((others == 0).all())
+
+
 def test_codes_out_of_range():
     z, codes, grads = make(6, 100, BF16)
     codes[:] = torch.tensor([-1, 100, -2, 99, 2 ** 31 - 1, 0], device=DEV)
