@@ -56,6 +56,8 @@ __global__ void __launch_bounds__(kThreads) k_dropout(const DropoutArgs a) {
 
 // Anything else: a warp takes 256 elements, each lane working out one group of
 // them, so that lanes next to one another read and write next to one another.
+// Bound by instructions: 58 536 x 1025 bf16, rows 1031 apart, 129 us (bytes alone
+// 35).
 template <class T>
 __global__ void __launch_bounds__(kThreads) k_dropout_elements(const DropoutArgs a) {
   const Dropped drop(a.mask);
@@ -63,16 +65,29 @@ __global__ void __launch_bounds__(kThreads) k_dropout_elements(const DropoutArgs
   const int64_t all = a.rows * a.width, warps = (int64_t)gridDim.x * (kThreads / 32);
   for (int64_t e0 = (blockIdx.x * (int64_t)(kThreads / 32) + (threadIdx.x >> 5)) * 256; e0 < all; e0 += warps * 256) {
     const uint32_t bits = drop.group((uint64_t)(e0 / 8 + lane));
+    // Where the lane's elements lie, 32 apart: one division, then sums.  All are read before any is written (y may be
+    // x, so that the compiler keeps reads behind the writes that stand before them).
+    const int64_t row0 = (e0 + lane) / a.width, col0 = e0 + lane - row0 * a.width;
+    const int left = (int)min(all - e0 - lane, (int64_t)256);  // element i is there: i * 32 < left
+    auto walk = [&](int64_t stride, auto at) {
+      int64_t col = col0, place = row0 * stride + col0;
+      const int64_t gap = stride - a.width;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (i * 32 < left) at(i, place);
+        place += 32;
+        for (col += 32; col >= a.width; col -= a.width) place += gap;
+      }
+    };
+    float f[8], r[8] = {};
+    walk(a.xs, [&](int i, int64_t place) { f[i] = to_float(static_cast<const T *>(a.x)[place]); });
+    if (a.residual) walk(a.rs, [&](int i, int64_t place) { r[i] = to_float(static_cast<const T *>(a.residual)[place]); });
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int64_t e = e0 + i * 32 + lane;
-      const bool gone = Dropped::at(__shfl_sync(0xffffffffu, bits, i * 4 + lane / 8), lane & 7);
-      if (e >= all) continue;
-      const int64_t row = e / a.width, col = e - row * a.width;
-      float f = gone ? 0.f : __fmul_rn(to_float(static_cast<const T *>(a.x)[row * a.xs + col]), drop.factor);
-      if (a.residual) f = __fadd_rn(f, to_float(static_cast<const T *>(a.residual)[row * a.rs + col]));
-      static_cast<T *>(a.y)[row * a.ys + col] = from_float<T>(f);
+      f[i] = Dropped::at(__shfl_sync(0xffffffffu, bits, i * 4 + lane / 8), lane & 7) ? 0.f : __fmul_rn(f[i], drop.factor);
+      if (a.residual) f[i] = __fadd_rn(f[i], r[i]);
     }
+    walk(a.ys, [&](int i, int64_t place) { static_cast<T *>(a.y)[place] = from_float<T>(f[i]); });
   }
 }
 
