@@ -135,10 +135,11 @@ class _RmsNorm(torch.autograd.Function):
             nbytes = _rq.rvq_rms_norm_workspace_bytes(*total.shape)
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=total.device)
         _rq.rvq_rms_norm_backward(dy, total, weight, rstd, dresidual, dweight, workspace, dtotal, mask, dx)
-        if mask is None:
-            dx = dresidual
-        return (dx.view(ctx.shape) if need[0] else None, dresidual.view(ctx.shape) if need[1] else None, dweight,
-                None, None, None)
+        dresidual = None if dresidual is None else dresidual.view(ctx.shape)
+        # without a mask x's gradient is the residual's, and the same tensor: autograd gives a leaf a gradient that
+        # nothing else holds as it is, and two views of one memory would each be such a one
+        dx = dresidual if mask is None else None if dx is None else dx.view(ctx.shape)
+        return dx if need[0] else None, dresidual if need[1] else None, dweight, None, None, None
 
 
 def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: float = 1e-6,

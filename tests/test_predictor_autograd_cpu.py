@@ -1,0 +1,75 @@
+"""The predictor's autograd functions on the CPU: what they do around the kernels, whose calls are replaced by torch
+statements of the same."""
+
+import pytest
+import torch
+
+import residual_vector_quantisation_gb300 as rq
+import sublayer_ref as ref
+
+
+def stays(rows, mask):
+    keep, factor = ref.stays(rows.numel(), mask.p, mask.seed, mask.offset)
+    return torch.from_numpy(keep).view(rows.shape), factor
+
+
+def drop(rows, mask):
+    if mask is None:
+        return rows
+    keep, factor = stays(rows, mask)
+    return torch.where(keep, rows * factor, 0.0)
+
+
+def dropout(x, mask, y, residual=None):
+    y.copy_(drop(x, mask) if residual is None else drop(x, mask) + residual)
+
+
+def rms_norm(x, weight, eps, y, rstd=None, residual=None, mask=None, total=None):
+    h = drop(x, mask) if residual is None else drop(x, mask) + residual
+    if total is not None:
+        total.copy_(h)
+    rstd.copy_(1 / torch.sqrt((h * h).mean(1) + eps))
+    y.copy_(h * rstd[:, None] * (1 if weight is None else weight))
+
+
+def rms_norm_backward(dy, total, weight, rstd, dresidual, dweight, workspace, dtotal=None, mask=None, dx=None):
+    u, g = total * rstd[:, None], dy * (1 if weight is None else weight)
+    dh = rstd[:, None] * (g - u * (g * u).mean(1, keepdim=True))
+    if dtotal is not None:
+        dh = dh + dtotal
+    for out, value in ((dresidual, dh), (dx, None if mask is None else drop(dh, mask)), (dweight, (dy * u).sum(0))):
+        if out is not None:
+            out.copy_(value)
+
+
+@pytest.fixture(autouse=True)
+def statements(monkeypatch):
+    for name, f in (("rvq_dropout", dropout), ("rvq_rms_norm", rms_norm), ("rvq_rms_norm_backward", rms_norm_backward),
+                    ("rvq_rms_norm_workspace_bytes", lambda rows, width: 16)):
+        monkeypatch.setattr(rq, name, f)
+
+
+def tensors(n, *shape, seed=0):
+    g = torch.Generator().manual_seed(seed)
+    return [torch.randn(shape, generator=g, dtype=torch.float64) for _ in range(n)]
+
+
+def leaves(*values):
+    return [v.clone().requires_grad_() for v in values]
+
+
+@pytest.mark.parametrize("mask", [None, rq.rvq_dropout_mask(0.3, 5)])
+def test_rms_norm_gradients_have_memory_of_their_own(mask):
+    """A second pass adds to each leaf's gradient once, and a change of one leaves the other's."""
+    x, r, up, ut = tensors(4, 3, 4, 8)
+    x, r = leaves(x, r)
+
+    def both_passes():
+        torch.autograd.backward(rq.rms_norm(x, None, 1e-6, r, mask), (up, ut))
+
+    both_passes()
+    first = x.grad.clone(), r.grad.clone()
+    both_passes()
+    assert torch.equal(x.grad, 2 * first[0]) and torch.equal(r.grad, 2 * first[1])
+    x.grad.mul_(0.5)
+    assert torch.equal(r.grad, 2 * first[1])
