@@ -125,8 +125,16 @@ class _RmsNorm(torch.autograd.Function):
         if dy is None and dtotal is None:
             return (None,) * 6
         like = dict(dtype=total.dtype, device=total.device)
-        dy = torch.zeros(total.shape, **like) if dy is None else _as_rows(dy.to(total.dtype))
         dtotal = None if dtotal is None else _as_rows(dtotal.to(total.dtype))
+        if dy is None:  # the sum's gradient passes the norm by, whatever its rows hold
+            dresidual = dtotal.view(ctx.shape)
+            dx = dresidual
+            if need[0] and mask is not None:
+                dx = torch.empty(ctx.shape, **like)
+                _rq.rvq_dropout(dtotal, mask, dx.view(dtotal.shape))
+            return (dx if need[0] else None, dresidual if need[1] else None,
+                    torch.zeros_like(weight) if need[2] else None, None, None, None)
+        dy = _as_rows(dy.to(total.dtype))
         dresidual = torch.empty(total.shape, **like) if need[1] or (need[0] and mask is None) else None
         dx = torch.empty(total.shape, **like) if need[0] and mask is not None else None
         dweight = workspace = None

@@ -73,3 +73,24 @@ def test_rms_norm_gradients_have_memory_of_their_own(mask):
     assert torch.equal(x.grad, 2 * first[0]) and torch.equal(r.grad, 2 * first[1])
     x.grad.mul_(0.5)
     assert torch.equal(r.grad, 2 * first[1])
+
+
+@pytest.mark.parametrize("mask", [None, rq.rvq_dropout_mask(0.3, 5)])
+def test_gradient_of_the_sum_alone_passes_by_the_norm(mask):
+    """Rows whose norm is not finite (zeros without an eps, infinities, NaN) leave the sum's gradient as it is."""
+    x, r, ut = tensors(3, 5, 8)
+    x[0] = r[0] = 0.0
+    x[1, 2], r[2, 3] = torch.nan, torch.inf
+    x, r, w = leaves(x, r, torch.ones(8, dtype=torch.float64))
+    y, total = rq.rms_norm(x, w, 0.0, r, mask)
+    assert mask is not None or not bool(torch.isfinite(y[:3]).all(1).any())
+    total.backward(ut)
+    assert torch.equal(r.grad, ut) and torch.equal(x.grad, drop(ut, mask))
+    assert bool((w.grad == 0).all())
+    # x or residual alone, the sum's gradient as it comes from a sum
+    for given in (0, 1):
+        a, b = tensors(2, 5, 8)
+        one = leaves((a, b)[given])[0]
+        rq.rms_norm(*((one, w, 1e-6, b) if given == 0 else (a, w, 1e-6, one)), mask)[1].sum().backward()
+        ones = torch.ones_like(a)
+        assert torch.equal(one.grad, drop(ones, mask) if given == 0 else ones)
