@@ -120,6 +120,12 @@ class rvq_dropout_mask(ctypes.Structure):
         super().__init__(p, seed, offset, None if step is None else step.data_ptr())
         self.tensor = step
 
+    def copy(self) -> "rvq_dropout_mask":
+        """The same mask, with the same step; changes of one's fields do not reach the other."""
+        other = rvq_dropout_mask.from_buffer_copy(self)
+        other.tensor = self.tensor
+        return other
+
 
 class rvq_dropout_dims(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int64), ("width", ctypes.c_int64), ("dtype", ctypes.c_int32)]

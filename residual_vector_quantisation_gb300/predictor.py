@@ -77,7 +77,7 @@ class _Dropout(torch.autograd.Function):
         y = torch.empty(rows.shape, dtype=x.dtype, device=x.device)
         _rq.rvq_dropout(rows, mask, y, add)
         ctx.save_for_backward(step)  # counted up before the backward pass, it would give another mask
-        ctx.mask = mask
+        ctx.mask = mask.copy()  # its fields may be another place's by then
         return y.view(x.shape)
 
     @staticmethod
@@ -114,7 +114,7 @@ class _RmsNorm(torch.autograd.Function):
         _rq.rvq_rms_norm(rows, weight, eps, y, rstd, add, mask, total)
         ctx.save_for_backward(rows if total is None else total, weight, rstd, step)
         ctx.set_materialize_grads(False)
-        ctx.shape, ctx.mask = x.shape, mask
+        ctx.shape, ctx.mask = x.shape, None if mask is None else mask.copy()
         return y.view(x.shape) if total is None else (y.view(x.shape), total.view(x.shape))
 
     @staticmethod

@@ -94,3 +94,19 @@ def test_gradient_of_the_sum_alone_passes_by_the_norm(mask):
         rq.rms_norm(*((one, w, 1e-6, b) if given == 0 else (a, w, 1e-6, one)), mask)[1].sum().backward()
         ones = torch.ones_like(a)
         assert torch.equal(one.grad, drop(ones, mask) if given == 0 else ones)
+
+
+def test_a_mask_changed_between_the_passes():
+    """The backward pass is the forward pass's, whatever became of the mask's fields since: one mask that serves one
+    place of a model after the other."""
+    x, r, up, ut = tensors(4, 6, 8)
+    for call in (lambda x, r, m: (rq.dropout(x, m, r),), lambda x, r, m: rq.rms_norm(x, None, 1e-6, r, m)):
+        want, got = leaves(x, r), leaves(x, r)
+        out = call(*want, rq.rvq_dropout_mask(0.3, 5, 1))
+        torch.autograd.backward(out, (up, ut)[:len(out)])
+        mask = rq.rvq_dropout_mask(0.3, 5, 1)
+        out = call(*got, mask)
+        mask.p, mask.seed, mask.offset = 0.9, 6, 2
+        torch.autograd.backward(out, (up, ut)[:len(out)])
+        for a, b in zip(got, want):
+            assert torch.equal(a.grad, b.grad)
