@@ -93,15 +93,18 @@ class _Dropout(torch.autograd.Function):
         return dx, dy if ctx.needs_input_grad[1] else None, None, None
 
 
-def dropout(x: torch.Tensor, mask: _rq.rvq_dropout_mask, residual: Optional[torch.Tensor] = None) -> torch.Tensor:
-    """x where the mask has it stay, times the factor that keeps its mean, and 0 elsewhere; plus residual.
+def dropout(x: torch.Tensor, mask: Optional[_rq.rvq_dropout_mask],
+            residual: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """x where the mask has it stay, times the factor that keeps its mean, and 0 elsewhere; plus residual: a new tensor.
     Differentiable in x and residual (x's shape and dtype).  The mask is made anew in the backward pass and never
     stored: mask = rvq_dropout_mask(p, seed, offset, step) says which one, element by element of x in its order
-    (whatever its strides).  A step on the GPU has to be counted up after the backward pass.  Runs on the current
-    stream."""
+    (whatever its strides); None: nothing is dropped.  A step on the GPU has to be counted up after the backward pass.
+    Runs on the current stream."""
+    if mask is None:
+        mask = _rq.rvq_dropout_mask(0.0, 0)
     if x.numel() == 0:
         return x.clone() if residual is None else x + residual
-    return _Dropout.apply(x, residual, mask, None if mask is None else mask.tensor)
+    return _Dropout.apply(x, residual, mask, mask.tensor)
 
 
 class _RmsNorm(torch.autograd.Function):

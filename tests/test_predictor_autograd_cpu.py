@@ -110,3 +110,18 @@ def test_a_mask_changed_between_the_passes():
         torch.autograd.backward(out, (up, ut)[:len(out)])
         for a, b in zip(got, want):
             assert torch.equal(a.grad, b.grad)
+
+
+def test_dropout_without_a_mask_drops_nothing():
+    """As root-mean-square norm takes it: a model in evaluation hands on None."""
+    x, r, up = tensors(3, 2, 3, 8)
+    x, r = leaves(x, r)
+    y = rq.dropout(x, None)
+    assert torch.equal(y, x) and y.data_ptr() != x.data_ptr()
+    y = rq.dropout(x, None, r)
+    assert torch.equal(y, x + r)
+    y.backward(up)
+    assert torch.equal(x.grad, up) and torch.equal(r.grad, up)
+    for empty in (x[:0], x[..., :0]):
+        assert rq.dropout(empty, None).shape == empty.shape
+        assert rq.dropout(empty, None, empty).shape == empty.shape
