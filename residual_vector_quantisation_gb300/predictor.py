@@ -63,10 +63,14 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
     return _LayerNorm.apply(x, weight, bias, eps)
 
 
-def _beside(x: torch.Tensor, residual: Optional[torch.Tensor]):
-    """x and residual as rows."""
+def _same_kind(x: torch.Tensor, residual: Optional[torch.Tensor]) -> None:
     if residual is not None and (residual.shape != x.shape or residual.dtype != x.dtype):
         raise ValueError("residual must have x's shape and dtype")
+
+
+def _beside(x: torch.Tensor, residual: Optional[torch.Tensor]):
+    """x and residual as rows."""
+    _same_kind(x, residual)
     return _as_rows(x), None if residual is None else _as_rows(residual)
 
 
@@ -103,6 +107,7 @@ def dropout(x: torch.Tensor, mask: Optional[_rq.rvq_dropout_mask],
     if mask is None:
         mask = _rq.rvq_dropout_mask(0.0, 0)
     if x.numel() == 0:
+        _same_kind(x, residual)
         return x.clone() if residual is None else x + residual
     return _Dropout.apply(x, residual, mask, mask.tensor)
 

@@ -125,3 +125,12 @@ def test_dropout_without_a_mask_drops_nothing():
     for empty in (x[:0], x[..., :0]):
         assert rq.dropout(empty, None).shape == empty.shape
         assert rq.dropout(empty, None, empty).shape == empty.shape
+
+
+def test_dropout_refuses_another_residual_without_elements_too():
+    x = torch.zeros(2, 3, 8)
+    mask = rq.rvq_dropout_mask(0.1, 1)
+    for a, b in ((x, x[:1]), (x[:0], x[:1, :1]), (x[:0], x[:0].double())):
+        for m in (mask, None):
+            with pytest.raises(ValueError):
+                rq.dropout(a, m, b)
