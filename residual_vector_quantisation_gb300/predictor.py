@@ -25,16 +25,23 @@ def _as_rows(t: torch.Tensor) -> torch.Tensor:
     return r
 
 
+def _result(x: torch.Tensor, rows: torch.Tensor):
+    """A new tensor like x, and it as rows for the kernels.  An autograd function gives back the first: a view that it
+    made could not be changed in place."""
+    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    return y, y.view(rows.shape)
+
+
 class _LayerNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias, eps):
         rows = _as_rows(x)
-        y = torch.empty(rows.shape, dtype=x.dtype, device=x.device)
+        y, y_rows = _result(x, rows)
         mean, rstd = torch.empty((2, rows.shape[0]), dtype=torch.float32, device=x.device).unbind(0)
-        _rq.rvq_layer_norm(rows, weight, bias, eps, y, mean, rstd)
+        _rq.rvq_layer_norm(rows, weight, bias, eps, y_rows, mean, rstd)
         ctx.save_for_backward(rows, weight, bias, mean, rstd)
         ctx.shape = x.shape
-        return y.view(x.shape)
+        return y
 
     @staticmethod
     @once_differentiable
@@ -78,11 +85,11 @@ class _Dropout(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, residual, mask, step):
         rows, add = _beside(x, residual)
-        y = torch.empty(rows.shape, dtype=x.dtype, device=x.device)
-        _rq.rvq_dropout(rows, mask, y, add)
+        y, y_rows = _result(x, rows)
+        _rq.rvq_dropout(rows, mask, y_rows, add)
         ctx.save_for_backward(step)  # counted up before the backward pass, it would give another mask
         ctx.mask = mask.copy()  # its fields may be another place's by then
-        return y.view(x.shape)
+        return y
 
     @staticmethod
     @once_differentiable
@@ -116,19 +123,20 @@ class _RmsNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, residual, weight, eps, mask, step):
         rows, add = _beside(x, residual)
-        y = torch.empty(rows.shape, dtype=x.dtype, device=x.device)
-        total = None if add is None and mask is None else torch.empty_like(y)
+        y, y_rows = _result(x, rows)
+        total, total_rows = (None, None) if add is None and mask is None else _result(x, rows)
         rstd = torch.empty(rows.shape[0], dtype=torch.float32, device=x.device)
-        _rq.rvq_rms_norm(rows, weight, eps, y, rstd, add, mask, total)
+        _rq.rvq_rms_norm(rows, weight, eps, y_rows, rstd, add, mask, total_rows)
         ctx.save_for_backward(rows if total is None else total, weight, rstd, step)
         ctx.set_materialize_grads(False)
         ctx.shape, ctx.mask = x.shape, None if mask is None else mask.copy()
-        return y.view(x.shape) if total is None else (y.view(x.shape), total.view(x.shape))
+        return y if total is None else (y, total)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dy, dtotal=None):
         total, weight, rstd, _ = ctx.saved_tensors
+        total = total.view(-1, total.shape[-1])  # (a result of the forward pass, or rows)
         need, mask = ctx.needs_input_grad, ctx.mask
         if dy is None and dtotal is None:
             return (None,) * 6
@@ -210,16 +218,18 @@ class _LogProbs(torch.autograd.Function):
             codes = _int32(codes).reshape(-1).contiguous()
 
         def one(*shape, dtype=torch.float32):
-            return torch.empty((n,) + shape, dtype=dtype, device=rows.device)
+            return torch.empty(lead + shape, dtype=dtype, device=rows.device)
 
         log_p, h = None if codes is None else one(), one() if entropy else None
-        lse, stats = one(), one(2)
+        lse = one()
         best = (one(top), one(top, dtype=torch.int32)) if top else (None, None)
-        _rq.rvq_log_probs(rows, codes, temperature, log_p, h, lse, stats, *best)
+        out = log_p, h, lse, *best
+        stats = torch.empty((n, 2), dtype=torch.float32, device=rows.device)
+        flat = [None if t is None else t.view((n,) + t.shape[len(lead):]) for t in out]
+        _rq.rvq_log_probs(rows, codes, temperature, *flat[:3], stats, *flat[3:])
         ctx.save_for_backward(rows, codes, stats, h)
         ctx.set_materialize_grads(False)
         ctx.shape, ctx.temperature = logits.shape, temperature
-        out = tuple(None if t is None else t.view(lead + t.shape[1:]) for t in (log_p, h, lse, *best))
         ctx.mark_non_differentiable(*(t for t in out[3:] if t is not None))
         return out
 
@@ -227,6 +237,7 @@ class _LogProbs(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, grad_log_probs, grad_entropy, grad_lse, *_):
         rows, codes, stats, entropy = ctx.saved_tensors
+        entropy = None if entropy is None else entropy.view(-1)
         grads = [None if g is None else g.to(torch.float32).reshape(-1).contiguous()
                  for g in (grad_log_probs, grad_entropy, grad_lse)]
         dlogits = torch.empty(rows.shape, dtype=rows.dtype, device=rows.device)
@@ -273,12 +284,12 @@ class _Distill(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, top_logits, top_codes, teacher_lse, weights, temperature):
         rows, teacher = _teacher(logits, top_logits, top_codes, teacher_lse, weights)
-        loss = torch.empty(rows.shape[0], dtype=torch.float32, device=rows.device)
+        loss = torch.empty(logits.shape[:-1], dtype=torch.float32, device=rows.device)
         lse = torch.empty((rows.shape[0], 2), dtype=torch.float32, device=rows.device)
-        _rq.rvq_distill(rows, *teacher, temperature, loss, lse=lse)
+        _rq.rvq_distill(rows, *teacher, temperature, loss.view(-1), lse=lse)
         ctx.save_for_backward(rows, *teacher, lse)
         ctx.shape, ctx.temperature = logits.shape, temperature
-        return loss.view(logits.shape[:-1])
+        return loss
 
     @staticmethod
     @once_differentiable

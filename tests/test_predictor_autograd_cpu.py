@@ -134,3 +134,96 @@ def test_dropout_refuses_another_residual_without_elements_too():
         for m in (mask, None):
             with pytest.raises(ValueError):
                 rq.dropout(a, m, b)
+
+
+def log_probs(logits, codes, temperature, log_p=None, entropy=None, lse=None, stats=None, top_log_probs=None,
+              top_codes=None):
+    lp = torch.log_softmax(logits / temperature, 1)
+    if log_p is not None:
+        log_p.copy_(lp.gather(1, codes.long()[:, None])[:, 0])
+    if entropy is not None:
+        entropy.copy_(-(lp.exp() * lp).sum(1))
+    lse.copy_(torch.logsumexp(logits / temperature, 1))
+    if top_codes is not None:
+        best = torch.sort(lp, dim=1, descending=True, stable=True)
+        top_log_probs.copy_(best.values[:, :top_codes.shape[1]])
+        top_codes.copy_(best.indices[:, :top_codes.shape[1]])
+
+
+def log_probs_backward(grad_log_probs, grad_entropy, grad_lse, logits, codes, temperature, stats, entropy, dlogits):
+    lp = torch.log_softmax(logits / temperature, 1)
+    p, g = lp.exp(), torch.zeros_like(lp)
+    if grad_log_probs is not None:
+        g += grad_log_probs[:, None] * (torch.nn.functional.one_hot(codes.long(), lp.shape[1]) - p)
+    if grad_entropy is not None:
+        g -= grad_entropy[:, None] * p * (lp + entropy[:, None])
+    if grad_lse is not None:
+        g += grad_lse[:, None] * p
+    dlogits.copy_(g / temperature)
+
+
+def layer_norm(x, weight, bias, eps, y, mean=None, rstd=None):
+    mean.copy_(x.mean(1))
+    rstd.copy_(1 / torch.sqrt(x.var(1, unbiased=False) + eps))
+    y.copy_((x - mean[:, None].to(x)) * rstd[:, None].to(x))
+
+
+def layer_norm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, workspace):
+    r = rstd[:, None].to(x)
+    h = (x - mean[:, None].to(x)) * r
+    dx.copy_(r * (dy - dy.mean(1, keepdim=True) - h * (dy * h).mean(1, keepdim=True)))
+
+
+def distill(logits, top_logits, top_codes, teacher_lse, weights, temperature, loss, lse=None):
+    loss.copy_(logits.sum(1))
+
+
+def distill_backward(grad, logits, top_logits, top_codes, teacher_lse, weights, temperature, lse, dlogits):
+    dlogits.copy_(grad[:, None].expand_as(logits))
+
+
+@pytest.fixture
+def row_statements(monkeypatch):
+    for name, f in (("rvq_log_probs", log_probs), ("rvq_log_probs_backward", log_probs_backward),
+                    ("rvq_layer_norm", layer_norm), ("rvq_layer_norm_backward", layer_norm_backward),
+                    ("rvq_distill", distill), ("rvq_distill_backward", distill_backward)):
+        monkeypatch.setattr(rq, name, f)
+
+
+RESULTS = {  # call(x, r) and whether each result is one that the backward pass does not read
+    "dropout": (lambda x, r: (rq.dropout(x, rq.rvq_dropout_mask(0.3, 5), r),), [True]),
+    "rms_norm of x": (lambda x, r: (rq.rms_norm(x),), [True]),
+    "rms_norm of a sum": (lambda x, r: rq.rms_norm(x, None, 1e-6, r), [True, False]),
+    "log_probs": (lambda x, r: rq.log_probs(x, (r[..., 0] > 0).long(), entropy=True, top=2)[:4], [True, False, True, True]),
+    "layer_norm": (lambda x, r: (rq.layer_norm(x),), [True]),
+    "distill_loss": (lambda x, r: (rq.distill_loss(x, r[..., :2].detach(), (r[..., :2] > 0).int()),), [True]),
+}
+
+
+@pytest.mark.parametrize("shape", [(6, 8), (2, 3, 8), (8,)])
+@pytest.mark.parametrize("name", RESULTS)
+def test_results_can_be_changed_in_place(name, shape, row_statements):
+    """As those of torch's own operators: scaled by 3, they have 3 times the gradient.  What the backward pass reads (the
+    sum that was normalised, the entropy) is guarded as a saved result of torch's is."""
+    call, free = RESULTS[name]
+    x, r = tensors(2, *shape)
+    x, r = x.float(), r.float()
+    for i, ours in enumerate(free):
+        with torch.no_grad():
+            want = call(x, r)[i].clone()
+            assert torch.equal(call(x, r)[i].mul_(3.0), 3.0 * want)
+        a, b = leaves(x, r)
+        result = call(a, b)[i]
+        if not result.requires_grad:
+            continue
+        result.sum().backward()
+        c, d = leaves(x, r)
+        changed = call(c, d)[i]
+        changed.mul_(3.0)
+        if ours:
+            changed.sum().backward()
+            assert torch.allclose(c.grad, 3.0 * a.grad, rtol=1e-5, atol=1e-6)
+            assert d.grad is None or torch.allclose(d.grad, 3.0 * b.grad, rtol=1e-5, atol=1e-6)
+        else:
+            with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+                changed.sum().backward()
