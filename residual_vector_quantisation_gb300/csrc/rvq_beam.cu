@@ -62,12 +62,12 @@ __device__ __forceinline__ bool beam_live(const BeamArgs &a, int64_t row) {
 
 // A row's pieces and, unless its values are taken raw, the sum of e^z as (m, s),
 // s of this lane alone.
-template <class T, int NV>
+template <class T, int NV, int PARTS>
 __device__ __forceinline__ void beam_pieces(const CutRow<T> &in, int first, int step, int n, bool raw, float add,
                                             WarpRoom &r, float &m, float &s) {
   constexpr int N = 16 / (int)sizeof(T);
   m = -CUDART_INF_F, s = 0.f;
-  warp_pieces<T, NV>(in, first, step, n, add, r, [&](const uint4 (&z)[NV], float edge, float high) {
+  warp_pieces<T, NV, PARTS>(in, first, step, n, add, r, [&](const uint4 (&z)[NV], float edge, float high) {
     if (raw) return;
     const float top = fmaxf(m, warp_max_order(high)), at = top == -CUDART_INF_F ? 0.f : top;
     s *= exp2_fast((m - at) * kLog2e);
@@ -233,10 +233,10 @@ __device__ __forceinline__ void join_group(const BeamArgs &a, int64_t g, const u
 
 // A block per group: `per` warps' shares of each beam's row, then the join.
 // Bound by the chain of one group (score, row, bar, order, join: about 5 us)
-// against the eight or so groups that an SM holds: 54 us for 12000 groups of 4
+// against the eight or so groups that an SM holds: 49 us for 12000 groups of 4
 // rows of 1024 floats, whose bytes alone would take 30; with registers held
 // down for more groups (3 and 4 blocks of 512 threads) it spills and loses.
-template <class T>
+template <class T, int PARTS>
 __global__ void __launch_bounds__(32 * kGroupWarps, 2) k_beam_group(const BeamArgs a) {
   extern __shared__ uint64_t smem[];
   __shared__ Join join;
@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(32 * kGroupWarps, 2) k_beam_group(const BeamAr
     if (!beam_live(a, row)) continue;
     const CutRow<T> in(static_cast<const T *>(a.logits) + row * a.stride, a.dm.vocab);
     float m, s;
-    beam_pieces<T, kLane * (int)sizeof(T) / 16>(in, i % per, per, n, raw, raw ? a.scores[row] : 0.f, room, m, s);
+    beam_pieces<T, kLane * (int)sizeof(T) / 16, PARTS>(in, i % per, per, n, raw, raw ? a.scores[row] : 0.f, room, m, s);
     if (!raw) s = warp_sum(s);
     if (lane == 0) sum[i] = make_float2(m, s);
     for (int j = lane; j < n; j += 32) list[i * n + j] = room.best[j];
@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(32 * kGroupWarps, 2) k_beam_group(const BeamAr
 // 256 rows of 65536 bf16 (34 MB, 5 us of bandwidth) take 21 us here and 6 to 9
 // in the join: a warp reads its 4096 elements at once and then works on them
 // alone.  Half as many vectors a warp and twice the blocks took 25 us.
-template <class T>
+template <class T, int PARTS>
 __global__ void __launch_bounds__(32 * kRowWarps) k_beam_rows(const BeamArgs a) {
   __shared__ WarpRoom room[kRowWarps];
   __shared__ uint64_t all[kRowWarps * kBeamMax];
@@ -281,8 +281,8 @@ __global__ void __launch_bounds__(32 * kRowWarps) k_beam_rows(const BeamArgs a) 
   if (!beam_live(a, row)) return;
   const CutRow<T> in(static_cast<const T *>(a.logits) + row * a.stride, a.dm.vocab);
   float m, s;
-  beam_pieces<T, kRowVectors>(in, split * kRowWarps + warp, a.splits * kRowWarps, n, raw, raw ? a.scores[row] : 0.f,
-                              room[warp], m, s);
+  beam_pieces<T, kRowVectors, PARTS>(in, split * kRowWarps + warp, a.splits * kRowWarps, n, raw,
+                                     raw ? a.scores[row] : 0.f, room[warp], m, s);
   if (!raw) s = warp_sum(s);
   if (lane == 0) sums[warp] = make_float2(m, s);
   if (threadIdx.x == 0) bar = 0, count = 0;
@@ -552,20 +552,25 @@ rvq_status check_outputs(const BeamArgs &a, bool group, const void *workspace, s
 }
 
 std::atomic<bool> g_join_allowed[64];
-template <class T>
+template <class T, int PARTS>
 cudaError_t launch_beam(const BeamArgs &a, const BeamPlan &p, cudaStream_t st) {
   if (p.group) {
     static std::atomic<bool> allowed[64];
-    const cudaError_t e = p.smem > 24 * 1024 ? allow_smem(k_beam_group<T>, allowed) : cudaSuccess;
+    const auto kernel = k_beam_group<T, PARTS>;
+    const cudaError_t e = p.smem > 24 * 1024 ? allow_smem(kernel, allowed) : cudaSuccess;
     if (e != cudaSuccess) return e;
-    k_beam_group<T><<<(unsigned)a.dm.groups, 32 * p.warps, p.smem, st>>>(a);
+    kernel<<<(unsigned)a.dm.groups, 32 * p.warps, p.smem, st>>>(a);
     return cudaGetLastError();
   }
-  k_beam_rows<T><<<(unsigned)(a.dm.groups * a.dm.beams * p.splits), 32 * kRowWarps, 0, st>>>(a);
+  k_beam_rows<T, PARTS><<<(unsigned)(a.dm.groups * a.dm.beams * p.splits), 32 * kRowWarps, 0, st>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess && p.smem > 24 * 1024) e = allow_smem(k_beam_join, g_join_allowed);
   if (e != cudaSuccess) return e;
   return launch_next(k_beam_join, dim3((unsigned)a.dm.groups), 256, p.smem, st, a);
+}
+template <class T>
+cudaError_t launch_beam(const BeamArgs &a, const BeamPlan &p, cudaStream_t st) {
+  return a.dm.select <= 32 ? launch_beam<T, 2>(a, p, st) : launch_beam<T, 4>(a, p, st);
 }
 
 }  // namespace

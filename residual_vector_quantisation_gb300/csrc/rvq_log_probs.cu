@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(32 * kRowWarps, 8) k_log_probs_top(const LogPr
   if (row >= a.dm.rows) return;
   const CutRow<T> r = row_of<T>(a, row);
   Tally t = no_tally();
-  warp_pieces<T, NV>(r, 0, 1, n, 0.f, room[warp], [&](const uint4 (&z)[NV], float edge, float high) {
+  warp_pieces<T, NV, 4>(r, 0, 1, n, 0.f, room[warp], [&](const uint4 (&z)[NV], float edge, float high) {
     // (one piece: nothing to raise)
     t.m = warp_max_order(high);
     Adder<true> sums(t.m, a.c);
@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps) k_log_probs_row_top(const LogP
   if (cs > 1) cluster_arrive();
   const CutRow<T> r = row_of<T>(a, row);
   Tally t = no_tally();
-  warp_pieces<T, NV>(r, rank * warps + warp, cs * warps, n, 0.f, room[warp],
+  warp_pieces<T, NV, 4>(r, rank * warps + warp, cs * warps, n, 0.f, room[warp],
                      [&](const uint4 (&z)[NV], float edge, float high) {
                        const float m = fmaxf(t.m, warp_max_order(high));
                        t = raise(t, m, a.c);

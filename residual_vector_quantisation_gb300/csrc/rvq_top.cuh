@@ -57,8 +57,14 @@ __device__ __forceinline__ uint32_t warp_nth(uint32_t v, int n) {
 // the best n entries in order in r.best (0: none).  `sum(z, edge, high)` is
 // given each piece before its entries are looked for: the vectors (-inf where
 // there are none), the lane's element beside them and the largest of the lane's
-// elements.  `add` is added to every value first.
-template <class T, int NV, class Sum>
+// elements.  `add` is added to every value first.  PARTS: the parts of a lane's
+// elements whose largest values may make the bar, 2, or 4 where more than 32 are
+// kept: two live values more, which cost the beam step's block for a group its
+// last registers (12000 groups of 4 rows of 1024 floats, 4 kept: 51.3 us against
+// 48.8 with two; 2000 of 12 rows of 1025 bf16, 24 kept: 88.7 against 74.7), and
+// which pay where many are kept (500 of 64 rows of 1024 floats, 64 kept: 5.35 ms
+// against 7.06).
+template <class T, int NV, int PARTS, class Sum>
 __device__ __forceinline__ void warp_pieces(const CutRow<T> &in, int first, int step, int n, float add, WarpRoom &r,
                                             Sum sum) {
   constexpr int N = 16 / (int)sizeof(T);
@@ -76,34 +82,42 @@ __device__ __forceinline__ void warp_pieces(const CutRow<T> &in, int first, int 
     }
     const int edge_at = p == 0 ? in.edge(lane) : -1;
     const float edge = edge_at >= 0 ? to_float(in.z[edge_at]) + add : -CUDART_INF_F;
-    // each vector's largest, and the largest of each quarter of the lane's elements (z + add: add is 0 where the sum
-    // is wanted).  Once the sum is taken the vectors are done with: the few that hold an entry worth ordering are
+    // each vector's largest, and the largest of each part of the lane's elements (z + add: add is 0 where the sum is
+    // wanted).  Once the sum is taken the vectors are done with: the few that hold an entry worth ordering are
     // read again, by their lanes at the same time.
-    float most[NV], part[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+    float most[NV], part[PARTS];
+#pragma unroll
+    for (int i = 0; i < PARTS; ++i) part[i] = -CUDART_INF_F;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       most[j] = largest_of<T>(z[j]) + add;
-      part[j * 4 / NV] = fmaxf(part[j * 4 / NV], most[j]);
+      part[j * PARTS / NV] = fmaxf(part[j * PARTS / NV], most[j]);
     }
     part[0] = fmaxf(part[0], edge);
-    const float half[2] = {fmaxf(part[0], part[1]), fmaxf(part[2], part[3])}, high = fmaxf(half[0], half[1]);
+    float half[2];
+    if constexpr (PARTS == 4)
+      half[0] = fmaxf(part[0], part[1]), half[1] = fmaxf(part[2], part[3]);
+    else
+      half[0] = part[0], half[1] = part[1];
+    const float high = fmaxf(half[0], half[1]);
     sum(z, edge, high);
     const uint64_t last = held ? r.best[n - 1] : 0;  // an entry counts if it is above this
     const uint32_t last_value = (uint32_t)(last >> 32);
     if (!__any_sync(0xffffffffu, order_of(high) > 0 && order_of(high) >= last_value)) continue;
     // n entries reach the bar: the n-th of the lanes' largest, or, for more, half as far down among the largest of
     // their halves, or a quarter among those of their quarters.  (The 32nd of 32 is a low one: it let through more
-    // than there is room for, and 6 rows of 65536 f16 with 32 kept took 338 us.)
+    // than there is room for, and 6 rows of 65536 f16 with 32 kept took 338 us against 18.  Two searches cost more than
+    // a low bar up to 18: 2000 groups of 12 rows of 1025 bf16, 17 kept: 56.5 us against 58.5.)
     uint32_t bar;
-    if (n <= 16) {
+    if (n <= 18) {
       bar = warp_nth(order_of(high), n);
-    } else if (n <= 32) {
+    } else if (PARTS == 2 || n <= 32) {
       const int at = (n + 1) / 2;
       bar = min(warp_nth(order_of(half[0]), at), warp_nth(order_of(half[1]), at));
     } else {
       bar = 0xffffffffu;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) bar = min(bar, warp_nth(order_of(part[i]), (n + 3) / 4));
+      for (int i = 0; i < PARTS; ++i) bar = min(bar, warp_nth(order_of(part[i]), (n + PARTS - 1) / PARTS));
     }
     bar = max(bar, last_value);
     const float line = bar ? value_of(bar) : -3.402823466e38f;
