@@ -589,8 +589,10 @@ typedef struct rvq_rms_8bit {
  * total has to be NULL), y, rstd ([rows], kept for the backward pass) and q (the
  * output in 8 bits); one of total, y and q is needed.  The mask is that of the
  * call's rows of `width`.  total and y may each be x or residual (same stride);
- * what is written may lie over nothing else (RVQ_ERR_INVALID_ARG).  (mean(h^2) is
- * a float32: of a row past 1.8e19 it is infinite and y is zero.) */
+ * what is written may lie over nothing else (RVQ_ERR_INVALID_ARG).  (Squares are
+ * added up in float32: of a row whose squares come to more than 3.4e38, such as
+ * 1024 columns of 5.8e17, rstd and y are zero, and squares below 1.2e-38 lose bits,
+ * which counts where eps is as small.) */
 RVQ_API rvq_status rvq_rms_norm(rvq_norm_dims dims, const void *x, int64_t x_stride, const void *residual,
                                 int64_t residual_stride, const rvq_dropout_mask *mask, const void *weight, void *total,
                                 int64_t total_stride, void *y, int64_t y_stride, float *rstd, const rvq_rms_8bit *q,

@@ -40,6 +40,19 @@ def test_the_sum_beside_8_bits(dtype, block, mask):
                 ref.check_8bit(q.view(torch.float8_e4m3fn), s, val["y"], tol["y"], block, False)
 
 
+def test_squares_are_added_up_in_32_bits():
+    """Rows whose squares add up past 3.4e38 have rstd 0 and a result of zero; those just below are normalised."""
+    for width, size in ((100, 1.8e18), (1024, 5.7e17), (5000, 2.6e17), (16384, 1.4e17)):
+        assert width * size ** 2 < 3.4e38 < width * (1.1 * size) ** 2
+        x = torch.full((2, width), size, device=DEV)
+        x[1] *= 1.1
+        y, rstd = torch.empty_like(x), torch.empty(2, device=DEV)
+        rq.rvq_rms_norm(x, None, 1e-6, y, rstd)
+        assert rstd[1].item() == 0.0 and bool((y[1] == 0).all())
+        val, tol = ref.rms(x[:1], None, 1e-6)
+        ref.check(y[:1], val["y"], tol["y"], width)
+
+
 def leaves(*tensors):
     return [t.clone().requires_grad_() for t in tensors]
 
