@@ -644,8 +644,11 @@ typedef struct rvq_log_probs_dims {
  * A row of nothing but -inf has no distribution: its lse and its code's log p are
  * -inf, its entropy is 0.  A logit of +inf or NaN makes the row's numbers NaN (its
  * top_codes are those of its other values, +inf among them).  A row of nothing but
- * the type's lowest value is a uniform distribution.  What is written may not meet
- * anything else (RVQ_ERR_INVALID_ARG). */
+ * the type's lowest value is a uniform distribution.  The sum of the exponentials
+ * holds the largest code's 1 in float32: what all others have together counts down
+ * to 2^-24 or so, and log p, entropy and lse are right to some units of 2^-24 beside
+ * their relative error (the log p of a code that is nearly certain may be 0).  What
+ * is written may not meet anything else (RVQ_ERR_INVALID_ARG). */
 RVQ_API rvq_status rvq_log_probs(rvq_log_probs_dims dims, const void *logits, int64_t logits_stride,
                                  const int32_t *codes, float *log_probs, float *entropy, float *lse, float *stats,
                                  float *top_log_probs, int32_t *top_codes, int64_t *bad_codes, rvq_stream_t stream);

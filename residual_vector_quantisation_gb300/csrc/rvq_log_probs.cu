@@ -6,7 +6,10 @@
 // gives s = sum 2^y and a = sum 2^y y (the running largest value as m: a larger
 // one scales both), and from them
 //   log p[c] = (z_c - m) / T - ln s,   H = ln s - ln 2 * a / s,   lse = m / T + ln s.
-// Both terms of H are positive: nothing cancels.  The gradient needs no sum:
+// Both terms of H are positive: they do not cancel.  (s holds the largest code's
+// own 1: what the others have together below 2^-24 is rounded away in it and in
+// ln s, so that of rows that are nearly certain H keeps its second term alone and
+// is right to 2^-24 absolutely.)  The gradient needs no sum:
 //   dz_j = (2^y_j (k0 + k1 y_j) + [j = c] g) / T.
 #include "rvq_internal.cuh"
 #include "rvq_overlap.h"

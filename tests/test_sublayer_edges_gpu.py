@@ -110,6 +110,29 @@ def test_dropout_without_a_mask(dtype):
         assert torch.equal(rq.dropout(x, None, r), (x.float() + r.float()).to(dtype))
 
 
+@pytest.mark.parametrize("vocab", [40, 1025, 5000, 70000])
+def test_confident_rows(vocab):
+    """One code far above the others.  The sum of the exponentials holds its 1, so that log p, entropy and lse are right
+    to the roundings of numbers near 1, not to their own size: at most STEPS additions on a path, each rounded by U."""
+    others = [2.0 ** -k for k in (8, 14, 20, 23, 24, 25, 26, 30, 40, 60, 100)]       # all of them together
+    d = torch.tensor([math.log(m / (vocab - 1)) for m in others], dtype=F32, device=DEV)
+    z = d[:, None].expand(-1, vocab).contiguous()
+    at = vocab // 3
+    z[:, at] = 0.0
+    codes = torch.full((len(others),), at, dtype=torch.int32, device=DEV)
+    out = rq.log_probs(z, codes, entropy=True)
+    lp = torch.log_softmax(z.double(), 1)
+    entropy = -(lp.exp() * lp).sum(1)
+    assert bool((out.log_probs <= 0).all()) and bool((out.entropy >= 0).all()) and bool((out.lse >= 0).all())
+    off = ref.STEPS * ref.U
+    assert bool(((out.log_probs.double() - lp[:, at]).abs() <= off).all())
+    assert bool(((out.lse.double() - torch.logsumexp(z.double(), 1)).abs() <= off).all())
+    # the second term of the entropy, sum p d, is relative: its terms carry the exponentials' errors (4 roundings of d, and
+    # 2 units of the exponential) and the sum's
+    rel = (ref.STEPS + 8 + 4 * d.abs().double()) * ref.U
+    assert bool(((out.entropy.double() - entropy).abs() <= off + rel * entropy).all())
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("groups,beams,vocab", [(3, 3, 300), (2, 2, 1025), (3, 8, 4096), (1, 2, 70000)])
 def test_beam_step_and_alternatives_around_the_rules_of_the_bar(groups, beams, vocab, dtype):
