@@ -563,11 +563,14 @@ RVQ_API rvq_status rvq_dropout(rvq_dropout_dims dims, const void *x, int64_t x_s
 /* An output in 8 bits (e4m3) beside, or in place of, rvq_rms_norm's y: values
  * [rows] rows of width bytes, `stride` bytes apart; scales [rows][n], contiguous,
  * one for each `block` neighbouring columns (32, 64 or 128; n = ceil(width /
- * block)) or, block 0, one a row.  A value stands for itself times its scale:
+ * block)) or, block 0, one a row.  (Products that take block scales in a tiled
+ * layout need them brought into it.)  A value stands for itself times its scale:
  *   scale = max(largest magnitude of the block's y / 448, 2^-126)
- * (a product with 1 / 448, off by a unit in the last place at most), of scale_type RVQ_SCALE_F32, or, RVQ_SCALE_E8M0, rounded up to a power of two
- * and held as its biased exponent (a byte); value = y / scale, rounded to nearest
- * (y before its own rounding; the division is a product with the inverse).  A
+ * (a product with 1 / 448, off by a unit in the last place at most), of scale_type
+ * RVQ_SCALE_F32, or, RVQ_SCALE_E8M0, rounded up to a power of two and held as its
+ * biased exponent (a byte); value = y / scale, rounded to nearest (y before its own
+ * rounding; the division is a product with the inverse, so that a quotient that is a
+ * tie but for some 2^-23 of it may go either way).  A
  * NaN in a block makes its scale and all its values NaN.  An infinity makes its
  * own value NaN: in float32 the scale is infinite and the block's other values are
  * 0, as a power of two it is NaN and so are they. */

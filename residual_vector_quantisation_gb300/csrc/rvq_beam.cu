@@ -233,8 +233,8 @@ __device__ __forceinline__ void join_group(const BeamArgs &a, int64_t g, const u
 
 // A block per group: `per` warps' shares of each beam's row, then the join.
 // Bound by the chain of one group (score, row, bar, order, join: about 5 us)
-// against the eight or so groups that an SM holds: 49 us for 12000 groups of 4
-// rows of 1024 floats, whose bytes alone would take 30; with registers held
+// against the eight or so groups that an SM holds: 49 us a call in a graph for 12000
+// groups of 4 rows of 1024 floats, whose bytes alone would take 30; with registers held
 // down for more groups (3 and 4 blocks of 512 threads) it spills and loses.
 template <class T, int PARTS>
 __global__ void __launch_bounds__(32 * kGroupWarps, 2) k_beam_group(const BeamArgs a) {

@@ -54,10 +54,11 @@ __global__ void __launch_bounds__(kThreads) k_dropout(const DropoutArgs a) {
   }
 }
 
-// Anything else: a warp takes 256 elements, each lane working out one group of
-// them, so that lanes next to one another read and write next to one another.
-// Bound by instructions: 58 536 x 1025 bf16, rows 1031 apart, 129 us (bytes alone
-// 35).
+// Anything else (rows with gaps of no whole vectors, or without gaps and with
+// elements beside the last whole group): a warp takes 256 elements, each lane
+// working out one group of them, so that lanes next to one another read and write
+// next to one another.  Bound by instructions: 58 536 x 1025 bf16, rows 1031 apart,
+// 127 us (bytes alone 35).
 template <class T>
 __global__ void __launch_bounds__(kThreads) k_dropout_elements(const DropoutArgs a) {
   const Dropped drop(a.mask);

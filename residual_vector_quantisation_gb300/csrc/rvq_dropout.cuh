@@ -62,7 +62,8 @@ struct Dropped {
   // Whether element i of the 8 that `bits` is of is dropped.
   static __device__ __forceinline__ bool at(uint32_t bits, int i) { return bits >> (i / 2 + (i & 1) * 16) & 1; }
   __device__ __forceinline__ bool element(uint64_t e) const { return at(group(e >> 3), (int)(e & 7)); }
-  // In the same form, elements e to e + N - 1 (N 4 or 8).
+  // In the same form, elements e to e + N - 1 (N 4 or 8): one group, or two where they do not start at one (the norm
+  // with dropout, both passes: 60 000 x 1024 bf16 188 us, bytes alone 163; 58 536 x 1025, rows 1031 apart, 283 and 159).
   template <int N>
   __device__ __forceinline__ uint32_t from(uint64_t e) const {
     const int i = (int)(e & 7);

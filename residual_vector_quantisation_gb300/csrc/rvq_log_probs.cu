@@ -290,6 +290,8 @@ __device__ __forceinline__ int join_lists(const uint64_t *list, int stride, int 
 // With the best alternatives: each warp orders its pieces, the block the warps'
 // lists, the cluster's first block the blocks'.  6 rows of 65536 f16 with 32 kept
 // take 18 us over 8 blocks a row: latency of one piece's ordering and two joins.
+// 4096 rows of 65536 bf16 with 16 kept take 387 us (bytes alone: 79), with 64 kept
+// 11.3 ms: of 100 pieces 7 have more entries above the bar than there is room for.
 template <class T, int NV>
 __global__ void __launch_bounds__(32 * kMaxWarps) k_log_probs_row_top(const LogProbsArgs a, const int cs) {
   extern __shared__ uint64_t smem[];

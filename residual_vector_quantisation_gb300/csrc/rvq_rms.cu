@@ -304,7 +304,9 @@ __global__ void __launch_bounds__(rms_threads<T>(), 1) k_rms_ring(const RmsArgs 
 // ---------------------------------------------------------------------------
 
 // A warp's rows (WARP, up to 1024 columns, 4 a block) or a block's.  A warp takes
-// 256 columns at a time, 8 elements a lane in flight.
+// 256 columns at a time, 8 elements a lane in flight.  Latency of one row after the
+// other: 60 000 x 1024 bf16 122 us (bytes alone: 36), 58 536 x 1025, a block of 512
+// threads a row, 549 (35), 5000 x 16384 f32 with a residual 276 (193).
 constexpr int kAnyWidth = 1024, kAnyWarps = 4, kAnyThreads = 512;
 template <class T, bool WARP>
 __global__ void __launch_bounds__(WARP ? 32 * kAnyWarps : kAnyThreads)

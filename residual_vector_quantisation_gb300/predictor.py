@@ -169,7 +169,8 @@ class _RmsNorm(torch.autograd.Function):
 def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
              residual: Optional[torch.Tensor] = None, mask: Optional[_rq.rvq_dropout_mask] = None):
     """Root-mean-square norm over the last axis of x (float32, bfloat16 or float16), or of total = residual + drop(x):
-    y, or (y, total) where a residual or a mask is given, total being the residual of the next sublayer.
+    y, or (y, total) where a residual or a mask is given, total being the residual of the next sublayer (the backward pass
+    reads it: changed in place before, it is an error there).
     Differentiable in x, weight (float32, or x's dtype) and residual (x's shape and dtype), from both results.  mask: as
     in dropout.  Runs on the current stream."""
     if weight is not None and not weight.is_contiguous():
