@@ -141,15 +141,14 @@ class _RmsNorm(torch.autograd.Function):
         if dy is None and dtotal is None:
             return (None,) * 6
         like = dict(dtype=total.dtype, device=total.device)
-        dtotal = None if dtotal is None else _as_rows(dtotal.to(total.dtype))
-        if dy is None:  # the sum's gradient passes the norm by, whatever its rows hold
-            dresidual = dtotal.view(ctx.shape)
-            dx = dresidual
+        if dy is None:  # the sum's gradient passes the norm by, whatever its rows hold, as the tensor that it is
+            dx = dtotal
             if need[0] and mask is not None:
                 dx = torch.empty(ctx.shape, **like)
-                _rq.rvq_dropout(dtotal, mask, dx.view(dtotal.shape))
-            return (dx if need[0] else None, dresidual if need[1] else None,
+                _rq.rvq_dropout(_as_rows(dtotal), mask, dx.view(total.shape))
+            return (dx if need[0] else None, dtotal if need[1] else None,
                     torch.zeros_like(weight) if need[2] else None, None, None, None)
+        dtotal = None if dtotal is None else _as_rows(dtotal.to(total.dtype))
         dy = _as_rows(dy.to(total.dtype))
         dresidual = torch.empty(total.shape, **like) if need[1] or (need[0] and mask is None) else None
         dx = torch.empty(total.shape, **like) if need[0] and mask is not None else None

@@ -227,3 +227,26 @@ def test_results_can_be_changed_in_place(name, shape, row_statements):
         else:
             with pytest.raises(RuntimeError, match="modified by an inplace operation"):
                 changed.sum().backward()
+
+
+@pytest.mark.parametrize("shape", [(6, 8), (2, 3, 8), (8,)])
+@pytest.mark.parametrize("mask", [None, rq.rvq_dropout_mask(0.3, 5)])
+def test_gradients_that_pass_through_have_memory_of_their_own(mask, shape):
+    """What comes from above goes on as it is, as through an addition: no leaf's gradient is another's memory, nor that of
+    the gradient given."""
+    x, r, o, up = tensors(4, *shape)
+    for call in (lambda x, r: rq.rms_norm(x, None, 1e-6, r, mask)[1], lambda x, r: rq.dropout(x, mask, r)):
+        a, b, c = leaves(x, r, o)
+        given = up.clone()
+        for _ in range(2):
+            (call(a, b) + c).backward(given)
+        call(a, b).backward(given)
+        assert torch.equal(given, up)
+        for leaf, times in ((a, drop(up.view(-1, 8), mask).view(shape)), (b, up), (c, up * 2 / 3)):
+            assert torch.allclose(leaf.grad, 3 * times)
+        places = [t.data_ptr() for t in (a.grad, b.grad, c.grad, given)]
+        assert len(set(places)) == 4
+        a.grad = b.grad = c.grad = None
+        call(a, b).backward(given)
+        a.grad.zero_(), b.grad.zero_()
+        assert torch.equal(given, up)
